@@ -287,7 +287,7 @@ def _own(st):
         B.moe_route_scored(s, st["sc"], d["logits"], d["bias"], st["idx"], st["w"])
         out = {"idx": st["idx"], "w": st["w"]}
         if train:
-            B.moe_route_scored_backward(s, st["sc"], d["logits"], st["idx"], st["w"], d["dw"], st["dL"])
+            B.moe_route_scored_backward(s, st["sc"], d["logits"], st["idx"], d["dw"], st["dL"])
             out["d_logits"] = st["dL"]
         return out
     if c["op"] == "router":
