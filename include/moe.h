@@ -213,6 +213,72 @@ moe_status moe_router_backward_f32(const moe_shape* shape, const float* x,
                                    const float* w_router, const float* d_logits,
                                    float* dw_router, float* dx, hipStream_t stream);
 
+/* How moe_route_scored chooses and weighs.  With l the logits of a token over its E
+ * experts and s_e = sigmoid(l_e) (MOE_SCORE_SIGMOID) or the softmax of l over all E
+ * experts (MOE_SCORE_SOFTMAX), the choice value of an expert is c_e = s_e + bias_e.
+ * The experts form n_groups groups of E / n_groups neighbours; a group's score is the
+ * sum of its group_top largest c (1 or 2; of fewer where it has fewer experts in
+ * play), the topk_groups best groups stay, and the k largest c of their experts are
+ * chosen, in descending order; ties go to the lowest group and to the lowest id.
+ * The weight of a chosen expert is scale * s_e, divided by the sum of the chosen s if
+ * renormalise is set: the bias moves the choice alone, as balancing the experts' load
+ * needs, not the output.
+ * Limits: n_groups <= 64 and a divisor of E, 1 <= topk_groups <= n_groups,
+ * k <= topk_groups * E / n_groups, scale finite. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef struct {
+  int32_t score; /* moe_score */
+  int32_t n_groups, topk_groups, group_top;
+  int32_t renormalise; /* 0 or 1 */
+  float scale;
+} moe_scoring;
+
+/* Scored routing.
+ *   logits   fp32 [T, E]   in
+ *   bias     fp32 [E]      in, or NULL (zero)
+ *   topk_idx int32 [T, k]  out
+ *   topk_w   fp32 [T, k]   out
+ * An expert whose logit is -inf or NaN is out of play for that token; slots left over
+ * when fewer than k are in play get expert -1 and weight 0, which moe_plan leaves out
+ * (setting its err_flag).  A NaN in bias or a logit of +inf with softmax scores gives
+ * unspecified (in-range, distinct) experts and weights for its tokens.  Choice values
+ * are compared in double precision; without bias and groups the logits themselves
+ * decide, which is the same order, exactly.  The weights are computed in fp32 from
+ * ratios that neither overflow nor underflow for finite logits. */
+moe_status moe_route_scored(const moe_shape* shape, const moe_scoring* scoring,
+                            const float* logits, const float* bias, int32_t* topk_idx,
+                            float* topk_w, hipStream_t stream);
+
+/* Gradient of the logits of moe_route_scored from the gradient of its weights (the
+ * choice itself has none, nor has the bias).  Without renormalisation softmax scores
+ * give every expert in play a gradient; otherwise it is 0 off the choice.
+ *   logits as in the forward; topk_idx int32 [T, k] as it wrote them (ids outside
+ *   [0, E) are slots without an expert); d_topk_w fp32 [T, k] in;
+ *   d_logits fp32 [T, E] out (overwritten). */
+moe_status moe_route_scored_backward(const moe_shape* shape, const moe_scoring* scoring,
+                                     const float* logits, const int32_t* topk_idx,
+                                     const float* d_topk_w, float* d_logits,
+                                     hipStream_t stream);
+
+/* The router projection of the bf16 and MXFP8 layers: logits [T, E] (fp32) = x [T, H]
+ * (bf16) * w_router [E, H]^T (bf16), products and sums in fp32.
+ * ws [ws_bytes >= moe_router_workspace_bytes(shape, 0)] (may be NULL if that is 0). */
+moe_status moe_router_logits_bf16(const moe_shape* shape, const void* x, const void* w_router,
+                                  float* logits, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Its backward: dw_router [E, H] (bf16, overwritten) = d_logits^T x and
+ * dx [T, H] (bf16) = dx_in + d_logits w_router, summed in fp32 and rounded once;
+ * dx_in bf16 [T, H], or NULL (zero), may be dx itself.  d_logits fp32 [T, E] enters the
+ * products with 16 bits of mantissa (as two bf16 halves); where x or d_logits is not
+ * finite, neither are the gradients it enters (inf or NaN).
+ * ws [ws_bytes >= moe_router_workspace_bytes(shape, 1)]. */
+moe_status moe_router_backward_bf16(const moe_shape* shape, const void* x, const void* w_router,
+                                    const float* d_logits, const void* dx_in, void* dw_router,
+                                    void* dx, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Scratch bytes of the two (T, H, E are used; k and I are not); 0 for shapes they refuse. */
+size_t moe_router_workspace_bytes(const moe_shape* shape, int backward);
+
 /* ------------------------------------------------------------------ plan */
 
 /* Build the schedule table from the routing (sebask.de, § Das Scheduling: the
@@ -406,6 +472,58 @@ moe_status moe_backward_mxfp8(const moe_shape* shape, const void* plan, const vo
                               const void* dy, void* dx, void* dw_gate, void* dw_up, void* dw_down,
                               void* ds_gate, void* ds_up, void* ds_down, float* d_topk_w, void* ws,
                               size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------- low-rank adapters, bf16
+ * Adapters of many requests beside one projection that their tokens share: token t of
+ * adapter a gets
+ *   y[t, :] = base[t, :] + scale[a] * B_a (A_a x[t, :])
+ * where base is the projection's (or the layer's) own output.  A plan groups the tokens
+ * by adapter as moe_plan groups pairs by expert, once per batch for every projection and
+ * layer that the adapters stand beside.
+ *   T tokens, H_in, H_out: multiples of 8; n_adapters in [1, 1024]; rank: a multiple of
+ *   8 in [8, 128] (pad smaller ranks with zero rows of A and zero columns of B);
+ *   T * max(H_in, H_out) * 2 bytes below 4 GiB (MOE_E_UNSUPPORTED otherwise).
+ *   lora_a bf16 [n_adapters, rank, H_in], lora_b bf16 [n_adapters, H_out, rank],
+ *   scale fp32 [n_adapters]. */
+typedef struct {
+  int32_t T, H_in, H_out, n_adapters, rank;
+} moe_lora_shape;
+
+/* The schedule table of the adapters: a moe_plan of T tokens with k = 1 and E =
+ * n_adapters (its layout: moe_plan_layout_of that shape).  adapter_idx int32 [T]: the
+ * adapter of each token; an id outside [0, n_adapters), -1 by convention, is a token
+ * without one (it sets the plan's err_flag, which says no more than that). */
+size_t moe_lora_plan_bytes(const moe_lora_shape* shape);
+moe_status moe_lora_plan(const moe_lora_shape* shape, const int32_t* adapter_idx, void* plan,
+                         hipStream_t stream);
+
+/* Bytes of what the forward keeps for the backward, and of scratch of the forward
+ * (backward = 0) or the backward; 0 for shapes they refuse. */
+size_t moe_lora_saved_bytes(const moe_lora_shape* shape);
+size_t moe_lora_workspace_bytes(const moe_lora_shape* shape, int backward);
+
+/* Forward.  base bf16 [T, H_out], or NULL (zero), may be y itself: rows of tokens
+ * without an adapter are then left as they are, otherwise they get their base.  Both
+ * products are summed in fp32, u = A x is kept to 16 bits of mantissa between them, and
+ * y bf16 [T, H_out] is rounded once.  Where x, A or B is not finite, neither are the
+ * results it enters (inf or NaN); a token without an adapter may hold anything.
+ * saved: NULL where no backward follows. */
+moe_status moe_lora_bf16(const moe_lora_shape* shape, const void* plan, const void* x,
+                         const void* lora_a, const void* lora_b, const float* scale,
+                         const void* base, void* y, void* saved, void* ws, size_t ws_bytes,
+                         hipStream_t stream);
+
+/* Backward, from dy bf16 [T, H_out] and the forward's saved, with u_t = scale A x_t and
+ * v_t = scale B^T dy_t over the tokens of each adapter:
+ *   dx[t, :] = dx_in[t, :] + A^T v_t   (bf16 [T, H_in]; dx_in or NULL, may be dx itself,
+ *                                       as base and y)
+ *   d_lora_a = sum_t v_t (x) x_t, d_lora_b = sum_t dy_t (x) u_t   (bf16, overwritten;
+ *                                       zeros for adapters without tokens) */
+moe_status moe_lora_backward_bf16(const moe_lora_shape* shape, const void* plan, const void* x,
+                                  const void* lora_a, const void* lora_b, const float* scale,
+                                  const void* saved, const void* dy, const void* dx_in, void* dx,
+                                  void* d_lora_a, void* d_lora_b, void* ws, size_t ws_bytes,
+                                  hipStream_t stream);
 
 #ifdef __cplusplus
 }

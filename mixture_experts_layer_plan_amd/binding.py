@@ -46,8 +46,21 @@ class moe_plan_layout(ctypes.Structure):
                                               "max_wtiles")]
 
 
+class moe_scoring(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class moe_lora_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H_in", ctypes.c_int32), ("H_out", ctypes.c_int32),
+                ("n_adapters", ctypes.c_int32), ("rank", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _S = ctypes.POINTER(moe_shape)
+_SC = ctypes.POINTER(moe_scoring)
+_LS = ctypes.POINTER(moe_lora_shape)
 _Z = ctypes.c_size_t
 _I = ctypes.c_int
 
@@ -70,6 +83,17 @@ _SIGS = {
     "moe_route": (_I, [_S, _P, _P, _P, _P]),
     "moe_route_backward": (_I, [_S, _P, _P, _P, _P, _P]),
     "moe_router_backward_f32": (_I, [_S, _P, _P, _P, _P, _P, _P]),
+    "moe_route_scored": (_I, [_S, _SC, _P, _P, _P, _P, _P]),
+    "moe_route_scored_backward": (_I, [_S, _SC, _P, _P, _P, _P, _P]),
+    "moe_router_workspace_bytes": (_Z, [_S, _I]),
+    "moe_router_logits_bf16": (_I, [_S, _P, _P, _P, _P, _Z, _P]),
+    "moe_router_backward_bf16": (_I, [_S] + [_P] * 7 + [_Z, _P]),
+    "moe_lora_plan_bytes": (_Z, [_LS]),
+    "moe_lora_plan": (_I, [_LS, _P, _P, _P]),
+    "moe_lora_saved_bytes": (_Z, [_LS]),
+    "moe_lora_workspace_bytes": (_Z, [_LS, _I]),
+    "moe_lora_bf16": (_I, [_LS] + [_P] * 9 + [_Z, _P]),
+    "moe_lora_backward_bf16": (_I, [_LS] + [_P] * 12 + [_Z, _P]),
     "moe_plan": (_I, [_S, _P, _P, _P]),
     "moe_dispatch_bf16": (_I, [_S, _P, _P, _P, _P]),
     "moe_dispatch_f32": (_I, [_S, _P, _P, _P, _P]),
@@ -343,6 +367,115 @@ def moe_backward_mxfp8(s, plan, x, topk_w, wq, s_gate, s_up, s_down, saved, dy, 
           _bf16(s_down, ns), _ptr(saved), _bf16(dy, nt), _bf16(dx, nt), _bf16(dw_gate, nw),
           _bf16(dw_up, nw), _bf16(dw_down, nw), _bf16(ds_gate, ns), _bf16(ds_up, ns),
           _bf16(ds_down, ns), _f32(d_topk_w, s.T * s.k), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+
+
+# ------------------------------------------- scored routing, bf16 router, adapters
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+
+
+def scoring(score="softmax", n_groups=1, topk_groups=1, group_top=1, renormalise=True,
+            scale=1.0) -> moe_scoring:
+    if score not in SCORES:
+        raise ValueError(f"unsupported score {score!r}")
+    return moe_scoring(SCORES[score], int(n_groups), int(topk_groups), int(group_top),
+                       int(bool(renormalise)), float(scale))
+
+
+def lora_shape(T, H_in, H_out, n_adapters, rank) -> moe_lora_shape:
+    return moe_lora_shape(int(T), int(H_in), int(H_out), int(n_adapters), int(rank))
+
+
+def _here(*tensors):
+    """The launches go to the current device: a tensor of another one is refused."""
+    cur = None
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            cur = torch.cuda.current_device() if cur is None else cur
+            if t.device.index != cur:
+                raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+
+
+def _ws(t):
+    return _ptr(t), 0 if t is None else t.numel() * t.element_size()
+
+
+def _at_least(t, nbytes):
+    """Pointer of a buffer the library lays out itself, which may be larger than asked."""
+    if isinstance(t, torch.Tensor) and t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"buffer of {t.numel() * t.element_size()} bytes, {nbytes} needed")
+    return _ptr(t)
+
+
+def moe_route_scored(s, sc, logits, bias, topk_idx, topk_w, stream=None):
+    _here(logits, bias, topk_idx, topk_w)
+    _call("moe_route_scored", ctypes.byref(s), ctypes.byref(sc), _f32(logits, s.T * s.E),
+          _f32(bias, s.E), _ptr(topk_idx, torch.int32, s.T * s.k), _f32(topk_w, s.T * s.k),
+          _stream(stream))
+
+
+def moe_route_scored_backward(s, sc, logits, topk_idx, d_topk_w, d_logits, stream=None):
+    _here(logits, topk_idx, d_topk_w, d_logits)
+    _call("moe_route_scored_backward", ctypes.byref(s), ctypes.byref(sc),
+          _f32(logits, s.T * s.E), _ptr(topk_idx, torch.int32, s.T * s.k),
+          _f32(d_topk_w, s.T * s.k), _f32(d_logits, s.T * s.E), _stream(stream))
+
+
+def moe_router_workspace_bytes(s: moe_shape, backward: bool) -> int:
+    return lib().moe_router_workspace_bytes(ctypes.byref(s), int(backward))
+
+
+def moe_router_logits_bf16(s, x, w_router, logits, ws, stream=None):
+    _here(x, w_router, logits, ws)
+    _call("moe_router_logits_bf16", ctypes.byref(s), _bf16(x, s.T * s.H),
+          _bf16(w_router, s.E * s.H), _f32(logits, s.T * s.E), *_ws(ws), _stream(stream))
+
+
+def moe_router_backward_bf16(s, x, w_router, d_logits, dx_in, dw_router, dx, ws, stream=None):
+    _here(x, w_router, d_logits, dx_in, dw_router, dx, ws)
+    nt, nw = s.T * s.H, s.E * s.H
+    _call("moe_router_backward_bf16", ctypes.byref(s), _bf16(x, nt), _bf16(w_router, nw),
+          _f32(d_logits, s.T * s.E), _bf16(dx_in, nt), _bf16(dw_router, nw), _bf16(dx, nt),
+          *_ws(ws), _stream(stream))
+
+
+def moe_lora_plan_bytes(s: moe_lora_shape) -> int:
+    return lib().moe_lora_plan_bytes(ctypes.byref(s))
+
+
+def moe_lora_saved_bytes(s: moe_lora_shape) -> int:
+    return lib().moe_lora_saved_bytes(ctypes.byref(s))
+
+
+def moe_lora_workspace_bytes(s: moe_lora_shape, backward: bool) -> int:
+    return lib().moe_lora_workspace_bytes(ctypes.byref(s), int(backward))
+
+
+def moe_lora_plan(s, adapter_idx, plan, stream=None):
+    _here(adapter_idx, plan)
+    _call("moe_lora_plan", ctypes.byref(s), _ptr(adapter_idx, torch.int32, s.T),
+          _at_least(plan, moe_lora_plan_bytes(s)), _stream(stream))
+
+
+def moe_lora_bf16(s, plan, x, lora_a, lora_b, scale, base, y, saved, ws, stream=None):
+    _here(plan, x, lora_a, lora_b, scale, base, y, saved, ws)
+    n, r = s.n_adapters, s.rank
+    _call("moe_lora_bf16", ctypes.byref(s), _at_least(plan, moe_lora_plan_bytes(s)),
+          _bf16(x, s.T * s.H_in), _bf16(lora_a, n * r * s.H_in), _bf16(lora_b, n * r * s.H_out),
+          _f32(scale, n), _bf16(base, s.T * s.H_out), _bf16(y, s.T * s.H_out),
+          _at_least(saved, moe_lora_saved_bytes(s)), *_ws(ws), _stream(stream))
+
+
+def moe_lora_backward_bf16(s, plan, x, lora_a, lora_b, scale, saved, dy, dx_in, dx, d_lora_a,
+                           d_lora_b, ws, stream=None):
+    _here(plan, x, lora_a, lora_b, scale, saved, dy, dx_in, dx, d_lora_a, d_lora_b, ws)
+    n, r = s.n_adapters, s.rank
+    na, nb = n * r * s.H_in, n * r * s.H_out
+    _call("moe_lora_backward_bf16", ctypes.byref(s), _at_least(plan, moe_lora_plan_bytes(s)),
+          _bf16(x, s.T * s.H_in), _bf16(lora_a, na), _bf16(lora_b, nb), _f32(scale, n),
+          _at_least(saved, moe_lora_saved_bytes(s)), _bf16(dy, s.T * s.H_out),
+          _bf16(dx_in, s.T * s.H_in), _bf16(dx, s.T * s.H_in), _bf16(d_lora_a, na),
+          _bf16(d_lora_b, nb), *_ws(ws), _stream(stream))
 
 
 # ------------------------------------------------------------ kernel timing

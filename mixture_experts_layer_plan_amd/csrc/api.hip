@@ -12,6 +12,7 @@
 
 #include "../../include/moe.h"
 #include "internal.hpp"
+#include "skinny.hpp"
 
 using namespace moe;
 
@@ -920,6 +921,144 @@ moe_status scratch_of_current_device(void** out) {
   return MOE_OK;
 }
 
+// ------------------------------------------------------- router projection, adapters
+
+moe_status check_scoring(const moe_shape* s, const moe_scoring* sc) {
+  if (!sc) return MOE_E_NULL;
+  if (sc->score != MOE_SCORE_SOFTMAX && sc->score != MOE_SCORE_SIGMOID) return MOE_E_SHAPE;
+  if (sc->n_groups < 1 || sc->n_groups > 64 || s->E % sc->n_groups) return MOE_E_SHAPE;
+  if (sc->topk_groups < 1 || sc->topk_groups > sc->n_groups) return MOE_E_SHAPE;
+  if (sc->group_top < 1 || sc->group_top > 2) return MOE_E_SHAPE;
+  if (s->k > sc->topk_groups * (s->E / sc->n_groups)) return MOE_E_SHAPE;
+  if (sc->renormalise != 0 && sc->renormalise != 1) return MOE_E_SHAPE;
+  if (!(sc->scale - sc->scale == 0.0f)) return MOE_E_SHAPE;
+  return MOE_OK;
+}
+
+ScoreArgs score_args(const moe_scoring* sc) {
+  return {sc->score, sc->n_groups, sc->topk_groups, sc->group_top, sc->renormalise, sc->scale};
+}
+
+// Rows of one weight-gradient chunk: enough chunks to fill the chip where one group holds
+// every row, long enough that the parts' sum stays small beside the rows themselves.
+constexpr int WGRAD_CHUNK = 1024;
+
+int round8(int v) { return (v + 7) / 8 * 8; }
+
+// router forward: the K parts of the logits; backward: W^T, the halves of d_logits along
+// the tokens, the chunks' parts of dW
+struct RouterWs {
+  size_t parts, wt, ut, wparts, total;
+};
+RouterWs router_ws(const moe_shape* s, bool backward) {
+  Carve c;
+  RouterWs L;
+  memset(&L, 0, sizeof(L));
+  const size_t T = s->T, E = s->E, H = s->H;
+  if (!backward) {
+    const SkinnyPlan p = skinny_plan(s->T, 1, false, s->H, s->E);
+    L.parts = c.take(p.S > 1 ? (size_t)p.S * T * E * sizeof(float) : 0);
+  } else {
+    L.wt = c.take(H * (size_t)round8(s->E) * 2);
+    L.ut = c.take(halves_bytes(T, 1, s->E));
+    L.wparts = c.take(s->T > WGRAD_CHUNK ? (size_t)wgrad_chunk_slots(s->T, 0, WGRAD_CHUNK) * E * H * 4 : 0);
+  }
+  L.total = c.off;
+  return L;
+}
+
+moe_status check_router(const moe_shape* s) {
+  if (!s) return MOE_E_NULL;
+  moe_shape one = *s;
+  one.k = 1;  // k, I and the minibatches are not the router's
+  return check_shape(&one, false);
+}
+
+moe_status check_lora(const moe_lora_shape* s) {
+  if (!s) return MOE_E_NULL;
+  if (s->T < 0 || s->n_adapters < 1 || s->n_adapters > MOE_MAX_E) return MOE_E_SHAPE;
+  if (s->H_in < 8 || s->H_in % 8 || s->H_out < 8 || s->H_out % 8) return MOE_E_SHAPE;
+  if (s->rank < 8 || s->rank > 128 || s->rank % 8) return MOE_E_SHAPE;
+  if ((uint64_t)s->T * (uint64_t)std::max(s->H_in, s->H_out) * 2 >= 1ull << 32)
+    return MOE_E_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_shape lora_plan_shape(const moe_lora_shape* s) {
+  moe_shape p;
+  memset(&p, 0, sizeof(p));
+  p.T = s->T;
+  p.H = p.I = 128;
+  p.E = s->n_adapters;
+  p.k = 1;
+  return p;
+}
+
+// forward: the K parts of u; backward: the K parts of v, A and B transposed, the halves
+// of v along the rows, the chunks' parts of dA and dB
+struct LoraWs {
+  size_t parts, at, bt, vt, pa, pb, total;
+};
+LoraWs lora_ws(const moe_lora_shape* s, bool backward) {
+  Carve c;
+  LoraWs L;
+  memset(&L, 0, sizeof(L));
+  const size_t T = s->T, r = s->rank, n = s->n_adapters, hi = s->H_in, ho = s->H_out;
+  const SkinnyPlan p = skinny_plan(s->T, s->n_adapters, true, backward ? s->H_out : s->H_in, s->rank);
+  L.parts = c.take((size_t)p.S * T * r * sizeof(float));
+  if (backward) {
+    L.at = c.take(n * r * hi * 2);
+    L.bt = c.take(n * r * ho * 2);
+    L.vt = c.take(halves_bytes(T, s->n_adapters, s->rank));
+    const size_t slots = s->T > WGRAD_CHUNK ? wgrad_chunk_slots(s->T, s->n_adapters, WGRAD_CHUNK) : 0;
+    L.pa = c.take(slots * r * hi * 4);
+    L.pb = c.take(slots * r * ho * 4);
+  }
+  L.total = c.off;
+  return L;
+}
+
+// u or v, the first product, and the second with it (see skinny.hpp)
+moe_status lora_pair(const moe_lora_shape* s, const PlanView& v, const void* x, int K,
+                     const void* first, const char* dot_name, const void* second, int nout,
+                     const char* expand_name, const float* scale, const void* base, void* y,
+                     float* parts, void* halves, hipStream_t st) {
+  const SkinnyPlan p = skinny_plan(s->T, s->n_adapters, true, K, s->rank);
+  DotArgs d;
+  d.a = (const bf16_t_host*)x;
+  d.b = (const bf16_t_host*)first;
+  d.out = parts;
+  d.counts = v.counts;
+  d.src_token = v.src_token;
+  d.n = s->n_adapters;
+  d.T = s->T;
+  d.K = K;
+  d.N = s->rank;
+  d.S = p.S;
+  d.R = s->T;
+  MOE_TRY(launch_dot(dot_name, d, p.mb, p.tiles, st));
+  ExpandArgs e;
+  e.u = parts;
+  e.w = (const bf16_t_host*)second;
+  e.base = (const bf16_t_host*)base;
+  e.y = (bf16_t_host*)y;
+  e.scale = scale;
+  e.ut = (bf16_t_host*)halves;
+  e.counts = v.counts;
+  e.src_token = v.src_token;
+  e.pos = v.pos;
+  e.n = s->n_adapters;
+  e.T = s->T;
+  e.K = e.wld = s->rank;
+  e.S = p.S;
+  e.nout = nout;
+  e.max_tiles = p.tiles;
+  e.osplit = expand_osplit(p.tiles, nout);
+  e.R = s->T;
+  MOE_TRY(launch_expand(expand_name, e, p.mb, st));
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1201,6 +1340,189 @@ moe_status moe_backward_f32(const moe_shape* s, const void* plan, const float* x
   return backward_impl(MOE_F32, s, plan, x, topk_w, w_gate, w_up, w_down, s_gate, s_up, s_down,
                        saved, dy, dx, dw_gate, dw_up, dw_down, ds_gate, ds_up, ds_down, d_topk_w,
                        ws, ws_bytes, st);
+}
+
+moe_status moe_route_scored(const moe_shape* s, const moe_scoring* sc, const float* logits,
+                            const float* bias, int32_t* topk_idx, float* topk_w, hipStream_t st) {
+  moe_status rc = check_shape(s, false);
+  if (rc == MOE_OK) rc = check_scoring(s, sc);
+  if (rc != MOE_OK) return rc;
+  if (any_null_rows(s, {logits, topk_idx, topk_w})) return MOE_E_NULL;
+  if (!all_aligned({logits, bias, topk_idx, topk_w})) return MOE_E_ALIGN;
+  return hip_status(launch_route_scored(logits, bias, s->T, s->E, s->k, score_args(sc), topk_idx,
+                                        topk_w, st));
+}
+
+moe_status moe_route_scored_backward(const moe_shape* s, const moe_scoring* sc,
+                                     const float* logits, const int32_t* topk_idx,
+                                     const float* d_topk_w, float* d_logits, hipStream_t st) {
+  moe_status rc = check_shape(s, false);
+  if (rc == MOE_OK) rc = check_scoring(s, sc);
+  if (rc != MOE_OK) return rc;
+  if (any_null_rows(s, {logits, topk_idx, d_topk_w, d_logits})) return MOE_E_NULL;
+  if (!all_aligned({logits, topk_idx, d_topk_w, d_logits})) return MOE_E_ALIGN;
+  return hip_status(launch_route_scored_backward(logits, topk_idx, d_topk_w, s->T, s->E, s->k,
+                                                 score_args(sc), d_logits, st));
+}
+
+size_t moe_router_workspace_bytes(const moe_shape* s, int backward) {
+  return check_router(s) == MOE_OK ? router_ws(s, backward != 0).total : 0;
+}
+
+moe_status moe_router_logits_bf16(const moe_shape* s, const void* x, const void* w_router,
+                                  float* logits, void* ws, size_t ws_bytes, hipStream_t st) {
+  moe_status rc = check_router(s);
+  if (rc != MOE_OK) return rc;
+  const RouterWs W = router_ws(s, false);
+  if (!w_router || any_null_rows(s, {x, logits}) || (W.total && !ws)) return MOE_E_NULL;
+  if (!all_aligned({x, w_router, logits, ws})) return MOE_E_ALIGN;
+  if (ws_bytes < W.total) return MOE_E_WORKSPACE;
+  const SkinnyPlan p = skinny_plan(s->T, 1, false, s->H, s->E);
+  DotArgs d;
+  memset(&d, 0, sizeof(d));
+  d.a = (const bf16_t_host*)x;
+  d.b = (const bf16_t_host*)w_router;
+  d.out = p.S > 1 ? at<float>(ws, W.parts) : logits;
+  d.n = 1;
+  d.T = s->T;
+  d.K = s->H;
+  d.N = s->E;
+  d.S = p.S;
+  d.R = s->T;
+  MOE_TRY(launch_dot("router_logits_bf16", d, p.mb, p.tiles, st));
+  if (p.S > 1)
+    MOE_TRY(launch_sum_parts("router_logits_sum", d.out, p.S, (size_t)s->T * s->E, logits, st));
+  return MOE_OK;
+}
+
+moe_status moe_router_backward_bf16(const moe_shape* s, const void* x, const void* w_router,
+                                    const float* d_logits, const void* dx_in, void* dw_router,
+                                    void* dx, void* ws, size_t ws_bytes, hipStream_t st) {
+  moe_status rc = check_router(s);
+  if (rc != MOE_OK) return rc;
+  if (any_null({w_router, dw_router, ws}) || any_null_rows(s, {x, d_logits, dx})) return MOE_E_NULL;
+  if (!all_aligned({x, w_router, d_logits, dx_in, dw_router, dx, ws})) return MOE_E_ALIGN;
+  const RouterWs W = router_ws(s, true);
+  if (ws_bytes < W.total) return MOE_E_WORKSPACE;
+  TransposeArgs t;
+  t.src = (const bf16_t_host*)w_router;
+  t.dst = at<bf16_t_host>(ws, W.wt);
+  t.R = s->E;
+  t.C = s->H;
+  t.ldd = round8(s->E);
+  if (s->T > 0) MOE_TRY(launch_transpose("router_transpose", 1, t, nullptr, st));
+  ExpandArgs e;
+  memset(&e, 0, sizeof(e));
+  const int mb = s->T >= 32 && s->E <= 256 ? 4 : 1;  // the tokens' d_logits fit 64 KiB of LDS
+  e.u = d_logits;
+  e.w = t.dst;
+  e.base = (const bf16_t_host*)dx_in;
+  e.y = (bf16_t_host*)dx;
+  e.ut = at<bf16_t_host>(ws, W.ut);
+  e.n = 1;
+  e.T = s->T;
+  e.K = s->E;
+  e.S = 1;
+  e.wld = t.ldd;
+  e.nout = s->H;
+  e.max_tiles = skinny_tiles(s->T, 1, false, mb);
+  e.osplit = expand_osplit(e.max_tiles, s->H);
+  e.R = s->T;
+  MOE_TRY(launch_expand("router_dx", e, mb, st));
+  WgradArgs g;
+  memset(&g, 0, sizeof(g));
+  g.side[0] = {e.ut, (const bf16_t_host*)x, (bf16_t_host*)dw_router, at<float>(ws, W.wparts), s->H, 0};
+  g.n = 1;
+  g.T = s->T;
+  g.J = s->E;
+  g.chunk_rows = WGRAD_CHUNK;
+  MOE_TRY(launch_wgrad("router_dw", g, 1, st));
+  return MOE_OK;
+}
+
+size_t moe_lora_plan_bytes(const moe_lora_shape* s) {
+  if (check_lora(s) != MOE_OK) return 0;
+  const moe_shape p = lora_plan_shape(s);
+  return moe_plan_bytes(&p);
+}
+
+moe_status moe_lora_plan(const moe_lora_shape* s, const int32_t* adapter_idx, void* plan,
+                         hipStream_t st) {
+  const moe_status rc = check_lora(s);
+  if (rc != MOE_OK) return rc;
+  const moe_shape p = lora_plan_shape(s);
+  return moe_plan(&p, adapter_idx, plan, st);
+}
+
+size_t moe_lora_saved_bytes(const moe_lora_shape* s) {
+  return check_lora(s) == MOE_OK ? up(halves_bytes(s->T, s->n_adapters, s->rank)) : 0;
+}
+
+size_t moe_lora_workspace_bytes(const moe_lora_shape* s, int backward) {
+  return check_lora(s) == MOE_OK ? lora_ws(s, backward != 0).total : 0;
+}
+
+moe_status moe_lora_bf16(const moe_lora_shape* s, const void* plan, const void* x,
+                         const void* lora_a, const void* lora_b, const float* scale,
+                         const void* base, void* y, void* saved, void* ws, size_t ws_bytes,
+                         hipStream_t st) {
+  const moe_status rc = check_lora(s);
+  if (rc != MOE_OK) return rc;
+  if (any_null({plan, lora_a, lora_b, scale}) || (s->T > 0 && any_null({x, y, ws}))) return MOE_E_NULL;
+  if (!all_aligned({plan, x, lora_a, lora_b, scale, base, y, saved, ws})) return MOE_E_ALIGN;
+  const LoraWs W = lora_ws(s, false);
+  if (ws_bytes < W.total) return MOE_E_WORKSPACE;
+  if (s->T == 0) return MOE_OK;
+  const moe_shape ps = lora_plan_shape(s);
+  return lora_pair(s, view_plan(&ps, plan), x, s->H_in, lora_a, "lora_shrink", lora_b, s->H_out,
+                   "lora_expand", scale, base, y, at<float>(ws, W.parts), saved, st);
+}
+
+moe_status moe_lora_backward_bf16(const moe_lora_shape* s, const void* plan, const void* x,
+                                  const void* lora_a, const void* lora_b, const float* scale,
+                                  const void* saved, const void* dy, const void* dx_in, void* dx,
+                                  void* d_lora_a, void* d_lora_b, void* ws, size_t ws_bytes,
+                                  hipStream_t st) {
+  moe_status rc = check_lora(s);
+  if (rc != MOE_OK) return rc;
+  if (any_null({plan, lora_a, lora_b, scale, d_lora_a, d_lora_b}) ||
+      (s->T > 0 && any_null({x, saved, dy, dx, ws})))
+    return MOE_E_NULL;
+  if (!all_aligned({plan, x, lora_a, lora_b, scale, saved, dy, dx_in, dx, d_lora_a, d_lora_b, ws}))
+    return MOE_E_ALIGN;
+  const LoraWs W = lora_ws(s, true);
+  if (ws_bytes < W.total) return MOE_E_WORKSPACE;
+  const moe_shape ps = lora_plan_shape(s);
+  const PlanView v = view_plan(&ps, plan);
+  bf16_t_host* vt = at<bf16_t_host>(ws, W.vt);
+  if (s->T > 0) {
+    TransposeArgs ta, tb;
+    ta.src = (const bf16_t_host*)lora_a;  // [rank][H_in] -> [H_in][rank]
+    ta.dst = at<bf16_t_host>(ws, W.at);
+    ta.R = ta.ldd = s->rank;
+    ta.C = s->H_in;
+    tb.src = (const bf16_t_host*)lora_b;  // [H_out][rank] -> [rank][H_out]
+    tb.dst = at<bf16_t_host>(ws, W.bt);
+    tb.R = tb.ldd = s->H_out;
+    tb.C = s->rank;
+    MOE_TRY(launch_transpose("lora_transpose", s->n_adapters, ta, &tb, st));
+    rc = lora_pair(s, v, dy, s->H_out, tb.dst, "lora_shrink_dy", ta.dst, s->H_in, "lora_dx", scale,
+                   dx_in, dx, at<float>(ws, W.parts), vt, st);
+    if (rc != MOE_OK) return rc;
+  }
+  WgradArgs g;
+  memset(&g, 0, sizeof(g));
+  g.side[0] = {vt, (const bf16_t_host*)x, (bf16_t_host*)d_lora_a, at<float>(ws, W.pa), s->H_in, 0};
+  g.side[1] = {(const bf16_t_host*)saved, (const bf16_t_host*)dy, (bf16_t_host*)d_lora_b,
+               at<float>(ws, W.pb), s->H_out, 1};
+  g.counts = v.counts;
+  g.src_token = v.src_token;
+  g.n = s->n_adapters;
+  g.T = s->T;
+  g.J = s->rank;
+  g.chunk_rows = WGRAD_CHUNK;
+  MOE_TRY(launch_wgrad("lora_wgrad", g, 2, st));
+  return MOE_OK;
 }
 
 }  // extern "C"

@@ -41,6 +41,17 @@ hipError_t launch_router_logits_f32(const float* x, const float* wr, int T, int 
 hipError_t launch_router_backward_f32(const float* x, const float* wr, const float* dL, int T,
                                       int H, int E, float* dwr, float* dx, hipStream_t s);
 
+// scored routing (score.hip); score: 0 softmax, 1 sigmoid
+struct ScoreArgs {
+  int score, n_groups, topk_groups, group_top, renormalise;
+  float scale;
+};
+hipError_t launch_route_scored(const float* logits, const float* bias, int T, int E, int k,
+                               const ScoreArgs& sc, int32_t* idx, float* w, hipStream_t s);
+hipError_t launch_route_scored_backward(const float* logits, const int32_t* idx, const float* dw,
+                                        int T, int E, int k, const ScoreArgs& sc, float* dL,
+                                        hipStream_t s);
+
 // plan
 struct PlanPtrs {
   int32_t* counts;

@@ -28,3 +28,6 @@ from .moe import (  # noqa: F401
 from .mx import (  # noqa: F401
     e4m3_encode, e4m3_decode, mx_quantize, mx_dequantize, mx_roundtrip,
 )
+from .operators import (  # noqa: F401
+    route_scored, route_scored_backward, router_backward, lora, lora_backward,
+)

@@ -1,0 +1,118 @@
+"""Host-side refusals of scored routing, the bf16 router projection and the low-rank
+adapters (the fake pointers are never dereferenced: every call here is refused)."""
+import ctypes
+
+import pytest
+
+B = pytest.importorskip("mixture_experts_layer_plan_amd.binding")
+
+F, BAD = 0x10000, 0x10004
+OK, NULL, SHAPE, ALIGN, WS, UNSUP = 0, 1, 2, 3, 4, 5
+
+
+@pytest.fixture(scope="module")
+def L():
+    return B.lib()
+
+
+def s_(**kw):
+    d = dict(T=64, H=256, I=128, E=16, k=2)
+    d.update(kw)
+    return B.shape(**d)
+
+
+def route(L, s, sc, logits=F, bias=None, idx=F, w=F):
+    return L.moe_route_scored(ctypes.byref(s), sc if sc is None else ctypes.byref(sc), logits, bias,
+                              idx, w, None)
+
+
+def route_b(L, s, sc, logits=F, idx=F, dw=F, dL=F):
+    return L.moe_route_scored_backward(ctypes.byref(s), ctypes.byref(sc), logits, idx, dw, dL, None)
+
+
+@pytest.mark.parametrize("kw", [dict(n_groups=0), dict(n_groups=3), dict(n_groups=65),
+                                dict(n_groups=4, topk_groups=5), dict(topk_groups=0),
+                                dict(group_top=0), dict(group_top=3), dict(scale=float("nan")),
+                                dict(scale=float("inf")), dict(n_groups=16, topk_groups=1)])
+def test_scoring_that_does_not_fit(L, kw):
+    assert route(L, s_(), B.scoring(**kw)) == SHAPE
+    assert route_b(L, s_(), B.scoring(**kw)) == SHAPE
+
+
+def test_scoring_fields(L):
+    sc = B.scoring()
+    for name, v in (("score", 2), ("score", -1), ("renormalise", 2)):
+        bad = B.scoring()
+        setattr(bad, name, v)
+        assert route(L, s_(), bad) == SHAPE
+    assert route(L, s_(), None) == NULL
+    assert route(L, s_(), sc, logits=None) == NULL
+    assert route(L, s_(), sc, bias=BAD) == ALIGN
+    assert route(L, s_(k=17), sc) == SHAPE
+    assert route_b(L, s_(), sc, dw=None) == NULL
+    assert route_b(L, s_(), sc, dL=BAD) == ALIGN
+    assert route(L, s_(T=0), sc, logits=None, idx=None, w=None) == OK
+    with pytest.raises(ValueError):
+        B.scoring(score="tanh")
+
+
+def test_router_projection(L):
+    s = s_()
+    fwd, bwd = B.moe_router_workspace_bytes(s, False), B.moe_router_workspace_bytes(s, True)
+    assert bwd > 0
+
+    def logits(s, x=F, w=F, out=F, ws=F, n=fwd):
+        return L.moe_router_logits_bf16(ctypes.byref(s), x, w, out, ws, n, None)
+
+    def back(s, x=F, w=F, dL=F, dxi=F, dw=F, dx=F, ws=F, n=bwd):
+        return L.moe_router_backward_bf16(ctypes.byref(s), x, w, dL, dxi, dw, dx, ws, n, None)
+
+    assert logits(s_(H=200)) == SHAPE and back(s_(H=200)) == SHAPE
+    assert logits(s_(E=1025, k=1)) == SHAPE
+    assert logits(s, w=None) == NULL and logits(s, x=None) == NULL
+    assert logits(s, x=BAD) == ALIGN
+    if fwd:
+        assert logits(s, n=fwd - 1) == WS and logits(s, ws=None) == NULL
+    assert back(s, n=bwd - 1) == WS
+    assert back(s, ws=None) == NULL and back(s, dw=None) == NULL and back(s, dL=None) == NULL
+    assert back(s, dxi=BAD) == ALIGN
+    assert B.moe_router_workspace_bytes(s_(H=100), True) == 0
+
+
+def lora(L, s, n, plan=F, x=F, a=F, b=F, sc=F, base=F, y=F, saved=None, ws=F):
+    return L.moe_lora_bf16(ctypes.byref(s), plan, x, a, b, sc, base, y, saved, ws, n, None)
+
+
+def lora_b(L, s, n, plan=F, x=F, a=F, b=F, sc=F, saved=F, dy=F, dxi=F, dx=F, da=F, db=F, ws=F):
+    return L.moe_lora_backward_bf16(ctypes.byref(s), plan, x, a, b, sc, saved, dy, dxi, dx, da, db,
+                                    ws, n, None)
+
+
+@pytest.mark.parametrize("args,code", [((-1, 64, 64, 2, 8), SHAPE), ((4, 0, 64, 2, 8), SHAPE),
+                                       ((4, 60, 64, 2, 8), SHAPE), ((4, 64, 4, 2, 8), SHAPE),
+                                       ((4, 64, 64, 0, 8), SHAPE), ((4, 64, 64, 1025, 8), SHAPE),
+                                       ((4, 64, 64, 2, 4), SHAPE), ((4, 64, 64, 2, 12), SHAPE),
+                                       ((4, 64, 64, 2, 136), SHAPE),
+                                       ((1 << 20, 64, 4096, 2, 8), UNSUP)])
+def test_lora_shapes(L, args, code):
+    s = B.lora_shape(*args)
+    assert lora(L, s, 1 << 40) == code and lora_b(L, s, 1 << 40) == code
+    assert L.moe_lora_plan(ctypes.byref(s), F, F, None) == code
+    assert B.moe_lora_plan_bytes(s) == B.moe_lora_saved_bytes(s) == 0
+    assert B.moe_lora_workspace_bytes(s, True) == 0
+
+
+def test_lora_pointers_and_workspace(L):
+    s = B.lora_shape(70, 64, 128, 3, 16)
+    f, b = B.moe_lora_workspace_bytes(s, False), B.moe_lora_workspace_bytes(s, True)
+    assert f > 0 and b > f and B.moe_lora_saved_bytes(s) >= 70 * 16 * 4
+    for arg in ("plan", "x", "a", "b", "sc", "y", "ws"):
+        assert lora(L, s, f, **{arg: None}) == NULL
+    for arg in ("plan", "x", "a", "b", "sc", "saved", "dy", "dx", "da", "db", "ws"):
+        assert lora_b(L, s, b, **{arg: None}) == NULL
+    for arg in ("x", "base", "y", "saved"):
+        assert lora(L, s, f, **{arg: BAD}) == ALIGN
+    assert lora_b(L, s, b, dxi=BAD) == ALIGN
+    assert lora(L, s, f - 1) == WS and lora_b(L, s, b - 1) == WS
+    assert L.moe_lora_bf16(None, *[F] * 9, f, None) == NULL
+    assert lora(L, B.lora_shape(0, 64, 128, 3, 16), 0, x=None, y=None, ws=None) == OK
