@@ -261,7 +261,8 @@ moe_status moe_route_scored_backward(const moe_shape* shape, const moe_scoring* 
                                      hipStream_t stream);
 
 /* The router projection of the bf16 and MXFP8 layers: logits [T, E] (fp32) = x [T, H]
- * (bf16) * w_router [E, H]^T (bf16), products and sums in fp32.
+ * (bf16) * w_router [E, H]^T (bf16), products and sums in fp32.  T * H * 2 bytes below
+ * 4 GiB, as in the layer calls (MOE_E_UNSUPPORTED otherwise).
  * ws [ws_bytes >= moe_router_workspace_bytes(shape, 0)] (may be NULL if that is 0). */
 moe_status moe_router_logits_bf16(const moe_shape* shape, const void* x, const void* w_router,
                                   float* logits, void* ws, size_t ws_bytes, hipStream_t stream);

@@ -177,8 +177,15 @@ def _bf16(t, numel=None):
     return _ptr(t, _BF16, numel)
 
 
+# The current stream's handle without building a torch.cuda.Stream (0.1 us against 2.7):
+# what a call of a few microseconds on the GPU is measured by.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 

@@ -939,16 +939,11 @@ ScoreArgs score_args(const moe_scoring* sc) {
   return {sc->score, sc->n_groups, sc->topk_groups, sc->group_top, sc->renormalise, sc->scale};
 }
 
-// Rows of one weight-gradient chunk: enough chunks to fill the chip where one group holds
-// every row, long enough that the parts' sum stays small beside the rows themselves.
-constexpr int WGRAD_CHUNK = 1024;
-
-int round8(int v) { return (v + 7) / 8 * 8; }
-
-// router forward: the K parts of the logits; backward: W^T, the halves of d_logits along
-// the tokens, the chunks' parts of dW
+// router forward: the K parts of the logits; backward: the halves of d_logits along the
+// tokens, the chunks' parts of dW
 struct RouterWs {
-  size_t parts, wt, ut, wparts, total;
+  size_t parts, ut, wparts, total;
+  int chunk;
 };
 RouterWs router_ws(const moe_shape* s, bool backward) {
   Carve c;
@@ -959,9 +954,9 @@ RouterWs router_ws(const moe_shape* s, bool backward) {
     const SkinnyPlan p = skinny_plan(s->T, 1, false, s->H, s->E);
     L.parts = c.take(p.S > 1 ? (size_t)p.S * T * E * sizeof(float) : 0);
   } else {
-    L.wt = c.take(H * (size_t)round8(s->E) * 2);
     L.ut = c.take(halves_bytes(T, 1, s->E));
-    L.wparts = c.take(s->T > WGRAD_CHUNK ? (size_t)wgrad_chunk_slots(s->T, 0, WGRAD_CHUNK) * E * H * 4 : 0);
+    L.chunk = wgrad_chunk(s->T, (s->H + 127) / 128, s->E);
+    L.wparts = c.take(s->T > L.chunk ? wgrad_chunk_slots(s->T, 1, false, L.chunk) * E * H * 4 : 0);
   }
   L.total = c.off;
   return L;
@@ -971,7 +966,9 @@ moe_status check_router(const moe_shape* s) {
   if (!s) return MOE_E_NULL;
   moe_shape one = *s;
   one.k = 1;  // k, I and the minibatches are not the router's
-  return check_shape(&one, false);
+  const moe_status rc = check_shape(&one, false);
+  if (rc != MOE_OK) return rc;
+  return (uint64_t)s->T * s->H * 2 < 1ull << 32 ? MOE_OK : MOE_E_UNSUPPORTED;
 }
 
 moe_status check_lora(const moe_lora_shape* s) {
@@ -994,10 +991,11 @@ moe_shape lora_plan_shape(const moe_lora_shape* s) {
   return p;
 }
 
-// forward: the K parts of u; backward: the K parts of v, A and B transposed, the halves
-// of v along the rows, the chunks' parts of dA and dB
+// forward: the K parts of u; backward: the K parts of v, B transposed, the halves of v
+// along the rows, the chunks' parts of dA and dB
 struct LoraWs {
-  size_t parts, at, bt, vt, pa, pb, total;
+  size_t parts, bt, vt, pa, pb, total;
+  int chunk;
 };
 LoraWs lora_ws(const moe_lora_shape* s, bool backward) {
   Carve c;
@@ -1007,10 +1005,10 @@ LoraWs lora_ws(const moe_lora_shape* s, bool backward) {
   const SkinnyPlan p = skinny_plan(s->T, s->n_adapters, true, backward ? s->H_out : s->H_in, s->rank);
   L.parts = c.take((size_t)p.S * T * r * sizeof(float));
   if (backward) {
-    L.at = c.take(n * r * hi * 2);
     L.bt = c.take(n * r * ho * 2);
     L.vt = c.take(halves_bytes(T, s->n_adapters, s->rank));
-    const size_t slots = s->T > WGRAD_CHUNK ? wgrad_chunk_slots(s->T, s->n_adapters, WGRAD_CHUNK) : 0;
+    L.chunk = wgrad_chunk(s->T, (s->H_in + 127) / 128 + (s->H_out + 127) / 128, s->rank);
+    const size_t slots = s->T > L.chunk ? wgrad_chunk_slots(s->T, s->n_adapters, true, L.chunk) : 0;
     L.pa = c.take(slots * r * hi * 4);
     L.pb = c.take(slots * r * ho * 4);
   }
@@ -1020,7 +1018,7 @@ LoraWs lora_ws(const moe_lora_shape* s, bool backward) {
 
 // u or v, the first product, and the second with it (see skinny.hpp)
 moe_status lora_pair(const moe_lora_shape* s, const PlanView& v, const void* x, int K,
-                     const void* first, const char* dot_name, const void* second, int nout,
+                     const void* first, const char* dot_name, const void* second, bool nn, int nout,
                      const char* expand_name, const float* scale, const void* base, void* y,
                      float* parts, void* halves, hipStream_t st) {
   const SkinnyPlan p = skinny_plan(s->T, s->n_adapters, true, K, s->rank);
@@ -1036,7 +1034,7 @@ moe_status lora_pair(const moe_lora_shape* s, const PlanView& v, const void* x, 
   d.N = s->rank;
   d.S = p.S;
   d.R = s->T;
-  MOE_TRY(launch_dot(dot_name, d, p.mb, p.tiles, st));
+  MOE_TRY(launch_dot(dot_name, d, p, st));
   ExpandArgs e;
   e.u = parts;
   e.w = (const bf16_t_host*)second;
@@ -1049,13 +1047,14 @@ moe_status lora_pair(const moe_lora_shape* s, const PlanView& v, const void* x, 
   e.pos = v.pos;
   e.n = s->n_adapters;
   e.T = s->T;
-  e.K = e.wld = s->rank;
+  e.K = s->rank;
   e.S = p.S;
   e.nout = nout;
-  e.max_tiles = p.tiles;
-  e.osplit = expand_osplit(p.tiles, nout);
+  const ExpandPlan c = expand_plan(s->T, s->n_adapters, true, s->rank, nout);
+  e.max_tiles = c.tiles;
+  e.osplit = c.osplit;
   e.R = s->T;
-  MOE_TRY(launch_expand(expand_name, e, p.mb, st));
+  MOE_TRY(launch_expand(expand_name, e, c, nn, st));
   return MOE_OK;
 }
 
@@ -1389,7 +1388,7 @@ moe_status moe_router_logits_bf16(const moe_shape* s, const void* x, const void*
   d.N = s->E;
   d.S = p.S;
   d.R = s->T;
-  MOE_TRY(launch_dot("router_logits_bf16", d, p.mb, p.tiles, st));
+  MOE_TRY(launch_dot("router_logits_bf16", d, p, st));
   if (p.S > 1)
     MOE_TRY(launch_sum_parts("router_logits_sum", d.out, p.S, (size_t)s->T * s->E, logits, st));
   return MOE_OK;
@@ -1404,18 +1403,11 @@ moe_status moe_router_backward_bf16(const moe_shape* s, const void* x, const voi
   if (!all_aligned({x, w_router, d_logits, dx_in, dw_router, dx, ws})) return MOE_E_ALIGN;
   const RouterWs W = router_ws(s, true);
   if (ws_bytes < W.total) return MOE_E_WORKSPACE;
-  TransposeArgs t;
-  t.src = (const bf16_t_host*)w_router;
-  t.dst = at<bf16_t_host>(ws, W.wt);
-  t.R = s->E;
-  t.C = s->H;
-  t.ldd = round8(s->E);
-  if (s->T > 0) MOE_TRY(launch_transpose("router_transpose", 1, t, nullptr, st));
   ExpandArgs e;
   memset(&e, 0, sizeof(e));
-  const int mb = s->T >= 32 && s->E <= 256 ? 4 : 1;  // the tokens' d_logits fit 64 KiB of LDS
+  const ExpandPlan c = expand_plan(s->T, 1, false, s->E, s->H);
   e.u = d_logits;
-  e.w = t.dst;
+  e.w = (const bf16_t_host*)w_router;
   e.base = (const bf16_t_host*)dx_in;
   e.y = (bf16_t_host*)dx;
   e.ut = at<bf16_t_host>(ws, W.ut);
@@ -1423,19 +1415,18 @@ moe_status moe_router_backward_bf16(const moe_shape* s, const void* x, const voi
   e.T = s->T;
   e.K = s->E;
   e.S = 1;
-  e.wld = t.ldd;
   e.nout = s->H;
-  e.max_tiles = skinny_tiles(s->T, 1, false, mb);
-  e.osplit = expand_osplit(e.max_tiles, s->H);
+  e.max_tiles = c.tiles;
+  e.osplit = c.osplit;
   e.R = s->T;
-  MOE_TRY(launch_expand("router_dx", e, mb, st));
+  MOE_TRY(launch_expand("router_dx", e, c, true, st));
   WgradArgs g;
   memset(&g, 0, sizeof(g));
   g.side[0] = {e.ut, (const bf16_t_host*)x, (bf16_t_host*)dw_router, at<float>(ws, W.wparts), s->H, 0};
   g.n = 1;
   g.T = s->T;
   g.J = s->E;
-  g.chunk_rows = WGRAD_CHUNK;
+  g.chunk_rows = W.chunk;
   MOE_TRY(launch_wgrad("router_dw", g, 1, st));
   return MOE_OK;
 }
@@ -1474,8 +1465,8 @@ moe_status moe_lora_bf16(const moe_lora_shape* s, const void* plan, const void* 
   if (ws_bytes < W.total) return MOE_E_WORKSPACE;
   if (s->T == 0) return MOE_OK;
   const moe_shape ps = lora_plan_shape(s);
-  return lora_pair(s, view_plan(&ps, plan), x, s->H_in, lora_a, "lora_shrink", lora_b, s->H_out,
-                   "lora_expand", scale, base, y, at<float>(ws, W.parts), saved, st);
+  return lora_pair(s, view_plan(&ps, plan), x, s->H_in, lora_a, "lora_shrink", lora_b, false,
+                   s->H_out, "lora_expand", scale, base, y, at<float>(ws, W.parts), saved, st);
 }
 
 moe_status moe_lora_backward_bf16(const moe_lora_shape* s, const void* plan, const void* x,
@@ -1496,17 +1487,11 @@ moe_status moe_lora_backward_bf16(const moe_lora_shape* s, const void* plan, con
   const PlanView v = view_plan(&ps, plan);
   bf16_t_host* vt = at<bf16_t_host>(ws, W.vt);
   if (s->T > 0) {
-    TransposeArgs ta, tb;
-    ta.src = (const bf16_t_host*)lora_a;  // [rank][H_in] -> [H_in][rank]
-    ta.dst = at<bf16_t_host>(ws, W.at);
-    ta.R = ta.ldd = s->rank;
-    ta.C = s->H_in;
-    tb.src = (const bf16_t_host*)lora_b;  // [H_out][rank] -> [rank][H_out]
-    tb.dst = at<bf16_t_host>(ws, W.bt);
-    tb.R = tb.ldd = s->H_out;
-    tb.C = s->rank;
-    MOE_TRY(launch_transpose("lora_transpose", s->n_adapters, ta, &tb, st));
-    rc = lora_pair(s, v, dy, s->H_out, tb.dst, "lora_shrink_dy", ta.dst, s->H_in, "lora_dx", scale,
+    // B [H_out][rank] -> [rank][H_out]: K-major for the first product
+    bf16_t_host* bt = at<bf16_t_host>(ws, W.bt);
+    MOE_TRY(launch_transpose("lora_transpose", s->n_adapters, (const bf16_t_host*)lora_b, bt, s->H_out,
+                             s->rank, st));
+    rc = lora_pair(s, v, dy, s->H_out, bt, "lora_shrink_dy", lora_a, true, s->H_in, "lora_dx", scale,
                    dx_in, dx, at<float>(ws, W.parts), vt, st);
     if (rc != MOE_OK) return rc;
   }
@@ -1520,7 +1505,7 @@ moe_status moe_lora_backward_bf16(const moe_lora_shape* s, const void* plan, con
   g.n = s->n_adapters;
   g.T = s->T;
   g.J = s->rank;
-  g.chunk_rows = WGRAD_CHUNK;
+  g.chunk_rows = W.chunk;
   MOE_TRY(launch_wgrad("lora_wgrad", g, 2, st));
   return MOE_OK;
 }

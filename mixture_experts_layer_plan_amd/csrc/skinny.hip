@@ -24,9 +24,6 @@ typedef float f32x4v __attribute__((ext_vector_type(4)));
 MOE_DEV f32x4v mfma16(bf16x8_t a, bf16x8_t b, f32x4v c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-MOE_DEV f32x16_t mfma32(bf16x8_t a, bf16x8_t b, f32x16_t c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
 MOE_DEV bf16x8_t as_frag(const uint4& v) { return __builtin_bit_cast(bf16x8_t, v); }
 
 // Inclusive sum over the lanes of a wavefront.
@@ -45,10 +42,10 @@ MOE_DEV int wave_scan(int v) {
 }
 
 // Where unit `want` lies when group a has units(counts[a]) units, the groups in id order:
-// its group, its index inside the group, and the sums of rows and of 16-row tiles of the
+// its group, its index inside the group, and the sums of rows and of 32-row tiles of the
 // groups before.  Every wavefront finds its own (one pass over the counts).
 struct GroupPos {
-  int a, unit, count, row0, t16;
+  int a, unit, count, row0, t32;
 };
 template <class F>
 MOE_DEV bool find_group(const int32_t* __restrict__ counts, int n, int want, const F& units,
@@ -58,7 +55,7 @@ MOE_DEV bool find_group(const int32_t* __restrict__ counts, int n, int want, con
   for (int b = 0; b < n; b += 64) {
     const int c = b + lane < n ? counts[b + lane] : 0;
     const int u = b + lane < n ? units(c) : 0;
-    const int tt = (c + 15) >> 4;
+    const int tt = (c + 31) >> 5;
     const int us = wave_scan(u), rs = wave_scan(c), ts = wave_scan(tt);
     const unsigned long long m = ballot64(u0 + us > want);
     if (m) {
@@ -67,7 +64,7 @@ MOE_DEV bool find_group(const int32_t* __restrict__ counts, int n, int want, con
       g.count = __builtin_amdgcn_readlane(c, w);
       g.unit = want - u0 - __builtin_amdgcn_readlane(us - u, w);
       g.row0 = r0 + __builtin_amdgcn_readlane(rs - c, w);
-      g.t16 = t0 + __builtin_amdgcn_readlane(ts - tt, w);
+      g.t32 = t0 + __builtin_amdgcn_readlane(ts - tt, w);
       return true;
     }
     u0 += __builtin_amdgcn_readlane(us, 63);
@@ -77,10 +74,10 @@ MOE_DEV bool find_group(const int32_t* __restrict__ counts, int n, int want, con
   return false;
 }
 
-// Row tile `tile` of bm rows: its group, first row (of the plan's row order), valid rows
-// and first 16-row tile.
+// Row tile `tile` of bm rows: its group, first row (of the plan's row order) and valid
+// rows; its first row inside the group, the group's rows and first 32-row tile.
 struct SkinnyTile {
-  int a, row0, rows, t16;
+  int a, row0, rows, off, count, t32;
 };
 template <bool GR>
 MOE_DEV bool skinny_tile(const int32_t* counts, int n, int T, int bm, int tile, SkinnyTile& t) {
@@ -88,124 +85,247 @@ MOE_DEV bool skinny_tile(const int32_t* counts, int n, int T, int bm, int tile, 
     GroupPos g;
     if (!find_group(counts, n, tile, [bm](int c) { return (c + bm - 1) / bm; }, g)) return false;
     t.a = g.a;
-    t.row0 = g.row0 + g.unit * bm;
-    t.rows = min(bm, g.count - g.unit * bm);
-    t.t16 = g.t16 + g.unit * (bm >> 4);
-    return true;
+    t.off = g.unit * bm;
+    t.row0 = g.row0 + t.off;
+    t.count = g.count;
+    t.t32 = g.t32;
+  } else {
+    t.a = 0;
+    t.off = t.row0 = tile * bm;
+    t.count = T;
+    t.t32 = 0;
   }
-  t.a = 0;
-  t.row0 = tile * bm;
-  t.rows = min(bm, T - t.row0);
-  t.t16 = t.row0 >> 4;
+  t.rows = min(bm, t.count - t.off);
   return t.rows > 0;
 }
 
+// Workgroup i runs on XCD i mod 8: give each XCD a contiguous run of the work, so that
+// the column blocks and K parts of a row tile share that XCD's L2.
+MOE_DEV int xcd_order(int id, int total) {
+  const int per = total / N_XCD, rem = total % N_XCD, x = id % N_XCD, local = id / N_XCD;
+  return x < rem ? x * (per + 1) + local : rem * (per + 1) + (x - rem) * per + local;
+}
+
+// 4 neighbouring values of a row of N
+MOE_DEV void put4(float* o, int c, int N, const f32x4v& v) {
+  if ((N & 3) == 0) {
+    if (c < N) *(f32x4v*)(o + c) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < N) o[c + i] = v[i];
+  }
+}
+
 // ------------------------------------------------------------------------- dot
-// A workgroup of NW wavefronts forms 16 MB rows x 16 NB columns over one of S parts of K.
-// The wavefronts take 64-deep K steps in turn, each with the whole tile, and load their
-// fragments straight into registers: a row element is used by one wavefront only, so LDS
-// would add a copy and barriers, and no reuse.  The tiles are joined in LDS, pair by pair.
-template <int MB, int NB, int NW, bool GR>
-__global__ __launch_bounds__(NW * 64) void dot_kernel(DotArgs p) {
+// Few rows (a tile of 16): a workgroup of 8 wavefronts forms 16 rows x 16 NB columns over
+// one of S parts of K.  The wavefronts take 64-deep K blocks in turn and load their
+// fragments straight into registers; the tiles are joined in LDS, pair by pair.  (A
+// fragment's 16 lanes lie in 16 rows, which costs the address unit four times the cycles
+// of 256 neighbouring bytes: of no weight here, where latency counts, see dot_tile_kernel.)
+template <int NB, bool GR>
+__global__ __launch_bounds__(512) void dot_kernel(DotArgs p) {
+  constexpr int NW = 8;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int nblk = (p.N + 16 * NB - 1) / (16 * NB);
-  const int s = blockIdx.x % p.S, rest = blockIdx.x / p.S;
-  const int n0 = (rest % nblk) * 16 * NB;
+  const int id = xcd_order(blockIdx.x, gridDim.x);
+  const int n0 = (id % nblk) * 16 * NB, s = (id / nblk) % p.S;
   SkinnyTile t;
-  if (!skinny_tile<GR>(p.counts, p.n, p.T, 16 * MB, rest / nblk, t)) return;
+  if (!skinny_tile<GR>(p.counts, p.n, p.T, 16, id / (nblk * p.S), t)) return;
   const int K = p.K, kg = 8 * (lane >> 4);
-  const bf16_t* ap[MB];
+  // rows past the tile repeat its last row, columns the last
+  const int r = t.row0 + min(lane & 15, t.rows - 1);
+  const bf16_t* ap = p.a + (size_t)(GR ? p.src_token[r] : r) * K + kg;
   const bf16_t* bp[NB];
-#pragma unroll
-  for (int i = 0; i < MB; ++i) {  // rows past the tile repeat its last row, columns the last
-    const int r = t.row0 + min(16 * i + (lane & 15), t.rows - 1);
-    ap[i] = p.a + (size_t)(GR ? p.src_token[r] : r) * K + kg;
-  }
 #pragma unroll
   for (int i = 0; i < NB; ++i)
     bp[i] = p.b + ((size_t)t.a * p.N + min(n0 + 16 * i + (lane & 15), p.N - 1)) * K + kg;
-  f32x4v acc[MB][NB];
+  f32x4v acc[NB];
 #pragma unroll
-  for (int i = 0; i < MB; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) acc[i][j] = (f32x4v){0.f, 0.f, 0.f, 0.f};
-
-  const int steps = (K + 63) / 64, per = (steps + p.S - 1) / p.S;
-  const int end = min(steps, (s + 1) * per);
-  const auto load = [&](int st, uint4 (&fa)[2][MB], uint4 (&fb)[2][NB]) {
-    const int k0 = st * 64;
+  for (int j = 0; j < NB; ++j) acc[j] = (f32x4v){0.f, 0.f, 0.f, 0.f};
+  const int blocks = (K + 63) / 64, per = (blocks + p.S - 1) / p.S;
+  const int end = min(blocks, (s + 1) * per);
+  const auto load = [&](int b, uint4 (&fa)[2], uint4 (&fb)[2][NB]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int k = k0 + 32 * h;
-      if (k + 32 <= K) {
+      const int k = b * 64 + 32 * h;
+      const bool in = k + kg < K;  // K is a multiple of 8: a lane's 8 values go together
+      fa[h] = in ? *(const uint4*)(ap + k) : zero4();
 #pragma unroll
-        for (int i = 0; i < MB; ++i) fa[h][i] = *(const uint4*)(ap[i] + k);
-#pragma unroll
-        for (int j = 0; j < NB; ++j) fb[h][j] = *(const uint4*)(bp[j] + k);
-      } else {  // K is a multiple of 8: each lane's 8 values are in or out together
-        const bool in = k + kg < K;
-#pragma unroll
-        for (int i = 0; i < MB; ++i) fa[h][i] = in ? *(const uint4*)(ap[i] + k) : zero4();
-#pragma unroll
-        for (int j = 0; j < NB; ++j) fb[h][j] = in ? *(const uint4*)(bp[j] + k) : zero4();
-      }
+      for (int j = 0; j < NB; ++j) fb[h][j] = in ? *(const uint4*)(bp[j] + k) : zero4();
     }
   };
-  const auto mul = [&](const uint4 (&fa)[2][MB], const uint4 (&fb)[2][NB]) {
+  const auto mul = [&](const uint4 (&fa)[2], const uint4 (&fb)[2][NB]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j)  // columns as the M side: a lane gets 4 neighbours
-          acc[i][j] = mfma16(as_frag(fb[h][j]), as_frag(fa[h][i]), acc[i][j]);
+      for (int j = 0; j < NB; ++j)  // columns as the M side: a lane gets 4 neighbours
+        acc[j] = mfma16(as_frag(fb[h][j]), as_frag(fa[h]), acc[j]);
   };
-  uint4 fa0[2][MB], fb0[2][NB], fa1[2][MB], fb1[2][NB];
-  int st = s * per + wv;
-  if (st < end) load(st, fa0, fb0);
-  while (st < end) {
-    if (st + NW < end) load(st + NW, fa1, fb1);
+  uint4 fa0[2], fb0[2][NB], fa1[2], fb1[2][NB];
+  int b = s * per + wv;
+  if (b < end) load(b, fa0, fb0);
+  for (; b < end; b += 2 * NW) {
+    if (b + NW < end) load(b + NW, fa1, fb1);
     mul(fa0, fb0);
-    st += NW;
-    if (st >= end) break;
-    if (st + NW < end) load(st + NW, fa0, fb0);
+    if (b + NW >= end) break;
+    if (b + 2 * NW < end) load(b + 2 * NW, fa0, fb0);
     mul(fa1, fb1);
-    st += NW;
   }
-
-  __shared__ f32x4v part[NW / 2][MB * NB][64];
+  __shared__ f32x4v part[NW / 2][NB][64];
 #pragma unroll
   for (int h = NW / 2; h >= 1; h /= 2) {
     if (wv >= h && wv < 2 * h)
 #pragma unroll
-      for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j) part[wv - h][i * NB + j][lane] = acc[i][j];
+      for (int j = 0; j < NB; ++j) part[wv - h][j][lane] = acc[j];
     __syncthreads();
     if (wv < h)
 #pragma unroll
-      for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] += part[wv][i * NB + j][lane];
+      for (int j = 0; j < NB; ++j) acc[j] += part[wv][j][lane];
     __syncthreads();
   }
-  if (wv) return;
+  const int m = lane & 15;
+  if (wv || m >= t.rows) return;
+  float* o = p.out + ((size_t)s * p.R + t.row0 + m) * p.N;
 #pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int m = 16 * i + (lane & 15);
-    if (m >= t.rows) continue;
-    float* o = p.out + ((size_t)s * p.R + t.row0 + m) * p.N;
+  for (int j = 0; j < NB; ++j) put4(o, n0 + 16 * j + 4 * (lane >> 4), p.N, acc[j]);
+}
+
+// Many rows: a workgroup of 4 wavefronts forms 64 rows x BN columns over one of S parts of
+// K.  Both operands reach LDS by direct loads of 128-byte row pieces, 8 lanes each, into a
+// ring of NS 64-deep stages; the product of a stage runs while NS - 2 more are in flight.
+// Fragments loaded from memory without LDS took 121 us for the 8192 x 256 x 7168 router
+// product: 16 lanes in 16 rows keep the address unit busy for 64 cycles a KiB.
+// Row r's 16-byte chunk c lies at r * 128 + 16 (c ^ (r & 7)): the 16 rows of a fragment
+// read hit all 64 banks.
+constexpr int DT_NS = 4;
+template <int BN>
+struct DotTile {
+  static constexpr int WN = BN >= 64 ? 2 : 1, WM = 4 / WN;  // wavefronts along rows, columns
+  static constexpr int MB = 64 / 16 / WM, NB = BN / 16 / WN;
+  static constexpr int STAGE = (64 + BN) * 128, LOADS = (64 + BN) / 32;  // per wavefront
+};
+
+// NR fragments (16 x 32) from LDS, waited for in the same block: the compiler would wait
+// for every direct load in flight before a read of its own.
+MOE_DEV uint32_t lds_at(const char* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
+}
+MOE_DEV void lds_read3(const uint32_t (&a)[3], s16x8_t (&f)[3]) {
+  asm volatile(
+      "ds_read_b128 %0, %3\n\tds_read_b128 %1, %4\n\tds_read_b128 %2, %5\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2])
+      : "v"(a[0]), "v"(a[1]), "v"(a[2])
+      : "memory");
+}
+MOE_DEV void lds_read4(const uint32_t (&a)[4], s16x8_t (&f)[4]) {
+  asm volatile(
+      "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\t"
+      "ds_read_b128 %3, %7\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3])
+      : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3])
+      : "memory");
+}
+MOE_DEV void lds_read6(const uint32_t (&a)[6], s16x8_t (&f)[6]) {
+  asm volatile(
+      "ds_read_b128 %0, %6\n\tds_read_b128 %1, %7\n\tds_read_b128 %2, %8\n\t"
+      "ds_read_b128 %3, %9\n\tds_read_b128 %4, %10\n\tds_read_b128 %5, %11\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3]), "=&v"(f[4]), "=&v"(f[5])
+      : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "v"(a[4]), "v"(a[5])
+      : "memory");
+}
+
+template <int BN, bool GR>
+__global__ __launch_bounds__(256) void dot_tile_kernel(DotArgs p) {
+  using C = DotTile<BN>;
+  constexpr int NR = C::MB + C::NB;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int nblk = (p.N + BN - 1) / BN;
+  const int id = xcd_order(blockIdx.x, gridDim.x);
+  const int n0 = (id % nblk) * BN, s = (id / nblk) % p.S;
+  SkinnyTile t;
+  if (!skinny_tile<GR>(p.counts, p.n, p.T, 64, id / (nblk * p.S), t)) return;
+  const uint32_t K2 = (uint32_t)p.K * 2;
+  const rsrc_t ra = make_rsrc(p.a, (uint32_t)p.T * K2);  // below 4 GiB, checked on the host
+  const rsrc_t rb = make_rsrc(p.b + (size_t)t.a * p.N * p.K, (uint32_t)p.N * K2);
+  // load q of a wavefront brings rows 8 (4 q + wv) .. + 7 of the stage (the 64 rows of a,
+  // then the BN of b): lane L row L / 8, chunk (L % 8) ^ (L / 8); past the range: zeros
+  constexpr uint32_t OUT = 0xffffffffu;
+  const int r8 = lane >> 3, c8 = (lane & 7) ^ r8;
+  uint32_t off[C::LOADS];
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int c = n0 + 16 * j + 4 * (lane >> 4);
-      if ((p.N & 3) == 0) {
-        if (c < p.N) *(f32x4v*)(o + c) = acc[i][j];
-      } else {
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          if (c + v < p.N) o[c + v] = acc[i][j][v];
-      }
+  for (int q = 0; q < C::LOADS; ++q) {
+    const int r = 8 * (4 * q + wv) + r8;
+    if (q < 2) {
+      const int row = t.row0 + r;
+      off[q] = r < t.rows ? (uint32_t)(GR ? p.src_token[row] : row) * K2 + c8 * 16 : OUT;
+    } else {
+      const int n = n0 + r - 64;
+      off[q] = n < p.N ? (uint32_t)n * K2 + c8 * 16 : OUT;
     }
+  }
+  const int blocks = (p.K + 63) / 64, per = (blocks + p.S - 1) / p.S;
+  const int b0 = s * per, nk = min(blocks, b0 + per) - b0;
+  const auto issue = [&](int i) {
+    char* st = lds + (i % DT_NS) * C::STAGE;
+    const uint32_t k2 = (uint32_t)(b0 + i) * 128;
+    const bool in = k2 + c8 * 16 < K2;  // the last stage of a K that is no multiple of 64
+#pragma unroll
+    for (int q = 0; q < C::LOADS; ++q)
+      dma16_buf(q < 2 ? ra : rb, in && off[q] != OUT ? off[q] + k2 : OUT, 0u,
+                st + (4 * q + wv) * 1024);
+  };
+  f32x4v acc[C::MB][C::NB];
+#pragma unroll
+  for (int i = 0; i < C::MB; ++i)
+#pragma unroll
+    for (int j = 0; j < C::NB; ++j) acc[i][j] = (f32x4v){0.f, 0.f, 0.f, 0.f};
+  const int wm = wv / C::WN, wn = wv % C::WN, g = lane >> 4, rho = lane & 15;
+  for (int i = 0; i < DT_NS - 1 && i < nk; ++i) issue(i);
+  for (int i = 0; i < nk; ++i) {
+    // stage i is in (each later one has LOADS instructions), stage i - 1 no longer read
+    const int ahead = min(DT_NS - 2, nk - 1 - i);
+    constexpr int L = C::LOADS;
+    if (ahead >= 2) __builtin_amdgcn_s_waitcnt((2 * L) | 0x70);
+    else if (ahead == 1) __builtin_amdgcn_s_waitcnt(L | 0x70);
+    else __builtin_amdgcn_s_waitcnt(0x70);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (i + DT_NS - 1 < nk) issue(i + DT_NS - 1);
+    const char* st = lds + (i % DT_NS) * C::STAGE;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t ad[NR];
+      s16x8_t f[NR];
+      const int cx = ((4 * h + g) ^ (rho & 7)) << 4;
+#pragma unroll
+      for (int m = 0; m < C::MB; ++m)
+        ad[m] = lds_at(st + (16 * (C::MB * wm + m) + rho) * 128 + cx);
+#pragma unroll
+      for (int n = 0; n < C::NB; ++n)
+        ad[C::MB + n] = lds_at(st + (64 + 16 * (C::NB * wn + n) + rho) * 128 + cx);
+      if constexpr (NR == 3) lds_read3(ad, f);
+      else if constexpr (NR == 4) lds_read4(ad, f);
+      else lds_read6(ad, f);
+#pragma unroll
+      for (int m = 0; m < C::MB; ++m)
+#pragma unroll
+        for (int n = 0; n < C::NB; ++n)
+          acc[m][n] = mfma16(__builtin_bit_cast(bf16x8_t, f[C::MB + n]),
+                             __builtin_bit_cast(bf16x8_t, f[m]), acc[m][n]);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < C::MB; ++m) {
+    const int r = 16 * (C::MB * wm + m) + rho;
+    if (r >= t.rows) continue;
+    float* o = p.out + ((size_t)s * p.R + t.row0 + r) * p.N;
+#pragma unroll
+    for (int n = 0; n < C::NB; ++n)
+      put4(o, n0 + 16 * (C::NB * wn + n) + 4 * g, p.N, acc[m][n]);
   }
 }
 
@@ -215,309 +335,652 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict_
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   float v = 0.0f;
+#pragma unroll 4
   for (int s = 0; s < S; ++s) v += parts[(size_t)s * n + i];
   out[i] = v;
+}
+
+// The dot of a few tokens (at most TB): a workgroup per column, its row of b read once
+// and multiplied with every token's, without matrix instructions (which would leave
+// 16 - T of 16 rows idle and need a second launch to join the parts of K).
+template <int TB>
+__global__ __launch_bounds__(256) void dot_few_kernel(DotArgs p) {
+  __shared__ float part[4][TB];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const bf16_t* b = p.b + (size_t)blockIdx.x * p.K;
+  float acc[TB];
+#pragma unroll
+  for (int t = 0; t < TB; ++t) acc[t] = 0.0f;
+#pragma unroll 2
+  for (int k = threadIdx.x * 8; k < p.K; k += 2048) {
+    float fb[8];
+    unpack8(*(const uint4*)(b + k), fb);
+    uint4 xa[TB];
+#pragma unroll
+    for (int t = 0; t < TB; ++t)  // tokens past the last repeat it
+      xa[t] = *(const uint4*)(p.a + (size_t)min(t, p.T - 1) * p.K + k);
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      float fx[8];
+      unpack8(xa[t], fx);
+#pragma unroll
+      for (int v = 0; v < 8; ++v) acc[t] = fmaf(fx[v], fb[v], acc[t]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TB; ++t) {
+    const float v = wave_sum_f32(acc[t]);
+    if (lane == 0) part[wv][t] = v;
+  }
+  __syncthreads();
+  const int t = threadIdx.x;
+  if (t < TB && t < p.T)
+    p.out[(size_t)t * p.N + blockIdx.x] = (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]);
 }
 
 // ---------------------------------------------------------------------- expand
 // byte offset of 16-byte chunk c of row m in the LDS copy of u (kp values a row)
 MOE_DEV int u_chunk(int m, int c, int kp) { return m * kp * 2 + ((c ^ (m & 3)) << 4); }
 
-// A workgroup takes 16 MB rows and one of `osplit` parts of the output columns; each
-// wavefront 32 columns at a time.  The rows' u (summed over its S parts, scaled, split)
-// lies in LDS, in registers where KS (K steps of 32) is known; the weights come straight
-// from memory in the order of the fragments.  As the M side of the product, weight row i
-// of block b stands for column 8 (i / 4) + 4 b + i % 4, so that a lane ends with 8
-// neighbouring outputs: base and y move 16 bytes at a time, 64 bytes of a row per lane
-// group, without another trip through LDS.
-template <int MB, int KS, bool GR>
-__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs p) {
+// 8 rows of 8 bf16 (one uint4 each) -> the 8 columns, 8 values each: every output word
+// takes one half of two input words.
+MOE_DEV void transpose8(const uint4 (&r)[8], uint4 (&c)[8]) {
+#pragma unroll
+  for (int h = 0; h < 8; ++h) {
+    const uint32_t sel = h & 1 ? 0x07060302u : 0x05040100u;
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      w[q] = __builtin_amdgcn_perm(u4_word(r[2 * q + 1], h >> 1), u4_word(r[2 * q], h >> 1), sel);
+    c[h] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// The halves of u along the rows, in the order of wgrad's fragments (K = 32 rows):
+// [32-row tile][16 values of j][hi, lo][lane: j = lane % 16, rows 8 (lane / 16) .. + 7][8].
+// Rows past the group's last, up to its last tile's end, are zero.
+template <int MB>
+MOE_DEV void store_halves(const char* lds, int lo_off, int kp, int K, const SkinnyTile& t,
+                          bf16_t* __restrict__ ut) {
+  const int jb = (K + 15) / 16, js = 16 * jb;
+  const bool pad = t.off + 16 * MB >= t.count;  // the last tile: zeros up to a multiple of 32
+  const int groups = pad ? (((t.off + t.rows + 31) >> 5 << 5) - t.off) / 8 : 2 * MB;
+  for (int i = threadIdx.x; i < groups * js; i += 256) {
+    const int q = i / js, j = i - q * js, g8 = (t.off >> 3) + q;
+    uint32_t w[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        uint32_t v0 = 0, v1 = 0;
+        if (q < 2 * MB) {
+          const char* b = lds + h * lo_off + (j & 7) * 2;
+          v0 = *(const uint16_t*)(b + u_chunk(8 * q + 2 * r, j >> 3, kp));
+          v1 = *(const uint16_t*)(b + u_chunk(8 * q + 2 * r + 1, j >> 3, kp));
+        }
+        w[h][r] = v0 | (v1 << 16);
+      }
+    bf16_t* d = ut + (((size_t)(t.t32 + (g8 >> 2)) * jb + (j >> 4)) * 2) * 512 +
+                ((g8 & 3) * 16 + (j & 15)) * 8;
+    *(uint4*)d = make_uint4(w[0][0], w[0][1], w[0][2], w[0][3]);
+    *(uint4*)(d + 512) = make_uint4(w[1][0], w[1][1], w[1][2], w[1][3]);
+  }
+}
+
+// u of a row tile into LDS: its S parts summed, scaled and split, zeros past K and past
+// the tile's rows; kp = K rounded up to 32.
+template <int ROWS>
+MOE_DEV void fill_u(const ExpandArgs& p, const SkinnyTile& t, int kp, char* lds) {
+  const float sc = p.scale ? p.scale[t.a] : 1.0f;
+  const int ch = kp / 8, lo_off = ROWS * kp * 2;
+  for (int i = threadIdx.x; i < ROWS * ch; i += 256) {
+    const int m = i / ch, cc = i - m * ch;
+    float f[8];
+#pragma unroll
+    for (int v = 0; v < 8; ++v) f[v] = 0.0f;
+    if (m < t.rows) {
+      const float* u = p.u + ((size_t)t.row0 + m) * p.K;
+      const size_t part = p.R * p.K;
+      if ((p.K & 7) == 0) {
+        if (8 * cc < p.K) {
+#pragma unroll 4
+          for (int s = 0; s < p.S; ++s) {
+            const float4 a = *(const float4*)(u + s * part + 8 * cc);
+            const float4 b = *(const float4*)(u + s * part + 8 * cc + 4);
+            f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
+            f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
+          }
+        }
+      } else {
+        for (int s = 0; s < p.S; ++s)
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            if (8 * cc + v < p.K) f[v] += u[s * part + 8 * cc + v];
+      }
+    }
+    float lo[8];
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      f[v] *= sc;
+      const float hi = bf16_to_f32(f32_to_bf16(f[v]));
+      lo[v] = fabsf(hi) < INFINITY ? f[v] - hi : 0.0f;
+    }
+    *(uint4*)(lds + u_chunk(m, cc, kp)) = pack8(f);
+    *(uint4*)(lds + lo_off + u_chunk(m, cc, kp)) = pack8(lo);
+  }
+}
+
+// Rows without a group: the base alone, 16 tokens per workgroup.
+MOE_DEV void copy_ungrouped(const ExpandArgs& p, int b) {
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  for (int i = wv; i < 16; i += 4) {
+    const int tok = b * 16 + i;
+    if (tok >= p.T || p.pos[tok] >= 0) continue;
+    const size_t o = (size_t)tok * p.nout;
+    for (int c = lane * 8; c < p.nout; c += 512)
+      *(uint4*)(p.y + o + c) = p.base ? *(const uint4*)(p.base + o + c) : zero4();
+  }
+}
+
+// In both forms below u's rows are the M side of the product and fragment f's column i
+// stands for output column 8 i + f of a 128-column block: a lane ends with 8 neighbouring
+// outputs of 4 rows, and 16 lanes with 256 bytes of one row, so that base and y move in
+// whole lines without a trip through LDS.  (With the weights as the M side a store's 16
+// lanes lie in 16 rows: 92 us against 53 us for 8192 rows of 7168 at rank 64.)
+
+// Few rows (16 MB a tile): each wavefront takes 128-column blocks of one of `osplit` parts
+// of the columns; the weights come straight from memory, one K step of 32 ahead.
+template <int MB, bool NN, bool GR>
+__global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs p) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int tile = blockIdx.x / p.osplit, oz = blockIdx.x % p.osplit;
-  if (GR && tile >= p.max_tiles) {
-    // rows without a group: the base alone, 16 tokens per workgroup
-    const int b = blockIdx.x - p.max_tiles * p.osplit;
-    for (int i = wv; i < 16; i += 4) {
-      const int tok = b * 16 + i;
-      if (tok >= p.T || p.pos[tok] >= 0) continue;
-      const size_t o = (size_t)tok * p.nout;
-      for (int c = lane * 8; c < p.nout; c += 512)
-        *(uint4*)(p.y + o + c) = p.base ? *(const uint4*)(p.base + o + c) : zero4();
-    }
+  if (GR && (int)blockIdx.x >= p.max_tiles * p.osplit) {
+    copy_ungrouped(p, blockIdx.x - p.max_tiles * p.osplit);
     return;
   }
+  const int tile = blockIdx.x / p.osplit, oz = blockIdx.x % p.osplit;
   SkinnyTile t;
   if (!skinny_tile<GR>(p.counts, p.n, p.T, 16 * MB, tile, t)) return;
-  const int ksteps = KS ? KS : (p.K + 31) / 32, kp = 32 * ksteps;
-  const int lo_off = 16 * MB * kp * 2;
-  {
-    const float sc = p.scale ? p.scale[t.a] : 1.0f;
-    const int ch = kp / 8;
-    for (int i = threadIdx.x; i < 16 * MB * ch; i += 256) {
-      const int m = i / ch, c = i % ch;
-      float f[8];
+  const int ksteps = (p.K + 31) / 32, kp = 32 * ksteps, lo_off = 16 * MB * kp * 2;
+  const int g = lane >> 4, rho = lane & 15;
+  size_t rowo[MB][4];
 #pragma unroll
-      for (int v = 0; v < 8; ++v) f[v] = 0.0f;
-      if (m < t.rows) {
-        for (int s = 0; s < p.S; ++s) {
-          const float* u = p.u + ((size_t)s * p.R + t.row0 + m) * p.K;
-          if ((p.K & 3) == 0) {
+  for (int m = 0; m < MB; ++m)
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-              if (8 * c + 4 * q < p.K) {
-                const float4 v = *(const float4*)(u + 8 * c + 4 * q);
-                f[4 * q] += v.x; f[4 * q + 1] += v.y; f[4 * q + 2] += v.z; f[4 * q + 3] += v.w;
-              }
-          } else {
-#pragma unroll
-            for (int v = 0; v < 8; ++v)
-              if (8 * c + v < p.K) f[v] += u[8 * c + v];
-          }
-        }
-      }
-      float lo[8];
-#pragma unroll
-      for (int v = 0; v < 8; ++v) {
-        f[v] *= sc;
-        const float hi = bf16_to_f32(f32_to_bf16(f[v]));
-        lo[v] = fabsf(hi) < INFINITY ? f[v] - hi : 0.0f;  // inf stays inf, not NaN
-      }
-      *(uint4*)(lds + u_chunk(m, c, kp)) = pack8(f);
-      *(uint4*)(lds + lo_off + u_chunk(m, c, kp)) = pack8(lo);
+    for (int i = 0; i < 4; ++i) {
+      const int r = t.row0 + min(16 * m + 4 * g + i, t.rows - 1);
+      rowo[m][i] = (size_t)(GR ? p.src_token[r] : r) * p.nout + 8 * rho;
     }
-  }
-  __syncthreads();
-  if (p.ut && oz == 0) {
-    // the halves along the rows, for the weight gradients: [16-row tile][j][16 hi, 16 lo]
-    const int nt = (t.rows + 15) / 16;
-    for (int i = threadIdx.x; i < nt * p.K; i += 256) {
-      const int q = i / p.K, j = i % p.K;
-      uint32_t w[16];
+  const bf16_t* W = p.w + (size_t)t.a * p.nout * p.K;
+  const int blocks = (p.nout + 127) / 128, bper = (blocks + p.osplit - 1) / p.osplit;
+  const int c1 = min(blocks, (oz + 1) * bper);
+  const auto load_base = [&](int c, uint4 (&bs)[MB][4]) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+    for (int m = 0; m < MB; ++m)
 #pragma unroll
-        for (int r = 0; r < 16; r += 2) {
-          const char* b = lds + h * lo_off + (j & 7) * 2;
-          const uint32_t v0 = *(const uint16_t*)(b + u_chunk(16 * q + r, j >> 3, kp));
-          const uint32_t v1 = *(const uint16_t*)(b + u_chunk(16 * q + r + 1, j >> 3, kp));
-          w[8 * h + r / 2] = v0 | (v1 << 16);
-        }
-      uint4* d = (uint4*)(p.ut + ((size_t)(t.t16 + q) * p.K + j) * 32);
-#pragma unroll
-      for (int v = 0; v < 4; ++v) d[v] = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
-    }
-  }
-  const auto frag_u = [&](int i, int ks, int half) {
-    return as_frag(*(const uint4*)(lds + half * lo_off + u_chunk(16 * i + (lane & 15), 4 * ks + (lane >> 4), kp)));
+      for (int i = 0; i < 4; ++i)
+        bs[m][i] = p.base && c * 128 + 8 * rho < p.nout
+                       ? *(const uint4*)(p.base + rowo[m][i] + c * 128) : zero4();
   };
-  size_t rowo[MB];
-  bool ok[MB];
+  const auto load_w = [&](int c, int ks, uint4 (&wf)[8]) {
+    if constexpr (NN) {
+      const int col = min(c * 128 + 8 * rho, p.nout - 8);
 #pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int m = 16 * i + (lane & 15);
-    ok[i] = m < t.rows;
-    const int r = t.row0 + (ok[i] ? m : 0);
-    rowo[i] = (size_t)(GR ? p.src_token[r] : r) * p.nout + 8 * (lane >> 4);
-  }
-  bf16x8_t uh[KS ? MB : 1][KS ? KS : 1], ul[KS ? MB : 1][KS ? KS : 1];
-  if constexpr (KS > 0) {
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        uh[i][ks] = frag_u(i, ks, 0);
-        ul[i][ks] = frag_u(i, ks, 1);
-      }
-  }
-  const bf16_t* W = p.w + (size_t)t.a * p.nout * p.wld;
-  const int chunks = (p.nout + 31) / 32, cper = (chunks + p.osplit - 1) / p.osplit;
-  const int c1 = min(chunks, (oz + 1) * cper);
-  const int rho = lane & 15, wrow = 8 * (rho >> 2) + (rho & 3);
-  for (int c = oz * cper + wv; c < c1; c += 4) {
-    const int o0 = c * 32;
-    const bool in = o0 + 8 * (lane >> 4) < p.nout;
-    uint4 bs[MB];
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-      bs[i] = p.base && ok[i] && in ? *(const uint4*)(p.base + rowo[i] + o0) : zero4();
-    f32x4v acc[MB][2];
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) acc[i][b] = (f32x4v){0.f, 0.f, 0.f, 0.f};
-    const bf16_t* wp[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-      wp[b] = W + (size_t)min(o0 + wrow + 4 * b, p.nout - 1) * p.wld + 8 * (lane >> 4);
-    if constexpr (KS > 0) {
-      uint4 wf[KS][2];
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-          wf[ks][b] = 32 * ks + 8 * (lane >> 4) < p.wld ? *(const uint4*)(wp[b] + 32 * ks) : zero4();
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int i = 0; i < MB; ++i)
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            acc[i][b] = mfma16(as_frag(wf[ks][b]), ul[i][ks], acc[i][b]);
-            acc[i][b] = mfma16(as_frag(wf[ks][b]), uh[i][ks], acc[i][b]);
-          }
+      for (int i = 0; i < 8; ++i)  // rows past K meet zeros of u
+        wf[i] = *(const uint4*)(W + (size_t)min(32 * ks + 8 * g + i, p.K - 1) * p.nout + col);
     } else {
-#pragma unroll 2
-      for (int ks = 0; ks < ksteps; ++ks) {
-        uint4 wf[2];
+      const int k = 32 * ks + 8 * g;
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-          wf[b] = 32 * ks + 8 * (lane >> 4) < p.wld ? *(const uint4*)(wp[b] + 32 * ks) : zero4();
+      for (int f = 0; f < 8; ++f)
+        wf[f] = k < p.K ? *(const uint4*)(W + (size_t)min(c * 128 + 8 * rho + f, p.nout - 1) * p.K + k)
+                        : zero4();
+    }
+  };
+  // the first block's loads go out before u is put together
+  int c = oz * bper + wv;
+  uint4 bs[MB][4], wf0[8], wf1[8];
+  if (c < c1) {
+    load_w(c, 0, wf0);
+    load_base(c, bs);  // later blocks': at their start, after the stores before them
+  }
+  bool first = true;
+  fill_u<16 * MB>(p, t, kp, lds);
+  __syncthreads();
+  if (p.ut && oz == 0) store_halves<MB>(lds, lo_off, kp, p.K, t, p.ut);
+  for (; c < c1; c += 4) {
+    if (!first) load_base(c, bs);
+    first = false;
+    f32x4v acc[MB][8];
 #pragma unroll
-        for (int i = 0; i < MB; ++i) {
-          const bf16x8_t h = frag_u(i, ks, 0), l = frag_u(i, ks, 1);
+    for (int m = 0; m < MB; ++m)
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            acc[i][b] = mfma16(as_frag(wf[b]), l, acc[i][b]);
-            acc[i][b] = mfma16(as_frag(wf[b]), h, acc[i][b]);
-          }
-        }
+      for (int f = 0; f < 8; ++f) acc[m][f] = (f32x4v){0.f, 0.f, 0.f, 0.f};
+    const auto step = [&](int ks, const uint4 (&wf)[8]) {
+      bf16x8_t h[MB], l[MB];
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        const char* a = lds + u_chunk(16 * m + rho, 4 * ks + g, kp);
+        h[m] = as_frag(*(const uint4*)a);
+        l[m] = as_frag(*(const uint4*)(a + lo_off));
+      }
+      uint4 w[8];
+      if constexpr (NN) {
+        transpose8(wf, w);
+      } else {
+#pragma unroll
+        for (int f = 0; f < 8; ++f) w[f] = wf[f];
+      }
+#pragma unroll
+      for (int f = 0; f < 8; ++f) {
+#pragma unroll
+        for (int m = 0; m < MB; ++m) acc[m][f] = mfma16(l[m], as_frag(w[f]), acc[m][f]);
+#pragma unroll
+        for (int m = 0; m < MB; ++m) acc[m][f] = mfma16(h[m], as_frag(w[f]), acc[m][f]);
+      }
+    };
+    const bool more = c + 4 < c1;
+    for (int ks = 0; ks < ksteps; ks += 2) {
+      if (ks + 1 < ksteps) load_w(c, ks + 1, wf1);
+      else if (more) load_w(c + 4, 0, wf1);
+      step(ks, wf0);
+      if (ks + 1 < ksteps) {
+        if (ks + 2 < ksteps) load_w(c, ks + 2, wf0);
+        else if (more) load_w(c + 4, 0, wf0);
+        step(ks + 1, wf1);
+      } else {
+#pragma unroll
+        for (int f = 0; f < 8; ++f) wf0[f] = wf1[f];
       }
     }
+    if (c * 128 + 8 * rho < p.nout) {
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      if (!ok[i] || !in) continue;
-      float f[8];
-      unpack8(bs[i], f);
+      for (int m = 0; m < MB; ++m)
 #pragma unroll
-      for (int v = 0; v < 8; ++v) f[v] += acc[i][v >> 2][v & 3];
-      *(uint4*)(p.y + rowo[i] + o0) = pack8(f);
+        for (int i = 0; i < 4; ++i) {
+          if (16 * m + 4 * g + i >= t.rows) continue;
+          float f[8];
+          unpack8(bs[m][i], f);
+#pragma unroll
+          for (int v = 0; v < 8; ++v) f[v] += acc[m][v][i];
+          *(uint4*)(p.y + rowo[m][i] + c * 128) = pack8(f);
+        }
     }
   }
 }
 
-// ----------------------------------------------------------------------- wgrad
-// A workgroup of 4 wavefronts forms 32 JB WJ rows (j) x 128 columns (h) of one group's
-// gradient over one chunk of its rows.  The wide operand x passes through LDS, where the
-// transposing reads turn its rows into K-major fragments; the short one comes as the
-// halves that `expand` left along the rows, straight into registers.  WJ wavefronts share
-// out j, the others h.
-template <int JB, int WJ, bool GR>
-__global__ __launch_bounds__(256) void wgrad_kernel(WgradArgs p) {
-  constexpr int WH = 4 / WJ, HB = 4 / WH;  // wavefronts along h, 32-column blocks of each
-  __shared__ __attribute__((aligned(16))) char lds[2][64 * 256];
+// Many rows (64 MB a tile, 16 MB a wavefront): u stays in registers (KS K steps of 32) and
+// the weights of SB column blocks pass through LDS in fragment order, shared by the four
+// wavefronts, double-buffered: loaded from memory in whole lines while the blocks before
+// are multiplied, turned in registers (NN) or by where they are written (NT).  base is read
+// where it is needed: reading it a block ahead, between the stores, took the plain copy of
+// this pattern from 48 us (8192 x 7168) to 73, and to 90 four blocks ahead.
+template <int MB, int KS, bool NN, bool GR>
+__global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void expand_tile_kernel(ExpandArgs p) {
+  constexpr int SB = KS >= 4 ? 1 : 4 / KS;  // column blocks of a stage
+  constexpr int NU = SB * KS / 4;           // fragment groups (8 KiB) a wavefront brings
+  constexpr int STAGE = SB * KS * 8192;
+  constexpr int ROWS = 64 * MB, KP = 32 * KS;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const WgradSide d = p.side[blockIdx.z];
-  const int h0 = blockIdx.x * 128, ch = blockIdx.y / p.jblk;
-  const int j0 = (blockIdx.y % p.jblk) * 32 * JB * WJ + (wv % WJ) * 32 * JB;
-  const int hw = (wv / WJ) * 32 * HB;
-  if (h0 >= d.H) return;
-  GroupPos g;
+  if (GR && (int)blockIdx.x >= p.max_tiles * p.osplit) {
+    copy_ungrouped(p, blockIdx.x - p.max_tiles * p.osplit);
+    return;
+  }
+  const int tile = blockIdx.x / p.osplit, oz = blockIdx.x % p.osplit;
+  SkinnyTile t;
+  if (!skinny_tile<GR>(p.counts, p.n, p.T, ROWS, tile, t)) return;
+  const int g = lane >> 4, rho = lane & 15;
+  const bf16_t* W = p.w + (size_t)t.a * p.nout * p.K;
+  const int blocks = (p.nout + 128 * SB - 1) / (128 * SB), bper = (blocks + p.osplit - 1) / p.osplit;
+  const int s0 = oz * bper, s1 = min(blocks, s0 + bper);
+  uint4 wr[NU][8];
+  const auto load_w = [&](int sb) {
+#pragma unroll
+    for (int n = 0; n < NU; ++n) {
+      if constexpr (NN) {  // unit: K step ks of column block cb
+        const int unit = wv * NU + n, ks = unit % KS, cb = unit / KS;
+        const int col = min((sb * SB + cb) * 128 + 8 * rho, p.nout - 8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int k = 32 * ks + 8 * g + i;
+          wr[n][i] = k < p.K ? *(const uint4*)(W + (size_t)k * p.nout + col) : zero4();
+        }
+      } else {  // the stage's rows of K values lie one after the other: 16-byte pieces in turn
+        const int cpr = p.K >> 3;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int q = (n * 8 + i) * 256 + (int)threadIdx.x, row = sb * SB * 128 + q / cpr;
+          wr[n][i] = zero4();
+          if (q < SB * 128 * cpr && row < p.nout)
+            wr[n][i] = *(const uint4*)(W + (size_t)sb * SB * 128 * p.K + (size_t)q * 8);
+        }
+      }
+    }
+  };
+  const auto store_w = [&](char* st) {
+#pragma unroll
+    for (int n = 0; n < NU; ++n) {
+      if constexpr (NN) {
+        uint4 f[8];
+        transpose8(wr[n], f);
+        char* d = st + (wv * NU + n) * 8192 + lane * 16;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *(uint4*)(d + i * 1024) = f[i];
+      } else {
+        const int cpr = p.K >> 3;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int q = (n * 8 + i) * 256 + (int)threadIdx.x, row = q / cpr, c = q - row * cpr;
+          if (q < SB * 128 * cpr)  // row 8 rho + f of block cb, chunk 4 ks + g
+            *(uint4*)(st + (((row >> 7) * KS + (c >> 2)) * 8 + (row & 7)) * 1024 +
+                      ((c & 3) * 16 + ((row >> 3) & 15)) * 16) = wr[n][i];
+        }
+      }
+    }
+  };
+  // byte offsets of this lane's rows; past the tile's rows or the columns: out of range,
+  // where loads give zeros and stores nothing (as all of a null base), without branches
+  constexpr uint32_t OUT = 0xffffffffu;
+  const uint32_t nbytes = (uint32_t)p.T * (uint32_t)p.nout * 2;  // below 4 GiB
+  const rsrc_t rb = make_rsrc(p.base, p.base ? nbytes : 0), ry = make_rsrc(p.y, nbytes);
+  uint32_t rowo[MB][4];
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 16 * (MB * wv + m) + 4 * g + i, row = t.row0 + min(r, t.rows - 1);
+      const uint32_t o = (uint32_t)(GR ? p.src_token[row] : row) * (uint32_t)p.nout * 2;
+      rowo[m][i] = r < t.rows ? o + 16 * rho : OUT;
+    }
+  if (s0 < s1) load_w(s0);
+  fill_u<ROWS>(p, t, KP, lds);
+  __syncthreads();
+  if (p.ut && oz == 0) store_halves<4 * MB>(lds, ROWS * KP * 2, KP, p.K, t, p.ut);
+  bf16x8_t uh[MB][KS], ul[MB][KS];
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const char* a = lds + u_chunk(16 * (MB * wv + m) + rho, 4 * ks + g, KP);
+      uh[m][ks] = as_frag(*(const uint4*)a);
+      ul[m][ks] = as_frag(*(const uint4*)(a + ROWS * KP * 2));
+    }
+  __syncthreads();
+  if (!NN && (p.K & 31)) {  // K values that no store below writes
+    for (int i = threadIdx.x; i < 2 * STAGE / 16; i += 256) *(uint4*)(lds + i * 16) = zero4();
+    __syncthreads();
+  }
+  if (s0 < s1) store_w(lds);
+  __syncthreads();
+  for (int sb = s0; sb < s1; ++sb) {
+    const char* cur = lds + ((sb - s0) & 1) * STAGE;
+    const bool more = sb + 1 < s1;
+    if (more) load_w(sb + 1);
+#pragma unroll
+    for (int cb = 0; cb < SB; ++cb) {
+      const int c = sb * SB + cb;
+      const bool in = c * 128 + 8 * rho < p.nout;
+      u32x4_t bs[MB][4];
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          bs[m][i] = __builtin_amdgcn_raw_buffer_load_b128(
+              rb, in && rowo[m][i] != OUT ? rowo[m][i] + (uint32_t)c * 256 : OUT, 0, 0);
+      f32x4v acc[MB][8];
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int f = 0; f < 8; ++f) acc[m][f] = (f32x4v){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int f = 0; f < 8; ++f) {
+          const bf16x8_t w = as_frag(*(const uint4*)(cur + ((cb * KS + ks) * 8 + f) * 1024 + lane * 16));
+#pragma unroll
+          for (int m = 0; m < MB; ++m) acc[m][f] = mfma16(ul[m][ks], w, acc[m][f]);
+#pragma unroll
+          for (int m = 0; m < MB; ++m) acc[m][f] = mfma16(uh[m][ks], w, acc[m][f]);
+        }
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float f[8];
+          unpack8(__builtin_bit_cast(uint4, bs[m][i]), f);
+#pragma unroll
+          for (int v = 0; v < 8; ++v) f[v] += acc[m][v][i];
+          __builtin_amdgcn_raw_buffer_store_b128(
+              __builtin_bit_cast(u32x4_t, pack8(f)), ry,
+              in && rowo[m][i] != OUT ? rowo[m][i] + (uint32_t)c * 256 : OUT, 0, 0);
+        }
+    }
+    if (more) store_w(lds + ((sb + 1 - s0) & 1) * STAGE);
+    __syncthreads();
+  }
+}
+
+// ----------------------------------------------------------------------- wgrad
+// A workgroup of 4 wavefronts forms 16 JT WJ rows (j) x 128 columns (h) of one group's
+// gradient over one chunk of its rows; WJ wavefronts share out j, the others the chunk's
+// 32-row tiles, whose sums are joined in LDS at the end.  Both operands reach LDS by direct
+// loads into a ring of 32-row tiles, x as whole 256-byte pieces of its rows, the short one
+// as the halves that `expand` left in fragment order, so that enough is in flight without
+// registers (with both in registers one tile ahead: 88 us against 235 MB of x and dy).  A
+// lane reads 8 rows of 8 columns and turns them in registers into 8 fragments along the
+// rows; row i of fragment f stands for column 8 i + f.
+//   TR = false, [J][H]: x as the M side, a lane ends with 8 neighbouring h
+//   TR = true, [H][J]: the halves as the M side, a lane ends with 4 neighbouring j
+template <int JT, int WJ>
+struct WgradTile {
+  static constexpr int WK = 4 / WJ, JB = JT * WJ;       // 16-row blocks of j
+  static constexpr int UB = JB < 2 ? 4096 : JB * 2048;  // bytes of halves a tile
+  static constexpr int STAGE = WK * (8192 + UB);        // a tile for each wavefront along K
+  static constexpr int NS = STAGE == 32768 ? 4 : 3;  // 132, 76 or 148 KiB with the tokens
+  static constexpr int LOADS = WK * (2 + UB / 4096);    // per wavefront and stage
+  static constexpr int TOK = 4 * WGRAD_MAX_CHUNK;
+  static constexpr int LDS = NS * STAGE + TOK;
+};
+
+// 8 x 16 bytes of x (256 apart) and 2 JT x 16 bytes of halves (1024 apart)
+MOE_DEV void lds_read_x(uint32_t a, s16x8_t (&x)[8]) {
+  asm volatile(
+      "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:256\n\t"
+      "ds_read_b128 %2, %8 offset:512\n\tds_read_b128 %3, %8 offset:768\n\t"
+      "ds_read_b128 %4, %8 offset:1024\n\tds_read_b128 %5, %8 offset:1280\n\t"
+      "ds_read_b128 %6, %8 offset:1536\n\tds_read_b128 %7, %8 offset:1792\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]),
+        "=&v"(x[6]), "=&v"(x[7])
+      : "v"(a)
+      : "memory");
+}
+MOE_DEV void lds_read_u(uint32_t a, s16x8_t (&u)[2][2]) {
+  asm volatile(
+      "ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:1024\n\t"
+      "ds_read_b128 %2, %4 offset:2048\n\tds_read_b128 %3, %4 offset:3072\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(u[0][0]), "=&v"(u[0][1]), "=&v"(u[1][0]), "=&v"(u[1][1])
+      : "v"(a)
+      : "memory");
+}
+MOE_DEV void lds_read_u(uint32_t a, s16x8_t (&u)[1][2]) {
+  asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %2 offset:1024\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(u[0][0]), "=&v"(u[0][1])
+               : "v"(a)
+               : "memory");
+}
+MOE_DEV int lds_read_int(uint32_t a) {
+  int v;
+  asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(v) : "v"(a) : "memory");
+  return v;
+}
+
+template <int JT, int WJ, bool GR, bool TR>
+MOE_DEV void wgrad_body(const WgradArgs& p, const WgradSide& d, int hb, int cj, char* lds) {
+  using C = WgradTile<JT, WJ>;
+  constexpr int WK = C::WK;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int h0 = hb * 128, ch = cj / p.jblk;
+  const int jb0 = (cj % p.jblk) * C::JB, wj = wv % WJ, wk = wv / WJ;
   const int crows = p.chunk_rows;
+  GroupPos gp;
   int nch;
   if (GR) {
     const auto units = [crows](int c) { return max(1, (c + crows - 1) / crows); };
-    if (!find_group(p.counts, p.n, ch, units, g)) return;
-    nch = units(g.count);
+    if (!find_group(p.counts, p.n, ch, units, gp)) return;
+    nch = units(gp.count);
   } else {
     nch = max(1, (p.T + crows - 1) / crows);
-    g.a = 0;
-    g.unit = ch;
-    g.count = p.T;
-    g.row0 = g.t16 = 0;
+    gp.a = 0;
+    gp.unit = ch;
+    gp.count = p.T;
+    gp.row0 = gp.t32 = 0;
   }
-  const int r0 = g.unit * crows, rows = max(0, min(crows, g.count - r0));
-  const int row0 = g.row0 + r0, t16 = g.t16 + (r0 >> 4);
-  f32x16_t acc[JB][HB];
-#pragma unroll
-  for (int i = 0; i < JB; ++i)
-#pragma unroll
-    for (int j = 0; j < HB; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-  const int kb = threadIdx.x >> 4, ib = threadIdx.x & 15;  // rows 4 kb .. + 3, columns 8 ib .. + 7
-  const bool cin = h0 + 8 * ib < d.H;
-  const auto load = [&](int st, uint4 (&r)[4]) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int m = st * 64 + 4 * kb + q;
-      r[q] = zero4();
-      if (m < rows && cin) {
-        const int tok = GR ? p.src_token[row0 + m] : row0 + m;
-        r[q] = *(const uint4*)(d.x + (size_t)tok * d.H + h0 + 8 * ib);
-      }
-    }
-  };
-  const auto store = [&](char* t, const uint4 (&r)[4]) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int k = 4 * kb + q;
-      *(uint4*)(t + k * 256 + ((ib ^ mn_swz(k)) << 4)) = r[q];
-    }
-  };
-  const int stages = (rows + 63) / 64, nt = (rows + 15) / 16;
-  uint4 r[4];
-  if (stages) {
-    load(0, r);
-    store(lds[0], r);
-  }
-  __syncthreads();
-  for (int st = 0; st < stages; ++st) {
-    if (st + 1 < stages) load(st + 1, r);
-    const char* cur = lds[st & 1];
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      const int tt = st * 4 + ks;
-      if (tt < nt) {  // past the last tile there are no halves
-        bf16x8_t uh[JB], ul[JB];
-#pragma unroll
-        for (int i = 0; i < JB; ++i) {
-          const int j = min(j0 + 32 * i + (lane & 31), p.J - 1);
-          const bf16_t* u = d.ut + ((size_t)(t16 + tt) * p.J + j) * 32 + 8 * (lane >> 5);
-          uh[i] = as_frag(*(const uint4*)u);
-          ul[i] = as_frag(*(const uint4*)(u + 16));
-        }
-#pragma unroll
-        for (int c = 0; c < HB; ++c) {
-          const bf16x8_t x = frag16<false>(cur, hw + 32 * c, ks, lane);
-#pragma unroll
-          for (int i = 0; i < JB; ++i) {
-            if (d.transposed) {  // j along a lane's registers
-              acc[i][c] = mfma32(ul[i], x, acc[i][c]);
-              acc[i][c] = mfma32(uh[i], x, acc[i][c]);
-            } else {             // h along a lane's registers
-              acc[i][c] = mfma32(x, ul[i], acc[i][c]);
-              acc[i][c] = mfma32(x, uh[i], acc[i][c]);
-            }
-          }
-        }
-      }
-    }
-    if (st + 1 < stages) store(lds[(st + 1) & 1], r);
+  const int r0 = gp.unit * crows, rows = max(0, min(crows, gp.count - r0));
+  const int row0 = gp.row0 + r0;
+  char* tok = lds + C::NS * C::STAGE;  // the chunk's tokens
+  if (GR) {
+    for (int i = threadIdx.x; i < rows; i += 256) ((int32_t*)tok)[i] = p.src_token[row0 + i];
     __syncthreads();
+  }
+  const int g = lane >> 4, rho = lane & 15;
+  const int jb = (p.J + 15) / 16;
+  constexpr uint32_t OUT = 0xffffffffu;
+  const rsrc_t rx = make_rsrc(d.x, (uint32_t)p.T * (uint32_t)d.H * 2);  // below 4 GiB
+  const bool cin = h0 + 8 * rho < d.H;
+  // the chunk's halves, jb * 2048 bytes a tile, from block jb0 on
+  const int tiles = (rows + 31) / 32;
+  const rsrc_t ru = make_rsrc(d.ut + (size_t)(gp.t32 + (r0 >> 5)) * jb * 1024,
+                              (uint32_t)tiles * (uint32_t)jb * 2048);
+  f32x4v acc[JT][8];
+#pragma unroll
+  for (int i = 0; i < JT; ++i)
+#pragma unroll
+    for (int f = 0; f < 8; ++f) acc[i][f] = (f32x4v){0.f, 0.f, 0.f, 0.f};
+  const int stages = (tiles + WK - 1) / WK;
+  const auto issue = [&](int st) {
+    char* dst = lds + (st % C::NS) * C::STAGE;
+#pragma unroll
+    for (int w = 0; w < WK; ++w) {
+      const int tt = st * WK + w;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {  // rows 4 (2 wv + q) .. + 3: lane L row L / 16, 16 (L % 16)
+        const int m = 32 * tt + 4 * (2 * wv + q) + g;
+        uint32_t off = OUT;
+        if (GR) {
+          const int tk = lds_read_int(lds_at(tok) + 4 * min(m, crows - 1));
+          if (m < rows && cin) off = ((uint32_t)tk * (uint32_t)d.H + h0 + 8 * rho) * 2;
+        } else {
+          if (m < rows && cin) off = ((uint32_t)(row0 + m) * (uint32_t)d.H + h0 + 8 * rho) * 2;
+        }
+        dma16_buf(rx, off, 0u, dst + w * 8192 + (2 * wv + q) * 1024);
+      }
+#pragma unroll
+      for (int q = 0; q < C::UB / 4096; ++q) {  // 1 KiB pieces; of blocks past the last: zeros
+        const int piece = q * 4 + wv;
+        const bool in = tt < tiles && jb0 * 2 + piece < jb * 2;
+        dma16_buf(ru, in ? (uint32_t)(tt * jb + jb0) * 2048 + piece * 1024 + lane * 16 : OUT, 0u,
+                  dst + WK * 8192 + w * C::UB + piece * 1024);
+      }
+    }
+  };
+  for (int st = 0; st < C::NS - 1 && st < stages; ++st) issue(st);
+  for (int st = 0; st < stages; ++st) {
+    constexpr int L = C::LOADS;
+    const int ahead = min(C::NS - 2, stages - 1 - st);
+    // s_waitcnt vmcnt(ahead * L) lgkmcnt(0); vmcnt's high bits are bits 14 and 15
+    constexpr int W1 = (L & 15) | ((L >> 4) << 14) | 0x70;
+    constexpr int W2 = ((2 * L) & 15) | (((2 * L) >> 4) << 14) | 0x70;
+    if (ahead >= 2) __builtin_amdgcn_s_waitcnt(W2);
+    else if (ahead == 1) __builtin_amdgcn_s_waitcnt(W1);
+    else __builtin_amdgcn_s_waitcnt(0x70);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (st + C::NS - 1 < stages) issue(st + C::NS - 1);
+    const char* cur = lds + (st % C::NS) * C::STAGE;
+    s16x8_t x[8], u[JT][2];
+    lds_read_x(lds_at(cur + wk * 8192) + 8 * g * 256 + rho * 16, x);
+    lds_read_u(lds_at(cur + WK * 8192 + wk * C::UB) + wj * JT * 2048 + lane * 16, u);
+    uint4 xr[8], f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) xr[i] = __builtin_bit_cast(uint4, x[i]);
+    transpose8(xr, f);
+#pragma unroll
+    for (int v = 0; v < 8; ++v)
+#pragma unroll
+      for (int h = 1; h >= 0; --h)
+#pragma unroll
+        for (int j = 0; j < JT; ++j) {
+          const bf16x8_t uf = __builtin_bit_cast(bf16x8_t, u[j][h]);
+          acc[j][v] = TR ? mfma16(uf, as_frag(f[v]), acc[j][v]) : mfma16(as_frag(f[v]), uf, acc[j][v]);
+        }
+  }
+  __syncthreads();  // every wavefront is done with the ring
+  if constexpr (WK > 1) {
+    f32x4v(*part)[8][64] = (f32x4v(*)[8][64])lds;
+#pragma unroll
+    for (int j = 0; j < JT; ++j)
+#pragma unroll
+      for (int h = WK / 2; h >= 1; h /= 2) {
+        __syncthreads();
+        if (wk >= h && wk < 2 * h)
+#pragma unroll
+          for (int v = 0; v < 8; ++v) part[(wk - h) * WJ + wj][v][lane] = acc[j][v];
+        __syncthreads();
+        if (wk < h)
+#pragma unroll
+          for (int v = 0; v < 8; ++v) acc[j][v] += part[wk * WJ + wj][v][lane];
+      }
+    if (wk) return;
   }
   const size_t per = (size_t)p.J * d.H;
   float* part = d.parts + (size_t)ch * per;
-  bf16_t* out = d.out + (size_t)g.a * per;
+  bf16_t* out = d.out + (size_t)gp.a * per;
 #pragma unroll
-  for (int i = 0; i < JB; ++i)
+  for (int j = 0; j < JT; ++j) {
+    if constexpr (TR) {
+      const int jj = (jb0 + wj * JT + j) * 16 + 4 * g;
+      if (jj >= p.J) continue;  // J is a multiple of 8 here
 #pragma unroll
-    for (int c = 0; c < HB; ++c)
+      for (int v = 0; v < 8; ++v) {
+        const int h = h0 + 8 * rho + v;
+        if (h >= d.H) continue;
+        const f32x4v a = acc[j][v];
+        const size_t at = (size_t)h * p.J + jj;
+        if (nch > 1) *(f32x4v*)(part + at) = a;
+        else *(uint2*)(out + at) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+      }
+    } else {
+      const int jj = (jb0 + wj * JT + j) * 16 + rho;
+      if (jj >= p.J) continue;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int one = lane & 31, four = 8 * q + 4 * (lane >> 5);
-        const int j = j0 + 32 * i + (d.transposed ? four : one);
-        const int h = h0 + hw + 32 * c + (d.transposed ? one : four);
-        if (j >= p.J || h >= d.H) continue;
-        const f32x4v v = {acc[i][c][4 * q], acc[i][c][4 * q + 1], acc[i][c][4 * q + 2],
-                          acc[i][c][4 * q + 3]};
-        const size_t at = d.transposed ? (size_t)h * p.J + j : (size_t)j * d.H + h;
+      for (int i = 0; i < 4; ++i) {
+        const int h = h0 + 8 * (4 * g + i);
+        if (h >= d.H) continue;
+        float f[8];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) f[v] = acc[j][v][i];
+        const size_t at = (size_t)jj * d.H + h;
         if (nch > 1) {
-          *(f32x4v*)(part + at) = v;
+          *(float4*)(part + at) = make_float4(f[0], f[1], f[2], f[3]);
+          *(float4*)(part + at + 4) = make_float4(f[4], f[5], f[6], f[7]);
         } else {
-          *(uint2*)(out + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+          *(uint4*)(out + at) = pack8(f);
         }
       }
+    }
+  }
+}
+
+template <int JT, int WJ, bool GR>
+__global__ __launch_bounds__(256) void wgrad_kernel(WgradArgs p) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  const int hb = blockIdx.x % p.hblk, rest = blockIdx.x / p.hblk;
+  const bool second = hb >= p.hblk0;
+  const WgradSide d = p.side[second ? 1 : 0];
+  if (GR && d.transposed) wgrad_body<JT, WJ, GR, true>(p, d, hb - (second ? p.hblk0 : 0), rest, lds);
+  else wgrad_body<JT, WJ, GR, false>(p, d, hb, rest, lds);
 }
 
 // Gradients of the groups with several chunks: the sum of the chunks' parts, in order.
@@ -541,92 +1004,134 @@ __global__ __launch_bounds__(256) void wgrad_sum_kernel(WgradArgs p) {
   const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= per) return;
   f32x4v v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
   for (int c = 0; c < nch; ++c) v += *(const f32x4v*)(d.parts + (size_t)(first + c) * per + i);
   *(uint2*)(d.out + (size_t)a * per + i) =
       make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
 // ------------------------------------------------------------------- transpose
-// dst [n][C][ldd] = src [n][R][C] transposed, zero for rows R .. ldd - 1; 64 x 64 tiles.
-__global__ __launch_bounds__(256) void transpose_kernel(TransposeArgs a0, TransposeArgs a1) {
-  const TransposeArgs a = blockIdx.z ? a1 : a0;
+// dst [n][C][R] = src [n][R][C] transposed (R and C multiples of 8); 64 x 64 tiles.
+__global__ __launch_bounds__(256) void transpose_kernel(const bf16_t* __restrict__ src_all,
+                                                        bf16_t* __restrict__ dst_all, int R, int C) {
   __shared__ bf16_t t[64][66];
-  const int rt = (a.ldd + 63) / 64, ct = (a.C + 63) / 64;
-  const int g = blockIdx.y;
-  if ((int)blockIdx.x >= rt * ct) return;
+  const int rt = (R + 63) / 64;
   const int r0 = (blockIdx.x % rt) * 64, c0 = (blockIdx.x / rt) * 64;
-  const bf16_t* src = a.src + (size_t)g * a.R * a.C;
-  bf16_t* dst = a.dst + (size_t)g * a.C * a.ldd;
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int r = r0 + i / 64, c = c0 + i % 64;
-    t[i / 64][i % 64] = r < a.R && c < a.C ? src[(size_t)r * a.C + c] : (bf16_t)0;
+  const bf16_t* src = src_all + (size_t)blockIdx.y * R * C;
+  bf16_t* dst = dst_all + (size_t)blockIdx.y * R * C;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int i = threadIdx.x + 256 * q, r = i >> 3, c = (i & 7) * 8;
+    uint4 v = zero4();
+    if (r0 + r < R && c0 + c < C) v = *(const uint4*)(src + (size_t)(r0 + r) * C + c0 + c);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) *(uint32_t*)&t[r][c + 2 * w] = u4_word(v, w);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int c = c0 + i / 64, r = r0 + i % 64;
-    if (c < a.C && r < a.ldd) dst[(size_t)c * a.ldd + r] = t[i % 64][i / 64];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int i = threadIdx.x + 256 * q, c = i >> 3, r = (i & 7) * 8;
+    if (c0 + c >= C || r0 + r >= R) continue;
+    uint32_t w[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) w[v] = t[r + 2 * v][c] | ((uint32_t)t[r + 2 * v + 1][c] << 16);
+    *(uint4*)(dst + (size_t)(c0 + c) * R + r0 + r) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-}
-
-template <int MB, int NB, int NW>
-hipError_t dot_go(const char* name, const DotArgs& p, int tiles, hipStream_t s) {
-  const long g = (long)tiles * ((p.N + 16 * NB - 1) / (16 * NB)) * p.S;
-  if (p.counts)
-    return MOE_LAUNCH(name, s, dot_kernel<MB, NB, NW, true><<<(unsigned)g, NW * 64, 0, s>>>(p));
-  return MOE_LAUNCH(name, s, dot_kernel<MB, NB, NW, false><<<(unsigned)g, NW * 64, 0, s>>>(p));
-}
-
-template <int MB, int KS>
-hipError_t expand_go(const char* name, const ExpandArgs& p, hipStream_t s) {
-  const int ksteps = KS ? KS : (p.K + 31) / 32;
-  const unsigned lds = 16u * MB * 32 * ksteps * 4;
-  const long extra = p.counts && p.base != p.y ? (p.T + 15) / 16 : 0;
-  const unsigned g = (unsigned)((long)p.max_tiles * p.osplit + extra);
-  if (p.counts) {
-    auto* k = expand_kernel<MB, KS, true>;
-    return MOE_LAUNCH(name, s, k<<<g, 256, lds, s>>>(p));
-  }
-  auto* k = expand_kernel<MB, KS, false>;
-  return MOE_LAUNCH(name, s, k<<<g, 256, lds, s>>>(p));
 }
 
 int div_up(int a, int b) { return (a + b - 1) / b; }
+
+template <int NB>
+hipError_t dot_small(const char* name, const DotArgs& p, int tiles, hipStream_t s) {
+  const unsigned g = (unsigned)((long)tiles * div_up(p.N, 16 * NB) * p.S);
+  if (p.counts) return MOE_LAUNCH(name, s, dot_kernel<NB, true><<<g, 512, 0, s>>>(p));
+  return MOE_LAUNCH(name, s, dot_kernel<NB, false><<<g, 512, 0, s>>>(p));
+}
+
+template <int BN>
+hipError_t dot_tiles(const char* name, const DotArgs& p, int tiles, hipStream_t s) {
+  const unsigned g = (unsigned)((long)tiles * div_up(p.N, BN) * p.S);
+  const unsigned lds = DT_NS * DotTile<BN>::STAGE;
+  if (p.counts) return MOE_LAUNCH(name, s, dot_tile_kernel<BN, true><<<g, 256, lds, s>>>(p));
+  return MOE_LAUNCH(name, s, dot_tile_kernel<BN, false><<<g, 256, lds, s>>>(p));
+}
+
+unsigned expand_grid(const ExpandArgs& p) {
+  const long extra = p.counts && p.base != p.y ? div_up(p.T, 16) : 0;
+  return (unsigned)((long)p.max_tiles * p.osplit + extra);
+}
+
+template <int MB, bool NN, bool GR>
+hipError_t expand_small(const char* name, const ExpandArgs& p, hipStream_t s) {
+  const unsigned lds = 16u * MB * 32 * div_up(p.K, 32) * 4;
+  auto* k = expand_kernel<MB, NN, GR>;
+  return MOE_LAUNCH(name, s, k<<<expand_grid(p), 256, lds, s>>>(p));
+}
+
+template <int MB, int KS, bool NN, bool GR>
+hipError_t expand_tiles(const char* name, const ExpandArgs& p, hipStream_t s) {
+  const unsigned w = 2u * (KS >= 4 ? KS : 4) * 8192, u = 64u * MB * 32 * KS * 4;
+  auto* k = expand_tile_kernel<MB, KS, NN, GR>;
+  return MOE_LAUNCH(name, s, k<<<expand_grid(p), 256, w > u ? w : u, s>>>(p));
+}
+
+template <bool NN, bool GR>
+hipError_t expand_ks(const char* name, const ExpandArgs& p, const ExpandPlan& c, hipStream_t s) {
+  if (c.ks == 0) {
+    if constexpr (!GR)  // rank <= 128: grouped tiles of 64 rows and more have their K steps
+      if (c.mb == 2) return expand_small<2, NN, GR>(name, p, s);
+    return expand_small<1, NN, GR>(name, p, s);
+  }
+  if (c.ks == 8) {
+    if constexpr (!GR) return expand_tiles<2, 8, NN, GR>(name, p, s);  // rank <= 128
+    return hipErrorNotSupported;
+  }
+  if (c.mb == 1) {
+    if (c.ks == 1) return expand_tiles<1, 1, NN, GR>(name, p, s);
+    if (c.ks == 2) return expand_tiles<1, 2, NN, GR>(name, p, s);
+    return expand_tiles<1, 4, NN, GR>(name, p, s);
+  }
+  if (c.ks == 1) return expand_tiles<2, 1, NN, GR>(name, p, s);
+  if (c.ks == 2) return expand_tiles<2, 2, NN, GR>(name, p, s);
+  return expand_tiles<2, 4, NN, GR>(name, p, s);
+}
+
+int row_tiles(int T, int n, bool grouped, int rows) {
+  return div_up(T, rows) + (grouped ? (n < T ? n : T) : 0);
+}
 
 }  // namespace
 
 SkinnyPlan skinny_plan(int T, int n, bool grouped, int K, int N) {
   SkinnyPlan c;
   const int groups = !grouped ? 1 : (n < T ? n : T);
-  c.mb = T >= 32 * groups ? 4 : 1;
-  c.tiles = skinny_tiles(T, n, grouped, c.mb);
-  const int nblk = div_up(N, N > 32 ? 64 : (N > 16 ? 32 : 16));
-  const int nw = c.mb == 4 ? 4 : 8, steps = div_up(K, 64);
-  const int most = div_up(steps, c.mb == 4 ? 2 * nw : nw);
-  const int want = c.tiles > 0 ? div_up(512, c.tiles * nblk) : 1;
-  c.S = want < most ? want : most;
+  c.few = !grouped && T <= DOT_FEW;
+  c.tile = T >= 32 * groups;
+  c.bn = !c.tile ? (N <= 16 ? 16 : (N <= 32 ? 32 : 64)) : (N <= 32 ? 32 : (N <= 64 ? 64 : 128));
+  c.tiles = row_tiles(T, n, grouped, c.tile ? 64 : 16);
+  const int wg = c.tiles * div_up(N, c.bn), blocks = div_up(K, 64);
+  const int most = div_up(blocks, 8);  // 8 blocks of 64: a step of each wavefront, or a full ring
+  const int target = c.tile && c.bn == 128 ? 256 : 512;
+  const int want = wg > 0 ? div_up(target, wg) : 1;
+  c.S = c.few ? 1 : (want < most ? want : most);
   return c;
 }
 
-int skinny_tiles(int T, int n, bool grouped, int mb) {
-  return div_up(T, 16 * mb) + (grouped ? (n < T ? n : T) : 0);
-}
-
-int expand_osplit(int tiles, int nout) {
-  const int most = div_up(div_up(nout, 32), 4);
-  int w = div_up(1024, tiles > 0 ? tiles : 1);
-  return w < most ? w : most;
-}
-
-hipError_t launch_dot(const char* name, const DotArgs& p, int mb, int tiles, hipStream_t s) {
-  if (tiles == 0) return hipSuccess;
-  if (mb == 4) {
-    if (p.N <= 16) return dot_go<4, 1, 4>(name, p, tiles, s);
-    if (p.N <= 32) return dot_go<4, 2, 4>(name, p, tiles, s);
-    return dot_go<4, 4, 4>(name, p, tiles, s);
+hipError_t launch_dot(const char* name, const DotArgs& p, const SkinnyPlan& c, hipStream_t s) {
+  if (p.T == 0) return hipSuccess;
+  if (c.few) {
+    if (p.T <= 1) return MOE_LAUNCH(name, s, dot_few_kernel<1><<<(unsigned)p.N, 256, 0, s>>>(p));
+    if (p.T <= 4) return MOE_LAUNCH(name, s, dot_few_kernel<4><<<(unsigned)p.N, 256, 0, s>>>(p));
+    return MOE_LAUNCH(name, s, dot_few_kernel<DOT_FEW><<<(unsigned)p.N, 256, 0, s>>>(p));
   }
-  if (p.N <= 16) return dot_go<1, 1, 8>(name, p, tiles, s);
-  if (p.N <= 32) return dot_go<1, 2, 8>(name, p, tiles, s);
-  return dot_go<1, 4, 8>(name, p, tiles, s);
+  if (!c.tile) {
+    if (c.bn == 16) return dot_small<1>(name, p, c.tiles, s);
+    if (c.bn == 32) return dot_small<2>(name, p, c.tiles, s);
+    return dot_small<4>(name, p, c.tiles, s);
+  }
+  if (c.bn == 32) return dot_tiles<32>(name, p, c.tiles, s);
+  if (c.bn == 64) return dot_tiles<64>(name, p, c.tiles, s);
+  return dot_tiles<128>(name, p, c.tiles, s);
 }
 
 hipError_t launch_sum_parts(const char* name, const float* parts, int S, size_t n, float* out,
@@ -635,36 +1140,60 @@ hipError_t launch_sum_parts(const char* name, const float* parts, int S, size_t 
   return MOE_LAUNCH(name, s, sum_parts_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(parts, S, n, out));
 }
 
-hipError_t launch_expand(const char* name, const ExpandArgs& p, int mb, hipStream_t s) {
-  if (p.T == 0) return hipSuccess;
-  const int ks = div_up(p.K, 32);
-  if (mb == 4) {
-    if (ks == 1) return expand_go<4, 1>(name, p, s);
-    if (ks == 2) return expand_go<4, 2>(name, p, s);
-    return expand_go<4, 0>(name, p, s);
+ExpandPlan expand_plan(int T, int n, bool grouped, int K, int nout) {
+  ExpandPlan c;
+  const int groups = !grouped ? 1 : (n < T ? n : T);
+  if (T < 32 * groups || K > 256) {
+    c.ks = 0;
+    c.mb = T >= 32 * groups && K <= 512 ? 2 : 1;  // the rows' halves take at most 64 KiB of LDS
+    c.tiles = row_tiles(T, n, grouped, 16 * c.mb);
+    const int most = div_up(div_up(nout, 128), 4), w = c.tiles > 0 ? div_up(1024, c.tiles) : 1;
+    c.osplit = w < most ? w : most;
+  } else {
+    c.ks = K <= 32 ? 1 : (K <= 64 ? 2 : (K <= 128 ? 4 : 8));
+    c.mb = c.ks == 8 || T >= 128 * groups ? 2 : 1;
+    c.tiles = row_tiles(T, n, grouped, 64 * c.mb);
+    const int stages = div_up(nout, c.ks >= 4 ? 128 : 512 / c.ks);
+    const int target = c.ks == 8 ? 256 : 512, w = c.tiles > 0 ? div_up(target, c.tiles) : 1;
+    c.osplit = w < stages ? w : stages;
   }
-  if (ks == 1) return expand_go<1, 1>(name, p, s);
-  if (ks == 2) return expand_go<1, 2>(name, p, s);
-  return expand_go<1, 0>(name, p, s);
+  return c;
 }
 
-int wgrad_chunk_slots(int T, int n, int chunk_rows) {
-  return n > 0 ? T / chunk_rows + n : (T > 0 ? div_up(T, chunk_rows) : 1);
+hipError_t launch_expand(const char* name, const ExpandArgs& p, const ExpandPlan& c, bool nn,
+                         hipStream_t s) {
+  if (p.T == 0) return hipSuccess;
+  if (!p.counts) return expand_ks<true, false>(name, p, c, s);
+  return nn ? expand_ks<true, true>(name, p, c, s) : expand_ks<false, true>(name, p, c, s);
+}
+
+int wgrad_chunk(int T, int hblocks, int J) {
+  const int wg = hblocks * div_up(J, 128);
+  const int chunks = wg < 512 ? 512 / wg : 1;
+  const int r = div_up(div_up(T > 0 ? T : 1, chunks), 128) * 128;
+  return r > WGRAD_MAX_CHUNK ? WGRAD_MAX_CHUNK : r;
+}
+
+int wgrad_chunk_slots(int T, int n, bool grouped, int chunk_rows) {
+  return grouped ? T / chunk_rows + n : (T > 0 ? div_up(T, chunk_rows) : 1);
 }
 
 hipError_t launch_wgrad(const char* name, WgradArgs p, int sides, hipStream_t s) {
   const int hmax = sides > 1 && p.side[1].H > p.side[0].H ? p.side[1].H : p.side[0].H;
-  const int slots = wgrad_chunk_slots(p.T, p.counts ? p.n : 0, p.chunk_rows);
-  const int jt = p.J <= 32 ? 32 : (p.J <= 64 ? 64 : (p.J <= 128 ? 128 : 256));
-  p.jblk = div_up(p.J, jt);
-  const dim3 g((unsigned)div_up(hmax, 128), (unsigned)(slots * p.jblk), (unsigned)sides);
+  const int slots = wgrad_chunk_slots(p.T, p.n, p.counts != nullptr, p.chunk_rows);
+  p.jblk = div_up(p.J, 128);
+  p.hblk0 = div_up(p.side[0].H, 128);
+  p.hblk = p.hblk0 + (sides > 1 ? div_up(p.side[1].H, 128) : 0);
+  const unsigned g = (unsigned)((long)p.hblk * slots * p.jblk);
   hipError_t e;
-#define MOE_WGRAD_GO(JB, WJ)                                                                  \
-  e = p.counts ? MOE_LAUNCH(name, s, wgrad_kernel<JB, WJ, true><<<g, 256, 0, s>>>(p))         \
-               : MOE_LAUNCH(name, s, wgrad_kernel<JB, WJ, false><<<g, 256, 0, s>>>(p))
-  if (jt == 32) MOE_WGRAD_GO(1, 1);
-  else if (jt == 64) MOE_WGRAD_GO(2, 1);
-  else if (jt == 128) MOE_WGRAD_GO(2, 2);
+#define MOE_WGRAD_GO(JT, WJ)                                                                     \
+  e = p.counts ? MOE_LAUNCH(name, s,                                                             \
+                            wgrad_kernel<JT, WJ, true><<<g, 256, WgradTile<JT, WJ>::LDS, s>>>(p)) \
+               : MOE_LAUNCH(name, s,                                                             \
+                            wgrad_kernel<JT, WJ, false><<<g, 256, WgradTile<JT, WJ>::LDS, s>>>(p))
+  if (p.J <= 16) MOE_WGRAD_GO(1, 1);
+  else if (p.J <= 32) MOE_WGRAD_GO(2, 1);
+  else if (p.J <= 64) MOE_WGRAD_GO(2, 2);
   else MOE_WGRAD_GO(2, 4);
 #undef MOE_WGRAD_GO
   if (e != hipSuccess || p.T <= p.chunk_rows) return e;
@@ -674,16 +1203,10 @@ hipError_t launch_wgrad(const char* name, WgradArgs p, int sides, hipStream_t s)
   return MOE_LAUNCH("wgrad_sum", s, wgrad_sum_kernel<false><<<gs, 256, 0, s>>>(p));
 }
 
-hipError_t launch_transpose(const char* name, int n, const TransposeArgs& a, const TransposeArgs* b,
+hipError_t launch_transpose(const char* name, int n, const bf16_t* src, bf16_t* dst, int R, int C,
                             hipStream_t s) {
-  int blocks = div_up(a.ldd, 64) * div_up(a.C, 64);
-  if (b) {
-    const int o = div_up(b->ldd, 64) * div_up(b->C, 64);
-    if (o > blocks) blocks = o;
-  }
-  return MOE_LAUNCH(name, s,
-                    transpose_kernel<<<dim3((unsigned)blocks, (unsigned)n, b ? 2u : 1u), 256, 0, s>>>(
-                        a, b ? *b : a));
+  const dim3 g((unsigned)(div_up(R, 64) * div_up(C, 64)), (unsigned)n);
+  return MOE_LAUNCH(name, s, transpose_kernel<<<g, 256, 0, s>>>(src, dst, R, C));
 }
 
 }  // namespace moe

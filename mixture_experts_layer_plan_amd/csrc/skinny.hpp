@@ -23,7 +23,7 @@ struct DotArgs {
 // y[m, :] = base[m, :] + (scale_a sum over parts of u[m, :]) w^T, rounded once
 struct ExpandArgs {
   const float* u;  // [S][R][K]
-  const bf16_t* w; // [n][nout][wld], wld >= K, zeros past K
+  const bf16_t* w;  // [n][nout][K], or nn: [n][K][nout]
   const bf16_t* base;  // by token, or null (zero); may be y
   bf16_t* y;
   const float* scale;  // [n] or null
@@ -31,11 +31,13 @@ struct ExpandArgs {
   const int32_t* counts;
   const int32_t* src_token;
   const int32_t* pos;  // row of each token, < 0: none (its y is its base)
-  int n, T, K, S, wld, nout, max_tiles, osplit;
+  int n, T, K, S, nout, max_tiles, osplit;
   size_t R;
 };
 // bytes of the halves of `rows` rows in n groups, K values each
-inline size_t halves_bytes(size_t rows, int n, int K) { return (rows / 16 + n) * (size_t)K * 64; }
+inline size_t halves_bytes(size_t rows, int n, int K) {
+  return (rows / 32 + n) * (size_t)((K + 15) / 16) * 2048;
+}
 
 // out[a] = sum over group a's rows of u (x) x: [J][H], or [H][J] if transposed
 struct WgradSide {
@@ -49,31 +51,36 @@ struct WgradArgs {
   WgradSide side[2];
   const int32_t* counts;
   const int32_t* src_token;
-  int n, T, J, chunk_rows, jblk;
+  int n, T, J, chunk_rows;
+  int jblk, hblk, hblk0;  // set by launch_wgrad
 };
 
-struct TransposeArgs {
-  const bf16_t* src;
-  bf16_t* dst;
-  int R, C, ldd;
-};
+constexpr int WGRAD_MAX_CHUNK = 1024;  // rows of one chunk (their tokens lie in LDS)
+constexpr int DOT_FEW = 8;             // tokens of the dot without matrix instructions
 
-// Row tile, row tiles (an upper bound) and K parts of a dot over T rows in n groups
-// (one if not grouped): from the sizes alone, so that the order of every sum is too.
+// How a dot or an expand of T rows in n groups (one if not grouped) is cut up: from the
+// sizes alone, so that the order of every sum is too.  tiles: row tiles, an upper bound.
 struct SkinnyPlan {
-  int mb, tiles, S;
+  bool few, tile;  // dot_few_kernel; dot_tile_kernel (else dot_kernel)
+  int bn, tiles, S;
 };
 SkinnyPlan skinny_plan(int T, int n, bool grouped, int K, int N);
-int skinny_tiles(int T, int n, bool grouped, int mb);  // row tiles of 16 mb rows, at most
-int expand_osplit(int tiles, int nout);
-int wgrad_chunk_slots(int T, int n, int chunk_rows);
+struct ExpandPlan {
+  int ks;  // K steps of expand_tile_kernel, 0: expand_kernel
+  int mb, tiles, osplit;
+};
+ExpandPlan expand_plan(int T, int n, bool grouped, int K, int nout);
+int wgrad_chunk(int T, int hblocks, int J);      // rows of a chunk; 128-column blocks of all sides
+int wgrad_chunk_slots(int T, int n, bool grouped, int chunk_rows);
 
-hipError_t launch_dot(const char* name, const DotArgs& p, int mb, int tiles, hipStream_t s);
+hipError_t launch_dot(const char* name, const DotArgs& p, const SkinnyPlan& c, hipStream_t s);
 hipError_t launch_sum_parts(const char* name, const float* parts, int S, size_t n, float* out,
                             hipStream_t s);
-hipError_t launch_expand(const char* name, const ExpandArgs& p, int mb, hipStream_t s);
+hipError_t launch_expand(const char* name, const ExpandArgs& p, const ExpandPlan& c, bool nn,
+                         hipStream_t s);
 hipError_t launch_wgrad(const char* name, WgradArgs p, int sides, hipStream_t s);
-hipError_t launch_transpose(const char* name, int n, const TransposeArgs& a, const TransposeArgs* b,
+// dst [n][C][R] from src [n][R][C]
+hipError_t launch_transpose(const char* name, int n, const bf16_t* src, bf16_t* dst, int R, int C,
                             hipStream_t s);
 
 }  // namespace moe
