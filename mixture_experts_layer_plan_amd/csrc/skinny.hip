@@ -21,10 +21,23 @@ namespace {
 
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 
+typedef __bf16 bf16x4v __attribute__((ext_vector_type(4)));
+MOE_DEV uint2 cvt4(const f32x4v& v) {
+  return __builtin_bit_cast(uint2, __builtin_convertvector(v, bf16x4v));
+}
+
 MOE_DEV f32x4v mfma16(bf16x8_t a, bf16x8_t b, f32x4v c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 MOE_DEV bf16x8_t as_frag(const uint4& v) { return __builtin_bit_cast(bf16x8_t, v); }
+
+// 8 floats -> 8 bf16 by the conversion instruction (two values each, to nearest even); the
+// integer form of pack8 is six instructions a value, more than the matrix work beside it.
+typedef float f32x8v __attribute__((ext_vector_type(8)));
+MOE_DEV uint4 cvt8(const float* f) {
+  const f32x8v v = {f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]};
+  return __builtin_bit_cast(uint4, __builtin_convertvector(v, bf16x8_t));
+}
 
 // Inclusive sum over the lanes of a wavefront.
 template <int CTRL, int ROWS>
@@ -192,19 +205,35 @@ __global__ __launch_bounds__(512) void dot_kernel(DotArgs p) {
 }
 
 // Many rows: a workgroup of 4 wavefronts forms 64 rows x BN columns over one of S parts of
-// K.  Both operands reach LDS by direct loads of 128-byte row pieces, 8 lanes each, into a
-// ring of NS 64-deep stages; the product of a stage runs while NS - 2 more are in flight.
+// K.  Both operands reach LDS by direct loads of K2-byte row pieces, 16 bytes a lane, into
+// a ring of NS stages; the product of a stage runs while NS - 1 more are in flight.
 // Fragments loaded from memory without LDS took 121 us for the 8192 x 256 x 7168 router
 // product: 16 lanes in 16 rows keep the address unit busy for 64 cycles a KiB.
-// Row r's 16-byte chunk c lies at r * 128 + 16 (c ^ (r & 7)): the 16 rows of a fragment
-// read hit all 64 banks.
-constexpr int DT_NS = 4;
+// Row r's 16-byte chunk c lies at r * K2 + 16 (c ^ (r & (CH - 1))): the 16 rows of a
+// fragment read hit all 64 banks.
 template <int BN>
 struct DotTile {
+  // 128 columns: 256-byte pieces and 8 wavefronts, of which two share a tile and halve K
+  static constexpr int KG = BN == 128 ? 2 : 1, BK = 64 * KG, K2 = 2 * BK, CH = K2 / 16;
   static constexpr int WN = BN >= 64 ? 2 : 1, WM = 4 / WN;  // wavefronts along rows, columns
   static constexpr int MB = 64 / 16 / WM, NB = BN / 16 / WN;
-  static constexpr int STAGE = (64 + BN) * 128, LOADS = (64 + BN) / 32;  // per wavefront
+  static constexpr int NS = 3, STAGE = (64 + BN) * K2;  // 36, 48, 144 KiB: 4, 3, 1 a CU
+  static constexpr int LOADS = STAGE / (4096 * KG), ALOADS = 64 * K2 / (4096 * KG);  // a wavefront
 };
+
+// Wait until at most `ahead` (0, 1, 2) stages of L loads are in flight, then meet the
+// workgroup.  vmcnt's two high bits are bits 14 and 15 of the operand.
+template <int L>
+MOE_DEV void ring_wait_for(int ahead) {
+  static_assert(2 * L < 64, "vmcnt has 6 bits");
+  constexpr int W1 = (L & 15) | ((L >> 4) << 14) | 0x70;
+  constexpr int W2 = ((2 * L) & 15) | (((2 * L) >> 4) << 14) | 0x70;
+  if (ahead >= 2) __builtin_amdgcn_s_waitcnt(W2);
+  else if (ahead == 1) __builtin_amdgcn_s_waitcnt(W1);
+  else __builtin_amdgcn_s_waitcnt(0x70);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");  // no LDS read of the stage moves above the barrier
+}
 
 // NR fragments (16 x 32) from LDS, waited for in the same block: the compiler would wait
 // for every direct load in flight before a read of its own.
@@ -238,75 +267,73 @@ MOE_DEV void lds_read6(const uint32_t (&a)[6], s16x8_t (&f)[6]) {
 }
 
 template <int BN, bool GR>
-__global__ __launch_bounds__(256) void dot_tile_kernel(DotArgs p) {
+__global__ __launch_bounds__(256 * DotTile<BN>::KG) void dot_tile_kernel(DotArgs p) {
   using C = DotTile<BN>;
-  constexpr int NR = C::MB + C::NB;
+  constexpr int NR = C::MB + C::NB, NWV = 4 * C::KG;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int nblk = (p.N + BN - 1) / BN;
-  const int id = xcd_order(blockIdx.x, gridDim.x);
+  // a row tile's column blocks on one XCD (grouped: one block; empty tiles spread evenly)
+  const int id = GR ? (int)blockIdx.x : xcd_order(blockIdx.x, gridDim.x);
   const int n0 = (id % nblk) * BN, s = (id / nblk) % p.S;
   SkinnyTile t;
   if (!skinny_tile<GR>(p.counts, p.n, p.T, 64, id / (nblk * p.S), t)) return;
   const uint32_t K2 = (uint32_t)p.K * 2;
   const rsrc_t ra = make_rsrc(p.a, (uint32_t)p.T * K2);  // below 4 GiB, checked on the host
   const rsrc_t rb = make_rsrc(p.b + (size_t)t.a * p.N * p.K, (uint32_t)p.N * K2);
-  // load q of a wavefront brings rows 8 (4 q + wv) .. + 7 of the stage (the 64 rows of a,
-  // then the BN of b): lane L row L / 8, chunk (L % 8) ^ (L / 8); past the range: zeros
+  // load q of a wavefront brings the RP rows from RP (NWV q + wv) on of the stage (the 64
+  // rows of a, then the BN of b): lane L row L / CH, chunk L % CH of LDS; out of range: zeros
   constexpr uint32_t OUT = 0xffffffffu;
-  const int r8 = lane >> 3, c8 = (lane & 7) ^ r8;
-  uint32_t off[C::LOADS];
+  constexpr int RP = 64 / C::CH;
+  uint32_t off[C::LOADS];  // of the row's first byte
+  int cq[C::LOADS];        // byte of its chunk in the piece
 #pragma unroll
   for (int q = 0; q < C::LOADS; ++q) {
-    const int r = 8 * (4 * q + wv) + r8;
-    if (q < 2) {
-      const int row = t.row0 + r;
-      off[q] = r < t.rows ? (uint32_t)(GR ? p.src_token[row] : row) * K2 + c8 * 16 : OUT;
+    const int r = RP * (NWV * q + wv) + lane / C::CH;
+    cq[q] = ((lane ^ r) & (C::CH - 1)) * 16;
+    if (q < C::ALOADS) {
+      const int row = t.row0 + min(r, t.rows - 1);
+      off[q] = (uint32_t)(GR ? p.src_token[row] : row) * K2;
+      if (r >= t.rows) off[q] = OUT;
     } else {
       const int n = n0 + r - 64;
-      off[q] = n < p.N ? (uint32_t)n * K2 + c8 * 16 : OUT;
+      off[q] = n < p.N ? (uint32_t)n * K2 : OUT;
     }
   }
-  const int blocks = (p.K + 63) / 64, per = (blocks + p.S - 1) / p.S;
+  const int blocks = (p.K + C::BK - 1) / C::BK, per = (blocks + p.S - 1) / p.S;
   const int b0 = s * per, nk = min(blocks, b0 + per) - b0;
   const auto issue = [&](int i) {
-    char* st = lds + (i % DT_NS) * C::STAGE;
-    const uint32_t k2 = (uint32_t)(b0 + i) * 128;
-    const bool in = k2 + c8 * 16 < K2;  // the last stage of a K that is no multiple of 64
+    char* st = lds + (i % C::NS) * C::STAGE;
 #pragma unroll
-    for (int q = 0; q < C::LOADS; ++q)
-      dma16_buf(q < 2 ? ra : rb, in && off[q] != OUT ? off[q] + k2 : OUT, 0u,
-                st + (4 * q + wv) * 1024);
+    for (int q = 0; q < C::LOADS; ++q) {
+      const uint32_t k2 = (uint32_t)(b0 + i) * C::K2 + cq[q];  // past K in the last stage
+      dma16_buf(q < C::ALOADS ? ra : rb, k2 < K2 && off[q] != OUT ? off[q] + k2 : OUT, 0u,
+                st + (NWV * q + wv) * 1024);
+    }
   };
   f32x4v acc[C::MB][C::NB];
 #pragma unroll
   for (int i = 0; i < C::MB; ++i)
 #pragma unroll
     for (int j = 0; j < C::NB; ++j) acc[i][j] = (f32x4v){0.f, 0.f, 0.f, 0.f};
-  const int wm = wv / C::WN, wn = wv % C::WN, g = lane >> 4, rho = lane & 15;
-  for (int i = 0; i < DT_NS - 1 && i < nk; ++i) issue(i);
+  const int kg = wv / 4, wm = (wv % 4) / C::WN, wn = wv % C::WN, g = lane >> 4, rho = lane & 15;
+  for (int i = 0; i < C::NS - 1 && i < nk; ++i) issue(i);
   for (int i = 0; i < nk; ++i) {
     // stage i is in (each later one has LOADS instructions), stage i - 1 no longer read
-    const int ahead = min(DT_NS - 2, nk - 1 - i);
-    constexpr int L = C::LOADS;
-    if (ahead >= 2) __builtin_amdgcn_s_waitcnt((2 * L) | 0x70);
-    else if (ahead == 1) __builtin_amdgcn_s_waitcnt(L | 0x70);
-    else __builtin_amdgcn_s_waitcnt(0x70);
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if (i + DT_NS - 1 < nk) issue(i + DT_NS - 1);
-    const char* st = lds + (i % DT_NS) * C::STAGE;
+    ring_wait_for<C::LOADS>(min(C::NS - 2, nk - 1 - i));
+    if (i + C::NS - 1 < nk) issue(i + C::NS - 1);
+    const char* st = lds + (i % C::NS) * C::STAGE;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t ad[NR];
       s16x8_t f[NR];
-      const int cx = ((4 * h + g) ^ (rho & 7)) << 4;
+      const int cx = ((4 * (2 * kg + h) + g) ^ (rho & (C::CH - 1))) << 4;
 #pragma unroll
       for (int m = 0; m < C::MB; ++m)
-        ad[m] = lds_at(st + (16 * (C::MB * wm + m) + rho) * 128 + cx);
+        ad[m] = lds_at(st + (16 * (C::MB * wm + m) + rho) * C::K2 + cx);
 #pragma unroll
       for (int n = 0; n < C::NB; ++n)
-        ad[C::MB + n] = lds_at(st + (64 + 16 * (C::NB * wn + n) + rho) * 128 + cx);
+        ad[C::MB + n] = lds_at(st + (64 + 16 * (C::NB * wn + n) + rho) * C::K2 + cx);
       if constexpr (NR == 3) lds_read3(ad, f);
       else if constexpr (NR == 4) lds_read4(ad, f);
       else lds_read6(ad, f);
@@ -317,6 +344,21 @@ __global__ __launch_bounds__(256) void dot_tile_kernel(DotArgs p) {
           acc[m][n] = mfma16(__builtin_bit_cast(bf16x8_t, f[C::MB + n]),
                              __builtin_bit_cast(bf16x8_t, f[m]), acc[m][n]);
     }
+  }
+  if constexpr (C::KG == 2) {  // join the halves of K
+    __syncthreads();           // every wavefront is done with the ring
+    f32x4v(*part)[C::NB][64] = (f32x4v(*)[C::NB][64])(lds + (wv % 4) * C::MB * C::NB * 1024);
+    if (kg)
+#pragma unroll
+      for (int m = 0; m < C::MB; ++m)
+#pragma unroll
+        for (int n = 0; n < C::NB; ++n) part[m][n][lane] = acc[m][n];
+    __syncthreads();
+    if (kg) return;
+#pragma unroll
+    for (int m = 0; m < C::MB; ++m)
+#pragma unroll
+      for (int n = 0; n < C::NB; ++n) acc[m][n] += part[m][n][lane];
   }
 #pragma unroll
   for (int m = 0; m < C::MB; ++m) {
@@ -402,11 +444,11 @@ MOE_DEV void transpose8(const uint4 (&r)[8], uint4 (&c)[8]) {
 template <int MB>
 MOE_DEV void store_halves(const char* lds, int lo_off, int kp, int K, const SkinnyTile& t,
                           bf16_t* __restrict__ ut) {
-  const int jb = (K + 15) / 16, js = 16 * jb;
+  const int jb = (K + 15) / 16;
   const bool pad = t.off + 16 * MB >= t.count;  // the last tile: zeros up to a multiple of 32
   const int groups = pad ? (((t.off + t.rows + 31) >> 5 << 5) - t.off) / 8 : 2 * MB;
-  for (int i = threadIdx.x; i < groups * js; i += 256) {
-    const int q = i / js, j = i - q * js, g8 = (t.off >> 3) + q;
+  for (int i = threadIdx.x >> 4; i < groups * jb; i += 16) {
+    const int q = i / jb, j = (i - q * jb) * 16 + (threadIdx.x & 15), g8 = (t.off >> 3) + q;
     uint32_t w[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -432,53 +474,80 @@ MOE_DEV void store_halves(const char* lds, int lo_off, int kp, int K, const Skin
 template <int ROWS>
 MOE_DEV void fill_u(const ExpandArgs& p, const SkinnyTile& t, int kp, char* lds) {
   const float sc = p.scale ? p.scale[t.a] : 1.0f;
-  const int ch = kp / 8, lo_off = ROWS * kp * 2;
-  for (int i = threadIdx.x; i < ROWS * ch; i += 256) {
-    const int m = i / ch, cc = i - m * ch;
-    float f[8];
+  const int ch = kp / 8, lo_off = ROWS * kp * 2, items = ROWS * ch;
+  const size_t part = p.R * p.K;
+#pragma unroll 1
+  for (int i0 = threadIdx.x; i0 < items; i0 += 4 * 256) {  // four pieces of 8 in flight
+    float f[4][8];
+    const float* u[4];
+    bool in[4];
 #pragma unroll
-    for (int v = 0; v < 8; ++v) f[v] = 0.0f;
-    if (m < t.rows) {
-      const float* u = p.u + ((size_t)t.row0 + m) * p.K;
-      const size_t part = p.R * p.K;
-      if ((p.K & 7) == 0) {
-        if (8 * cc < p.K) {
-#pragma unroll 4
-          for (int s = 0; s < p.S; ++s) {
-            const float4 a = *(const float4*)(u + s * part + 8 * cc);
-            const float4 b = *(const float4*)(u + s * part + 8 * cc + 4);
-            f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
-            f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
-          }
+    for (int q = 0; q < 4; ++q) {
+      const int i = min(i0 + q * 256, items - 1), m = i / ch, cc = i - m * ch;
+      in[q] = m < t.rows && 8 * cc < p.K;
+      u[q] = p.u + ((size_t)t.row0 + (in[q] ? m : 0)) * p.K + (in[q] ? 8 * cc : 0);
+#pragma unroll
+      for (int v = 0; v < 8; ++v) f[q][v] = 0.0f;
+    }
+    if ((p.K & 7) == 0) {
+#pragma unroll 2
+      for (int s = 0; s < p.S; ++s) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          a[q] = *(const float4*)(u[q] + s * part);
+          b[q] = *(const float4*)(u[q] + s * part + 4);
         }
-      } else {
-        for (int s = 0; s < p.S; ++s)
 #pragma unroll
-          for (int v = 0; v < 8; ++v)
-            if (8 * cc + v < p.K) f[v] += u[s * part + 8 * cc + v];
+        for (int q = 0; q < 4; ++q) {
+          f[q][0] += a[q].x; f[q][1] += a[q].y; f[q][2] += a[q].z; f[q][3] += a[q].w;
+          f[q][4] += b[q].x; f[q][5] += b[q].y; f[q][6] += b[q].z; f[q][7] += b[q].w;
+        }
+      }
+    } else {  // the router's dL: one part, rows of any length
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = min(i0 + q * 256, items - 1), left = p.K - 8 * (i % ch);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const float x = u[q][in[q] && v < left ? v : 0];
+          f[q][v] = v < left ? x : 0.0f;
+        }
       }
     }
-    float lo[8];
 #pragma unroll
-    for (int v = 0; v < 8; ++v) {
-      f[v] *= sc;
-      const float hi = bf16_to_f32(f32_to_bf16(f[v]));
-      lo[v] = fabsf(hi) < INFINITY ? f[v] - hi : 0.0f;
+    for (int q = 0; q < 4; ++q) {
+      const int i = i0 + q * 256, m = i / ch, cc = i - m * ch;
+      float hi[8], lo[8];
+#pragma unroll
+      for (int v = 0; v < 8; ++v) f[q][v] = in[q] ? f[q][v] * sc : 0.0f;
+      const uint4 h8 = cvt8(f[q]);
+      unpack8(h8, hi);
+#pragma unroll
+      for (int v = 0; v < 8; ++v) lo[v] = fabsf(hi[v]) < INFINITY ? f[q][v] - hi[v] : 0.0f;
+      if (i < items) {
+        *(uint4*)(lds + u_chunk(m, cc, kp)) = h8;
+        *(uint4*)(lds + lo_off + u_chunk(m, cc, kp)) = cvt8(lo);
+      }
     }
-    *(uint4*)(lds + u_chunk(m, cc, kp)) = pack8(f);
-    *(uint4*)(lds + lo_off + u_chunk(m, cc, kp)) = pack8(lo);
   }
 }
 
-// Rows without a group: the base alone, 16 tokens per workgroup.
+// Rows without a group: the base alone, a token per wavefront, 8 KiB in flight.
+constexpr int COPY_TOKENS = 4;
 MOE_DEV void copy_ungrouped(const ExpandArgs& p, int b) {
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  for (int i = wv; i < 16; i += 4) {
-    const int tok = b * 16 + i;
-    if (tok >= p.T || p.pos[tok] >= 0) continue;
-    const size_t o = (size_t)tok * p.nout;
-    for (int c = lane * 8; c < p.nout; c += 512)
-      *(uint4*)(p.y + o + c) = p.base ? *(const uint4*)(p.base + o + c) : zero4();
+  const int lane = threadIdx.x & 63, tok = b * COPY_TOKENS + (int)(threadIdx.x >> 6);
+  if (tok >= p.T || p.pos[tok] >= 0) return;
+  const size_t o = (size_t)tok * p.nout;
+#pragma unroll 1
+  for (int c = lane * 8; c < p.nout; c += 8 * 512) {
+    uint4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = p.base && c + i * 512 < p.nout ? *(const uint4*)(p.base + o + c + i * 512) : zero4();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i * 512 < p.nout) *(uint4*)(p.y + o + c + i * 512) = v[i];
   }
 }
 
@@ -602,7 +671,7 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs p) {
           unpack8(bs[m][i], f);
 #pragma unroll
           for (int v = 0; v < 8; ++v) f[v] += acc[m][v][i];
-          *(uint4*)(p.y + rowo[m][i] + c * 128) = pack8(f);
+          *(uint4*)(p.y + rowo[m][i] + c * 128) = cvt8(f);
         }
     }
   }
@@ -633,7 +702,9 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void expand_tile_kernel(Expan
   const bf16_t* W = p.w + (size_t)t.a * p.nout * p.K;
   const int blocks = (p.nout + 128 * SB - 1) / (128 * SB), bper = (blocks + p.osplit - 1) / p.osplit;
   const int s0 = oz * bper, s1 = min(blocks, s0 + bper);
-  uint4 wr[NU][8];
+  // a group's weights: past its K rows (NN) or columns (NT) zeros, without branches
+  const rsrc_t rw = make_rsrc(W, (uint32_t)p.K * (uint32_t)p.nout * 2);
+  u32x4_t wr[NU][8];
   const auto load_w = [&](int sb) {
 #pragma unroll
     for (int n = 0; n < NU; ++n) {
@@ -641,19 +712,15 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void expand_tile_kernel(Expan
         const int unit = wv * NU + n, ks = unit % KS, cb = unit / KS;
         const int col = min((sb * SB + cb) * 128 + 8 * rho, p.nout - 8);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int k = 32 * ks + 8 * g + i;
-          wr[n][i] = k < p.K ? *(const uint4*)(W + (size_t)k * p.nout + col) : zero4();
-        }
+        for (int i = 0; i < 8; ++i)
+          wr[n][i] = __builtin_amdgcn_raw_buffer_load_b128(
+              rw, ((uint32_t)(32 * ks + 8 * g + i) * (uint32_t)p.nout + col) * 2, 0, 0);
       } else {  // the stage's rows of K values lie one after the other: 16-byte pieces in turn
-        const int cpr = p.K >> 3;
+        const uint32_t at = (uint32_t)(sb * SB * 128) * (uint32_t)p.K * 2;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int q = (n * 8 + i) * 256 + (int)threadIdx.x, row = sb * SB * 128 + q / cpr;
-          wr[n][i] = zero4();
-          if (q < SB * 128 * cpr && row < p.nout)
-            wr[n][i] = *(const uint4*)(W + (size_t)sb * SB * 128 * p.K + (size_t)q * 8);
-        }
+        for (int i = 0; i < 8; ++i)
+          wr[n][i] = __builtin_amdgcn_raw_buffer_load_b128(
+              rw, at + ((n * 8 + i) * 256 + threadIdx.x) * 16, 0, 0);
       }
     }
   };
@@ -661,19 +728,22 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void expand_tile_kernel(Expan
 #pragma unroll
     for (int n = 0; n < NU; ++n) {
       if constexpr (NN) {
-        uint4 f[8];
-        transpose8(wr[n], f);
+        uint4 w[8], f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __builtin_bit_cast(uint4, wr[n][i]);
+        transpose8(w, f);
         char* d = st + (wv * NU + n) * 8192 + lane * 16;
 #pragma unroll
         for (int i = 0; i < 8; ++i) *(uint4*)(d + i * 1024) = f[i];
       } else {
-        const int cpr = p.K >> 3;
+        // q / cpr for q < 2048, cpr <= 16: exact, as 2048 / 65536 < 1 / 16
+        const int cpr = p.K >> 3, magic = (65535 + cpr) / cpr;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int q = (n * 8 + i) * 256 + (int)threadIdx.x, row = q / cpr, c = q - row * cpr;
+          const int q = (n * 8 + i) * 256 + (int)threadIdx.x, row = (q * magic) >> 16, c = q - row * cpr;
           if (q < SB * 128 * cpr)  // row 8 rho + f of block cb, chunk 4 ks + g
             *(uint4*)(st + (((row >> 7) * KS + (c >> 2)) * 8 + (row & 7)) * 1024 +
-                      ((c & 3) * 16 + ((row >> 3) & 15)) * 16) = wr[n][i];
+                      ((c & 3) * 16 + ((row >> 3) & 15)) * 16) = __builtin_bit_cast(uint4, wr[n][i]);
         }
       }
     }
@@ -714,9 +784,8 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void expand_tile_kernel(Expan
   __syncthreads();
   for (int sb = s0; sb < s1; ++sb) {
     const char* cur = lds + ((sb - s0) & 1) * STAGE;
-    const bool more = sb + 1 < s1;
-    if (more) load_w(sb + 1);
-#pragma unroll
+    load_w(sb + 1);  // past the last: not stored
+#pragma unroll 1  // short code: a workgroup that runs once pays for every line it fetches
     for (int cb = 0; cb < SB; ++cb) {
       const int c = sb * SB + cb;
       const bool in = c * 128 + 8 * rho < p.nout;
@@ -735,12 +804,19 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void expand_tile_kernel(Expan
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int f = 0; f < 8; ++f) {
-          const bf16x8_t w = as_frag(*(const uint4*)(cur + ((cb * KS + ks) * 8 + f) * 1024 + lane * 16));
+        for (int f4 = 0; f4 < 8; f4 += 4) {
+          bf16x8_t w[4];
 #pragma unroll
-          for (int m = 0; m < MB; ++m) acc[m][f] = mfma16(ul[m][ks], w, acc[m][f]);
+          for (int f = 0; f < 4; ++f)
+            w[f] = as_frag(*(const uint4*)(cur + ((cb * KS + ks) * 8 + f4 + f) * 1024 + lane * 16));
 #pragma unroll
-          for (int m = 0; m < MB; ++m) acc[m][f] = mfma16(uh[m][ks], w, acc[m][f]);
+          for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int m = 0; m < MB; ++m) acc[m][f4 + f] = mfma16(ul[m][ks], w[f], acc[m][f4 + f]);
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int m = 0; m < MB; ++m) acc[m][f4 + f] = mfma16(uh[m][ks], w[f], acc[m][f4 + f]);
         }
 #pragma unroll
       for (int m = 0; m < MB; ++m)
@@ -751,11 +827,11 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void expand_tile_kernel(Expan
 #pragma unroll
           for (int v = 0; v < 8; ++v) f[v] += acc[m][v][i];
           __builtin_amdgcn_raw_buffer_store_b128(
-              __builtin_bit_cast(u32x4_t, pack8(f)), ry,
+              __builtin_bit_cast(u32x4_t, cvt8(f)), ry,
               in && rowo[m][i] != OUT ? rowo[m][i] + (uint32_t)c * 256 : OUT, 0, 0);
         }
     }
-    if (more) store_w(lds + ((sb + 1 - s0) & 1) * STAGE);
+    if (sb + 1 < s1) store_w(lds + ((sb + 1 - s0) & 1) * STAGE);
     __syncthreads();
   }
 }
@@ -776,7 +852,7 @@ struct WgradTile {
   static constexpr int WK = 4 / WJ, JB = JT * WJ;       // 16-row blocks of j
   static constexpr int UB = JB < 2 ? 4096 : JB * 2048;  // bytes of halves a tile
   static constexpr int STAGE = WK * (8192 + UB);        // a tile for each wavefront along K
-  static constexpr int NS = STAGE == 32768 ? 4 : 3;  // 132, 76 or 148 KiB with the tokens
+  static constexpr int NS = 3;  // 76, 52, 76 KiB with the tokens: 2, 3, 2 a CU
   static constexpr int LOADS = WK * (2 + UB / 4096);    // per wavefront and stage
   static constexpr int TOK = 4 * WGRAD_MAX_CHUNK;
   static constexpr int LDS = NS * STAGE + TOK;
@@ -887,16 +963,7 @@ MOE_DEV void wgrad_body(const WgradArgs& p, const WgradSide& d, int hb, int cj, 
   };
   for (int st = 0; st < C::NS - 1 && st < stages; ++st) issue(st);
   for (int st = 0; st < stages; ++st) {
-    constexpr int L = C::LOADS;
-    const int ahead = min(C::NS - 2, stages - 1 - st);
-    // s_waitcnt vmcnt(ahead * L) lgkmcnt(0); vmcnt's high bits are bits 14 and 15
-    constexpr int W1 = (L & 15) | ((L >> 4) << 14) | 0x70;
-    constexpr int W2 = ((2 * L) & 15) | (((2 * L) >> 4) << 14) | 0x70;
-    if (ahead >= 2) __builtin_amdgcn_s_waitcnt(W2);
-    else if (ahead == 1) __builtin_amdgcn_s_waitcnt(W1);
-    else __builtin_amdgcn_s_waitcnt(0x70);
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    ring_wait_for<C::LOADS>(min(C::NS - 2, stages - 1 - st));
     if (st + C::NS - 1 < stages) issue(st + C::NS - 1);
     const char* cur = lds + (st % C::NS) * C::STAGE;
     s16x8_t x[8], u[JT][2];
@@ -949,7 +1016,7 @@ MOE_DEV void wgrad_body(const WgradArgs& p, const WgradSide& d, int hb, int cj, 
         const f32x4v a = acc[j][v];
         const size_t at = (size_t)h * p.J + jj;
         if (nch > 1) *(f32x4v*)(part + at) = a;
-        else *(uint2*)(out + at) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+        else *(uint2*)(out + at) = cvt4(a);
       }
     } else {
       const int jj = (jb0 + wj * JT + j) * 16 + rho;
@@ -966,7 +1033,7 @@ MOE_DEV void wgrad_body(const WgradArgs& p, const WgradSide& d, int hb, int cj, 
           *(float4*)(part + at) = make_float4(f[0], f[1], f[2], f[3]);
           *(float4*)(part + at + 4) = make_float4(f[4], f[5], f[6], f[7]);
         } else {
-          *(uint4*)(out + at) = pack8(f);
+          *(uint4*)(out + at) = cvt8(f);
         }
       }
     }
@@ -1007,7 +1074,7 @@ __global__ __launch_bounds__(256) void wgrad_sum_kernel(WgradArgs p) {
 #pragma unroll 4
   for (int c = 0; c < nch; ++c) v += *(const f32x4v*)(d.parts + (size_t)(first + c) * per + i);
   *(uint2*)(d.out + (size_t)a * per + i) =
-      make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      cvt4(v);
 }
 
 // ------------------------------------------------------------------- transpose
@@ -1051,13 +1118,14 @@ hipError_t dot_small(const char* name, const DotArgs& p, int tiles, hipStream_t 
 template <int BN>
 hipError_t dot_tiles(const char* name, const DotArgs& p, int tiles, hipStream_t s) {
   const unsigned g = (unsigned)((long)tiles * div_up(p.N, BN) * p.S);
-  const unsigned lds = DT_NS * DotTile<BN>::STAGE;
-  if (p.counts) return MOE_LAUNCH(name, s, dot_tile_kernel<BN, true><<<g, 256, lds, s>>>(p));
-  return MOE_LAUNCH(name, s, dot_tile_kernel<BN, false><<<g, 256, lds, s>>>(p));
+  const unsigned lds = DotTile<BN>::NS * DotTile<BN>::STAGE;
+  constexpr int NT = 256 * DotTile<BN>::KG;
+  if (p.counts) return MOE_LAUNCH(name, s, dot_tile_kernel<BN, true><<<g, NT, lds, s>>>(p));
+  return MOE_LAUNCH(name, s, dot_tile_kernel<BN, false><<<g, NT, lds, s>>>(p));
 }
 
 unsigned expand_grid(const ExpandArgs& p) {
-  const long extra = p.counts && p.base != p.y ? div_up(p.T, 16) : 0;
+  const long extra = p.counts && p.base != p.y ? div_up(p.T, COPY_TOKENS) : 0;
   return (unsigned)((long)p.max_tiles * p.osplit + extra);
 }
 
@@ -1109,8 +1177,8 @@ SkinnyPlan skinny_plan(int T, int n, bool grouped, int K, int N) {
   c.tile = T >= 32 * groups;
   c.bn = !c.tile ? (N <= 16 ? 16 : (N <= 32 ? 32 : 64)) : (N <= 32 ? 32 : (N <= 64 ? 64 : 128));
   c.tiles = row_tiles(T, n, grouped, c.tile ? 64 : 16);
-  const int wg = c.tiles * div_up(N, c.bn), blocks = div_up(K, 64);
-  const int most = div_up(blocks, 8);  // 8 blocks of 64: a step of each wavefront, or a full ring
+  const int wg = c.tiles * div_up(N, c.bn);
+  const int most = div_up(K, 512);  // a step of each of 8 wavefronts, or a ring's stages
   const int target = c.tile && c.bn == 128 ? 256 : 512;
   const int want = wg > 0 ? div_up(target, wg) : 1;
   c.S = c.few ? 1 : (want < most ? want : most);
@@ -1154,8 +1222,9 @@ ExpandPlan expand_plan(int T, int n, bool grouped, int K, int nout) {
     c.mb = c.ks == 8 || T >= 128 * groups ? 2 : 1;
     c.tiles = row_tiles(T, n, grouped, 64 * c.mb);
     const int stages = div_up(nout, c.ks >= 4 ? 128 : 512 / c.ks);
-    const int target = c.ks == 8 ? 256 : 512, w = c.tiles > 0 ? div_up(target, c.tiles) : 1;
-    c.osplit = w < stages ? w : stages;
+    // one round of workgroups: 2 a CU, 1 with 8 K steps
+    const int target = c.ks == 8 ? 256 : 512, w = c.tiles > 0 ? target / c.tiles : 1;
+    c.osplit = w < 1 ? 1 : (w < stages ? w : stages);
   }
   return c;
 }
@@ -1191,9 +1260,8 @@ hipError_t launch_wgrad(const char* name, WgradArgs p, int sides, hipStream_t s)
                             wgrad_kernel<JT, WJ, true><<<g, 256, WgradTile<JT, WJ>::LDS, s>>>(p)) \
                : MOE_LAUNCH(name, s,                                                             \
                             wgrad_kernel<JT, WJ, false><<<g, 256, WgradTile<JT, WJ>::LDS, s>>>(p))
-  if (p.J <= 16) MOE_WGRAD_GO(1, 1);
-  else if (p.J <= 32) MOE_WGRAD_GO(2, 1);
-  else if (p.J <= 64) MOE_WGRAD_GO(2, 2);
+  if (p.J <= 32) MOE_WGRAD_GO(1, 2);
+  else if (p.J <= 64) MOE_WGRAD_GO(1, 4);
   else MOE_WGRAD_GO(2, 4);
 #undef MOE_WGRAD_GO
   if (e != hipSuccess || p.T <= p.chunk_rows) return e;
