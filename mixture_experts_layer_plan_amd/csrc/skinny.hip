@@ -684,10 +684,10 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs p) {
 // where it is needed: reading it a block ahead, between the stores, took the plain copy of
 // this pattern from 48 us (8192 x 7168) to 73, and to 90 four blocks ahead.
 template <int MB, int KS, bool NN, bool GR>
-__global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void expand_tile_kernel(ExpandArgs p) {
+__global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(ExpandArgs p) {
   constexpr int SB = KS >= 4 ? 1 : 4 / KS;  // column blocks of a stage
-  constexpr int NU = SB * KS / 4;           // fragment groups (8 KiB) a wavefront brings
-  constexpr int STAGE = SB * KS * 8192;
+  constexpr int KC = KS > 4 ? 4 : KS;       // K steps of a stage
+  constexpr int STAGE = SB * KC * 8192;     // 32 KiB: a fragment group (8 KiB) a wavefront
   constexpr int ROWS = 64 * MB, KP = 32 * KS;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -704,47 +704,40 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void expand_tile_kernel(Expan
   const int s0 = oz * bper, s1 = min(blocks, s0 + bper);
   // a group's weights: past its K rows (NN) or columns (NT) zeros, without branches
   const rsrc_t rw = make_rsrc(W, (uint32_t)p.K * (uint32_t)p.nout * 2);
-  u32x4_t wr[NU][8];
-  const auto load_w = [&](int sb) {
+  u32x4_t wr[8];
+  const auto load_w = [&](int sb, int half) {
+    if constexpr (NN) {  // K step ks of column block cb
+      const int ks = wv % KC + half * KC, cb = wv / KC;
+      const int col = min((sb * SB + cb) * 128 + 8 * rho, p.nout - 8);
 #pragma unroll
-    for (int n = 0; n < NU; ++n) {
-      if constexpr (NN) {  // unit: K step ks of column block cb
-        const int unit = wv * NU + n, ks = unit % KS, cb = unit / KS;
-        const int col = min((sb * SB + cb) * 128 + 8 * rho, p.nout - 8);
+      for (int i = 0; i < 8; ++i)
+        wr[i] = __builtin_amdgcn_raw_buffer_load_b128(
+            rw, ((uint32_t)(32 * ks + 8 * g + i) * (uint32_t)p.nout + col) * 2, 0, 0);
+    } else {  // the stage's rows of K values lie one after the other: 16-byte pieces in turn
+      const uint32_t at = (uint32_t)(sb * SB * 128) * (uint32_t)p.K * 2;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          wr[n][i] = __builtin_amdgcn_raw_buffer_load_b128(
-              rw, ((uint32_t)(32 * ks + 8 * g + i) * (uint32_t)p.nout + col) * 2, 0, 0);
-      } else {  // the stage's rows of K values lie one after the other: 16-byte pieces in turn
-        const uint32_t at = (uint32_t)(sb * SB * 128) * (uint32_t)p.K * 2;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          wr[n][i] = __builtin_amdgcn_raw_buffer_load_b128(
-              rw, at + ((n * 8 + i) * 256 + threadIdx.x) * 16, 0, 0);
-      }
+      for (int i = 0; i < 8; ++i)
+        wr[i] = __builtin_amdgcn_raw_buffer_load_b128(rw, at + (i * 256 + threadIdx.x) * 16, 0, 0);
     }
   };
   const auto store_w = [&](char* st) {
+    if constexpr (NN) {
+      uint4 w[8], f[8];
 #pragma unroll
-    for (int n = 0; n < NU; ++n) {
-      if constexpr (NN) {
-        uint4 w[8], f[8];
+      for (int i = 0; i < 8; ++i) w[i] = __builtin_bit_cast(uint4, wr[i]);
+      transpose8(w, f);
+      char* d = st + wv * 8192 + lane * 16;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __builtin_bit_cast(uint4, wr[n][i]);
-        transpose8(w, f);
-        char* d = st + (wv * NU + n) * 8192 + lane * 16;
+      for (int i = 0; i < 8; ++i) *(uint4*)(d + i * 1024) = f[i];
+    } else {
+      // q / cpr for q < 2048, cpr <= 16: exact, as 2048 / 65536 < 1 / 16
+      const int cpr = p.K >> 3, magic = (65535 + cpr) / cpr;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) *(uint4*)(d + i * 1024) = f[i];
-      } else {
-        // q / cpr for q < 2048, cpr <= 16: exact, as 2048 / 65536 < 1 / 16
-        const int cpr = p.K >> 3, magic = (65535 + cpr) / cpr;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int q = (n * 8 + i) * 256 + (int)threadIdx.x, row = (q * magic) >> 16, c = q - row * cpr;
-          if (q < SB * 128 * cpr)  // row 8 rho + f of block cb, chunk 4 ks + g
-            *(uint4*)(st + (((row >> 7) * KS + (c >> 2)) * 8 + (row & 7)) * 1024 +
-                      ((c & 3) * 16 + ((row >> 3) & 15)) * 16) = __builtin_bit_cast(uint4, wr[n][i]);
-        }
+      for (int i = 0; i < 8; ++i) {
+        const int q = i * 256 + (int)threadIdx.x, row = (q * magic) >> 16, c = q - row * cpr;
+        if (q < SB * 128 * cpr)  // row 8 rho + f of block cb, chunk 4 ks + g
+          *(uint4*)(st + (((row >> 7) * KS + (c >> 2)) * 8 + (row & 7)) * 1024 +
+                    ((c & 3) * 16 + ((row >> 3) & 15)) * 16) = __builtin_bit_cast(uint4, wr[i]);
       }
     }
   };
@@ -762,7 +755,7 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void expand_tile_kernel(Expan
       const uint32_t o = (uint32_t)(GR ? p.src_token[row] : row) * (uint32_t)p.nout * 2;
       rowo[m][i] = r < t.rows ? o + 16 * rho : OUT;
     }
-  if (s0 < s1) load_w(s0);
+  if (s0 < s1) load_w(s0, 0);
   fill_u<ROWS>(p, t, KP, lds);
   __syncthreads();
   if (p.ut && oz == 0) store_halves<4 * MB>(lds, ROWS * KP * 2, KP, p.K, t, p.ut);
@@ -783,8 +776,6 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void expand_tile_kernel(Expan
   if (s0 < s1) store_w(lds);
   __syncthreads();
   for (int sb = s0; sb < s1; ++sb) {
-    const char* cur = lds + ((sb - s0) & 1) * STAGE;
-    load_w(sb + 1);  // past the last: not stored
 #pragma unroll 1  // short code: a workgroup that runs once pays for every line it fetches
     for (int cb = 0; cb < SB; ++cb) {
       const int c = sb * SB + cb;
@@ -802,22 +793,34 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void expand_tile_kernel(Expan
 #pragma unroll
         for (int f = 0; f < 8; ++f) acc[m][f] = (f32x4v){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
+      for (int half = 0; half < KS / KC; ++half) {
+        const int st = (sb - s0) * (KS / KC) + half;
+        const char* cur = lds + (st & 1) * STAGE;
+        const bool last_half = half + 1 == KS / KC;
+        if (cb == 0) load_w(last_half ? sb + 1 : sb, last_half ? 0 : half + 1);
 #pragma unroll
-        for (int f4 = 0; f4 < 8; f4 += 4) {
-          bf16x8_t w[4];
+        for (int kc = 0; kc < KC; ++kc)
 #pragma unroll
-          for (int f = 0; f < 4; ++f)
-            w[f] = as_frag(*(const uint4*)(cur + ((cb * KS + ks) * 8 + f4 + f) * 1024 + lane * 16));
+          for (int f4 = 0; f4 < 8; f4 += 4) {
+            const int ks = half * KC + kc;
+            bf16x8_t w[4];
 #pragma unroll
-          for (int f = 0; f < 4; ++f)
+            for (int f = 0; f < 4; ++f)
+              w[f] = as_frag(*(const uint4*)(cur + ((cb * KC + kc) * 8 + f4 + f) * 1024 + lane * 16));
 #pragma unroll
-            for (int m = 0; m < MB; ++m) acc[m][f4 + f] = mfma16(ul[m][ks], w[f], acc[m][f4 + f]);
+            for (int f = 0; f < 4; ++f)
 #pragma unroll
-          for (int f = 0; f < 4; ++f)
+              for (int m = 0; m < MB; ++m) acc[m][f4 + f] = mfma16(ul[m][ks], w[f], acc[m][f4 + f]);
 #pragma unroll
-            for (int m = 0; m < MB; ++m) acc[m][f4 + f] = mfma16(uh[m][ks], w[f], acc[m][f4 + f]);
+            for (int f = 0; f < 4; ++f)
+#pragma unroll
+              for (int m = 0; m < MB; ++m) acc[m][f4 + f] = mfma16(uh[m][ks], w[f], acc[m][f4 + f]);
+          }
+        if (!last_half) {  // SB is 1 here
+          store_w(lds + ((st + 1) & 1) * STAGE);
+          __syncthreads();
         }
+      }
 #pragma unroll
       for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -831,7 +834,8 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void expand_tile_kernel(Expan
               in && rowo[m][i] != OUT ? rowo[m][i] + (uint32_t)c * 256 : OUT, 0, 0);
         }
     }
-    if (sb + 1 < s1) store_w(lds + ((sb + 1 - s0) & 1) * STAGE);
+    // the next stage's weights (past the last: not used)
+    store_w(lds + ((sb + 1 - s0) * (KS / KC) & 1) * STAGE);
     __syncthreads();
   }
 }
@@ -917,7 +921,12 @@ MOE_DEV void wgrad_body(const WgradArgs& p, const WgradSide& d, int hb, int cj, 
   const int row0 = gp.row0 + r0;
   char* tok = lds + C::NS * C::STAGE;  // the chunk's tokens
   if (GR) {
-    for (int i = threadIdx.x; i < rows; i += 256) ((int32_t*)tok)[i] = p.src_token[row0 + i];
+    int32_t v[WGRAD_MAX_CHUNK / 256];
+#pragma unroll
+    for (int q = 0; q < WGRAD_MAX_CHUNK / 256; ++q)
+      v[q] = p.src_token[row0 + min((int)threadIdx.x + 256 * q, max(rows - 1, 0))];
+#pragma unroll
+    for (int q = 0; q < WGRAD_MAX_CHUNK / 256; ++q) ((int32_t*)tok)[threadIdx.x + 256 * q] = v[q];
     __syncthreads();
   }
   const int g = lane >> 4, rho = lane & 15;
@@ -945,7 +954,7 @@ MOE_DEV void wgrad_body(const WgradArgs& p, const WgradSide& d, int hb, int cj, 
         const int m = 32 * tt + 4 * (2 * wv + q) + g;
         uint32_t off = OUT;
         if (GR) {
-          const int tk = lds_read_int(lds_at(tok) + 4 * min(m, crows - 1));
+          const int tk = lds_read_int(lds_at(tok) + 4 * min(m, WGRAD_MAX_CHUNK - 1));
           if (m < rows && cin) off = ((uint32_t)tk * (uint32_t)d.H + h0 + 8 * rho) * 2;
         } else {
           if (m < rows && cin) off = ((uint32_t)(row0 + m) * (uint32_t)d.H + h0 + 8 * rho) * 2;
@@ -1138,7 +1147,7 @@ hipError_t expand_small(const char* name, const ExpandArgs& p, hipStream_t s) {
 
 template <int MB, int KS, bool NN, bool GR>
 hipError_t expand_tiles(const char* name, const ExpandArgs& p, hipStream_t s) {
-  const unsigned w = 2u * (KS >= 4 ? KS : 4) * 8192, u = 64u * MB * 32 * KS * 4;
+  const unsigned w = 2u * 32768, u = 64u * MB * 32 * KS * 4;
   auto* k = expand_tile_kernel<MB, KS, NN, GR>;
   return MOE_LAUNCH(name, s, k<<<expand_grid(p), 256, w > u ? w : u, s>>>(p));
 }
@@ -1151,7 +1160,7 @@ hipError_t expand_ks(const char* name, const ExpandArgs& p, const ExpandPlan& c,
     return expand_small<1, NN, GR>(name, p, s);
   }
   if (c.ks == 8) {
-    if constexpr (!GR) return expand_tiles<2, 8, NN, GR>(name, p, s);  // rank <= 128
+    if constexpr (!GR) return expand_tiles<1, 8, NN, GR>(name, p, s);  // rank <= 128
     return hipErrorNotSupported;
   }
   if (c.mb == 1) {
@@ -1219,11 +1228,10 @@ ExpandPlan expand_plan(int T, int n, bool grouped, int K, int nout) {
     c.osplit = w < most ? w : most;
   } else {
     c.ks = K <= 32 ? 1 : (K <= 64 ? 2 : (K <= 128 ? 4 : 8));
-    c.mb = c.ks == 8 || T >= 128 * groups ? 2 : 1;
+    c.mb = c.ks < 8 && T >= 128 * groups ? 2 : 1;
     c.tiles = row_tiles(T, n, grouped, 64 * c.mb);
     const int stages = div_up(nout, c.ks >= 4 ? 128 : 512 / c.ks);
-    // one round of workgroups: 2 a CU, 1 with 8 K steps
-    const int target = c.ks == 8 ? 256 : 512, w = c.tiles > 0 ? target / c.tiles : 1;
+    const int w = c.tiles > 0 ? 512 / c.tiles : 1;  // one round of workgroups, 2 a CU
     c.osplit = w < 1 ? 1 : (w < stages ? w : stages);
   }
   return c;
