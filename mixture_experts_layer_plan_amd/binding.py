@@ -8,6 +8,7 @@ raises ``MoeLibraryMissing``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -393,39 +394,63 @@ def lora_shape(T, H_in, H_out, n_adapters, rank) -> moe_lora_shape:
     return moe_lora_shape(int(T), int(H_in), int(H_out), int(n_adapters), int(rank))
 
 
-def _here(*tensors):
-    """The launches go to the current device: a tensor of another one is refused."""
-    cur = None
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and t.is_cuda:
-            cur = torch.cuda.current_device() if cur is None else cur
-            if t.device.index != cur:
-                raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+def _here(t, dtype, numel, dev):
+    """Device pointer of a contiguous tensor of the current device ``dev`` (None -> NULL).
+    The launches go to the current device, so a tensor of another one is refused, as are
+    another type or size (a call of a few microseconds: one pass of cheap checks)."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"expected a tensor on cuda:{dev}, the current device, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"expected a {dtype} tensor, got {t.dtype}")
+    if t.numel() != numel:
+        raise ValueError(f"expected {numel} elements, got {t.numel()}")
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
 
 
-def _ws(t):
-    return _ptr(t), 0 if t is None else t.numel() * t.element_size()
-
-
-def _at_least(t, nbytes):
-    """Pointer of a buffer the library lays out itself, which may be larger than asked."""
-    if isinstance(t, torch.Tensor) and t.numel() * t.element_size() < nbytes:
+def _buf(t, nbytes, dev):
+    """Pointer of a buffer the library lays out itself, of at least ``nbytes``."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"expected a tensor on cuda:{dev}, the current device, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    if t.numel() * t.element_size() < nbytes:
         raise ValueError(f"buffer of {t.numel() * t.element_size()} bytes, {nbytes} needed")
-    return _ptr(t)
+    return t.data_ptr()
+
+
+def _ws(t, dev):
+    return _buf(t, 0, dev), 0 if t is None else t.numel() * t.element_size()
+
+
+def _dev():
+    return torch.cuda.current_device()
+
+
+@functools.lru_cache(maxsize=256)
+def _lora_bytes(T, H_in, H_out, n, r):
+    """(plan, saved) bytes of a lora shape"""
+    s = lora_shape(T, H_in, H_out, n, r)
+    return moe_lora_plan_bytes(s), moe_lora_saved_bytes(s)
 
 
 def moe_route_scored(s, sc, logits, bias, topk_idx, topk_w, stream=None):
-    _here(logits, bias, topk_idx, topk_w)
-    _call("moe_route_scored", ctypes.byref(s), ctypes.byref(sc), _f32(logits, s.T * s.E),
-          _f32(bias, s.E), _ptr(topk_idx, torch.int32, s.T * s.k), _f32(topk_w, s.T * s.k),
-          _stream(stream))
+    T, E, k, d = s.T, s.E, s.k, _dev()
+    _call("moe_route_scored", ctypes.byref(s), ctypes.byref(sc), _here(logits, _F32, T * E, d),
+          _here(bias, _F32, E, d), _here(topk_idx, torch.int32, T * k, d),
+          _here(topk_w, _F32, T * k, d), _stream(stream))
 
 
 def moe_route_scored_backward(s, sc, logits, topk_idx, d_topk_w, d_logits, stream=None):
-    _here(logits, topk_idx, d_topk_w, d_logits)
+    T, E, k, d = s.T, s.E, s.k, _dev()
     _call("moe_route_scored_backward", ctypes.byref(s), ctypes.byref(sc),
-          _f32(logits, s.T * s.E), _ptr(topk_idx, torch.int32, s.T * s.k),
-          _f32(d_topk_w, s.T * s.k), _f32(d_logits, s.T * s.E), _stream(stream))
+          _here(logits, _F32, T * E, d), _here(topk_idx, torch.int32, T * k, d),
+          _here(d_topk_w, _F32, T * k, d), _here(d_logits, _F32, T * E, d), _stream(stream))
 
 
 def moe_router_workspace_bytes(s: moe_shape, backward: bool) -> int:
@@ -433,17 +458,18 @@ def moe_router_workspace_bytes(s: moe_shape, backward: bool) -> int:
 
 
 def moe_router_logits_bf16(s, x, w_router, logits, ws, stream=None):
-    _here(x, w_router, logits, ws)
-    _call("moe_router_logits_bf16", ctypes.byref(s), _bf16(x, s.T * s.H),
-          _bf16(w_router, s.E * s.H), _f32(logits, s.T * s.E), *_ws(ws), _stream(stream))
+    T, H, E, d = s.T, s.H, s.E, _dev()
+    _call("moe_router_logits_bf16", ctypes.byref(s), _here(x, _BF16, T * H, d),
+          _here(w_router, _BF16, E * H, d), _here(logits, _F32, T * E, d), *_ws(ws, d),
+          _stream(stream))
 
 
 def moe_router_backward_bf16(s, x, w_router, d_logits, dx_in, dw_router, dx, ws, stream=None):
-    _here(x, w_router, d_logits, dx_in, dw_router, dx, ws)
-    nt, nw = s.T * s.H, s.E * s.H
-    _call("moe_router_backward_bf16", ctypes.byref(s), _bf16(x, nt), _bf16(w_router, nw),
-          _f32(d_logits, s.T * s.E), _bf16(dx_in, nt), _bf16(dw_router, nw), _bf16(dx, nt),
-          *_ws(ws), _stream(stream))
+    T, H, E, d = s.T, s.H, s.E, _dev()
+    _call("moe_router_backward_bf16", ctypes.byref(s), _here(x, _BF16, T * H, d),
+          _here(w_router, _BF16, E * H, d), _here(d_logits, _F32, T * E, d),
+          _here(dx_in, _BF16, T * H, d), _here(dw_router, _BF16, E * H, d),
+          _here(dx, _BF16, T * H, d), *_ws(ws, d), _stream(stream))
 
 
 def moe_lora_plan_bytes(s: moe_lora_shape) -> int:
@@ -459,30 +485,30 @@ def moe_lora_workspace_bytes(s: moe_lora_shape, backward: bool) -> int:
 
 
 def moe_lora_plan(s, adapter_idx, plan, stream=None):
-    _here(adapter_idx, plan)
-    _call("moe_lora_plan", ctypes.byref(s), _ptr(adapter_idx, torch.int32, s.T),
-          _at_least(plan, moe_lora_plan_bytes(s)), _stream(stream))
+    d = _dev()
+    _call("moe_lora_plan", ctypes.byref(s), _here(adapter_idx, torch.int32, s.T, d),
+          _buf(plan, moe_lora_plan_bytes(s), d), _stream(stream))
 
 
 def moe_lora_bf16(s, plan, x, lora_a, lora_b, scale, base, y, saved, ws, stream=None):
-    _here(plan, x, lora_a, lora_b, scale, base, y, saved, ws)
-    n, r = s.n_adapters, s.rank
-    _call("moe_lora_bf16", ctypes.byref(s), _at_least(plan, moe_lora_plan_bytes(s)),
-          _bf16(x, s.T * s.H_in), _bf16(lora_a, n * r * s.H_in), _bf16(lora_b, n * r * s.H_out),
-          _f32(scale, n), _bf16(base, s.T * s.H_out), _bf16(y, s.T * s.H_out),
-          _at_least(saved, moe_lora_saved_bytes(s)), *_ws(ws), _stream(stream))
+    T, hi, ho, n, r, d = s.T, s.H_in, s.H_out, s.n_adapters, s.rank, _dev()
+    pb, sb = _lora_bytes(T, hi, ho, n, r)
+    _call("moe_lora_bf16", ctypes.byref(s), _buf(plan, pb, d), _here(x, _BF16, T * hi, d),
+          _here(lora_a, _BF16, n * r * hi, d), _here(lora_b, _BF16, n * r * ho, d),
+          _here(scale, _F32, n, d), _here(base, _BF16, T * ho, d), _here(y, _BF16, T * ho, d),
+          _buf(saved, sb, d), *_ws(ws, d), _stream(stream))
 
 
 def moe_lora_backward_bf16(s, plan, x, lora_a, lora_b, scale, saved, dy, dx_in, dx, d_lora_a,
                            d_lora_b, ws, stream=None):
-    _here(plan, x, lora_a, lora_b, scale, saved, dy, dx_in, dx, d_lora_a, d_lora_b, ws)
-    n, r = s.n_adapters, s.rank
-    na, nb = n * r * s.H_in, n * r * s.H_out
-    _call("moe_lora_backward_bf16", ctypes.byref(s), _at_least(plan, moe_lora_plan_bytes(s)),
-          _bf16(x, s.T * s.H_in), _bf16(lora_a, na), _bf16(lora_b, nb), _f32(scale, n),
-          _at_least(saved, moe_lora_saved_bytes(s)), _bf16(dy, s.T * s.H_out),
-          _bf16(dx_in, s.T * s.H_in), _bf16(dx, s.T * s.H_in), _bf16(d_lora_a, na),
-          _bf16(d_lora_b, nb), *_ws(ws), _stream(stream))
+    T, hi, ho, n, r, d = s.T, s.H_in, s.H_out, s.n_adapters, s.rank, _dev()
+    pb, sb = _lora_bytes(T, hi, ho, n, r)
+    na, nb = n * r * hi, n * r * ho
+    _call("moe_lora_backward_bf16", ctypes.byref(s), _buf(plan, pb, d), _here(x, _BF16, T * hi, d),
+          _here(lora_a, _BF16, na, d), _here(lora_b, _BF16, nb, d), _here(scale, _F32, n, d),
+          _buf(saved, sb, d), _here(dy, _BF16, T * ho, d), _here(dx_in, _BF16, T * hi, d),
+          _here(dx, _BF16, T * hi, d), _here(d_lora_a, _BF16, na, d),
+          _here(d_lora_b, _BF16, nb, d), *_ws(ws, d), _stream(stream))
 
 
 # ------------------------------------------------------------ kernel timing

@@ -936,7 +936,8 @@ moe_status check_scoring(const moe_shape* s, const moe_scoring* sc) {
 }
 
 ScoreArgs score_args(const moe_scoring* sc) {
-  return {sc->score, sc->n_groups, sc->topk_groups, sc->group_top, sc->renormalise, sc->scale};
+  return {sc->score, sc->n_groups, sc->topk_groups, sc->group_top, sc->renormalise, sc->scale,
+          0};
 }
 
 // router forward: the K parts of the logits; backward: the halves of d_logits along the

@@ -45,6 +45,7 @@ hipError_t launch_router_backward_f32(const float* x, const float* wr, const flo
 struct ScoreArgs {
   int score, n_groups, topk_groups, group_top, renormalise;
   float scale;
+  int lanes;  // set by the launch
 };
 hipError_t launch_route_scored(const float* logits, const float* bias, int T, int E, int k,
                                const ScoreArgs& sc, int32_t* idx, float* w, hipStream_t s);
