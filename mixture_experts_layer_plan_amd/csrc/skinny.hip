@@ -13,6 +13,8 @@
 // two bf16 halves (hi = round(v), lo = round(v - hi): 16 bits of the 24-bit mantissa, an
 // error of 2^-17 against the 2^-9 of the bf16 result), so that it costs two matrix
 // instructions and no accuracy.
+#include <type_traits>
+
 #include "gemm_common.hpp"
 #include "skinny.hpp"
 
@@ -471,18 +473,19 @@ MOE_DEV void store_halves(const char* lds, int lo_off, int kp, int K, const Skin
 
 // u of a row tile into LDS: its S parts summed, scaled and split, zeros past K and past
 // the tile's rows; kp = K rounded up to 32.
-template <int ROWS>
+// Q pieces of 8 and U parts are in flight at a time.
+template <int ROWS, int Q, int U>
 MOE_DEV void fill_u(const ExpandArgs& p, const SkinnyTile& t, int kp, char* lds) {
   const float sc = p.scale ? p.scale[t.a] : 1.0f;
   const int ch = kp / 8, lo_off = ROWS * kp * 2, items = ROWS * ch;
   const size_t part = p.R * p.K;
 #pragma unroll 1
-  for (int i0 = threadIdx.x; i0 < items; i0 += 4 * 256) {  // four pieces of 8 in flight
-    float f[4][8];
-    const float* u[4];
-    bool in[4];
+  for (int i0 = threadIdx.x; i0 < items; i0 += Q * 256) {
+    float f[Q][8];
+    const float* u[Q];
+    bool in[Q];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < Q; ++q) {
       const int i = min(i0 + q * 256, items - 1), m = i / ch, cc = i - m * ch;
       in[q] = m < t.rows && 8 * cc < p.K;
       u[q] = p.u + ((size_t)t.row0 + (in[q] ? m : 0)) * p.K + (in[q] ? 8 * cc : 0);
@@ -490,23 +493,30 @@ MOE_DEV void fill_u(const ExpandArgs& p, const SkinnyTile& t, int kp, char* lds)
       for (int v = 0; v < 8; ++v) f[q][v] = 0.0f;
     }
     if ((p.K & 7) == 0) {
-#pragma unroll 2
-      for (int s = 0; s < p.S; ++s) {
-        float4 a[4], b[4];
+#pragma unroll 1
+      for (int s = 0; s < p.S; s += U) {
+        float4 a[U][Q], b[U][Q];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          a[q] = *(const float4*)(u[q] + s * part);
-          b[q] = *(const float4*)(u[q] + s * part + 4);
-        }
+        for (int w = 0; w < U; ++w)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          f[q][0] += a[q].x; f[q][1] += a[q].y; f[q][2] += a[q].z; f[q][3] += a[q].w;
-          f[q][4] += b[q].x; f[q][5] += b[q].y; f[q][6] += b[q].z; f[q][7] += b[q].w;
+          for (int q = 0; q < Q; ++q) {  // parts past the last repeat it and are not added
+            const float* x = u[q] + min(s + w, p.S - 1) * part;
+            a[w][q] = *(const float4*)x;
+            b[w][q] = *(const float4*)(x + 4);
+          }
+#pragma unroll
+        for (int w = 0; w < U; ++w) {
+          if (w && s + w >= p.S) break;
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            f[q][0] += a[w][q].x; f[q][1] += a[w][q].y; f[q][2] += a[w][q].z; f[q][3] += a[w][q].w;
+            f[q][4] += b[w][q].x; f[q][5] += b[w][q].y; f[q][6] += b[w][q].z; f[q][7] += b[w][q].w;
+          }
         }
       }
     } else {  // the router's dL: one part, rows of any length
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < Q; ++q) {
         const int i = min(i0 + q * 256, items - 1), left = p.K - 8 * (i % ch);
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
@@ -516,7 +526,7 @@ MOE_DEV void fill_u(const ExpandArgs& p, const SkinnyTile& t, int kp, char* lds)
       }
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < Q; ++q) {
       const int i = i0 + q * 256, m = i / ch, cc = i - m * ch;
       float hi[8], lo[8];
 #pragma unroll
@@ -613,7 +623,7 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs p) {
     load_base(c, bs);  // later blocks': at their start, after the stores before them
   }
   bool first = true;
-  fill_u<16 * MB>(p, t, kp, lds);
+  fill_u<16 * MB, GR ? 1 : 2, GR ? 8 : 1>(p, t, kp, lds);
   __syncthreads();
   if (p.ut && oz == 0) store_halves<MB>(lds, lo_off, kp, p.K, t, p.ut);
   for (; c < c1; c += 4) {
@@ -746,17 +756,38 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
   constexpr uint32_t OUT = 0xffffffffu;
   const uint32_t nbytes = (uint32_t)p.T * (uint32_t)p.nout * 2;  // below 4 GiB
   const rsrc_t rb = make_rsrc(p.base, p.base ? nbytes : 0), ry = make_rsrc(p.y, nbytes);
+  // what only the tile decides goes out first: weights, tokens, u
+  if (s0 < s1) load_w(s0, 0);
   uint32_t rowo[MB][4];
 #pragma unroll
   for (int m = 0; m < MB; ++m)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = 16 * (MB * wv + m) + 4 * g + i, row = t.row0 + min(r, t.rows - 1);
-      const uint32_t o = (uint32_t)(GR ? p.src_token[row] : row) * (uint32_t)p.nout * 2;
-      rowo[m][i] = r < t.rows ? o + 16 * rho : OUT;
+      const int row = t.row0 + min(16 * (MB * wv + m) + 4 * g + i, t.rows - 1);
+      rowo[m][i] = (uint32_t)(GR ? p.src_token[row] : row);
     }
-  if (s0 < s1) load_w(s0, 0);
-  fill_u<ROWS>(p, t, KP, lds);
+  constexpr int Q = ROWS * KP / 2048 < 4 ? ROWS * KP / 2048 : 4;
+  fill_u<ROWS, Q, GR ? 8 / Q : 1>(p, t, KP, lds);
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      rowo[m][i] = 16 * (MB * wv + m) + 4 * g + i < t.rows
+                       ? (rowo[m][i] * (uint32_t)p.nout + 8 * rho) * 2 : OUT;
+  // base is read a block ahead where that fits the registers (small K: few blocks a
+  // workgroup, each of which would wait for its own)
+  constexpr bool AHEAD = MB * KS <= 2;
+  u32x4_t bs[MB][4], bn[MB][4];
+  const auto load_base = [&](int c, u32x4_t (&b)[MB][4]) {
+    const bool in = c < s1 * SB && c * 128 + 8 * rho < p.nout;
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        b[m][i] = __builtin_amdgcn_raw_buffer_load_b128(
+            rb, in && rowo[m][i] != OUT ? rowo[m][i] + (uint32_t)c * 256 : OUT, 0, 0);
+  };
+  if (AHEAD) load_base(s0 * SB, bs);
   __syncthreads();
   if (p.ut && oz == 0) store_halves<4 * MB>(lds, ROWS * KP * 2, KP, p.K, t, p.ut);
   bf16x8_t uh[MB][KS], ul[MB][KS];
@@ -780,13 +811,8 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
     for (int cb = 0; cb < SB; ++cb) {
       const int c = sb * SB + cb;
       const bool in = c * 128 + 8 * rho < p.nout;
-      u32x4_t bs[MB][4];
-#pragma unroll
-      for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          bs[m][i] = __builtin_amdgcn_raw_buffer_load_b128(
-              rb, in && rowo[m][i] != OUT ? rowo[m][i] + (uint32_t)c * 256 : OUT, 0, 0);
+      if constexpr (AHEAD) load_base(c + 1, bn);
+      else load_base(c, bs);
       f32x4v acc[MB][8];
 #pragma unroll
       for (int m = 0; m < MB; ++m)
@@ -829,10 +855,25 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
           unpack8(__builtin_bit_cast(uint4, bs[m][i]), f);
 #pragma unroll
           for (int v = 0; v < 8; ++v) f[v] += acc[m][v][i];
-          __builtin_amdgcn_raw_buffer_store_b128(
-              __builtin_bit_cast(u32x4_t, cvt8(f)), ry,
-              in && rowo[m][i] != OUT ? rowo[m][i] + (uint32_t)c * 256 : OUT, 0, 0);
+          bs[m][i] = __builtin_bit_cast(u32x4_t, cvt8(f));
         }
+      const auto put = [&](auto aux) {
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            __builtin_amdgcn_raw_buffer_store_b128(
+                bs[m][i], ry, in && rowo[m][i] != OUT ? rowo[m][i] + (uint32_t)c * 256 : OUT, 0,
+                decltype(aux)::value);
+      };
+      if (p.stream) put(std::integral_constant<int, 2>{});  // non-temporal
+      else put(std::integral_constant<int, 0>{});
+      if constexpr (AHEAD) {
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) bs[m][i] = bn[m][i];
+      }
     }
     // the next stage's weights (past the last: not used)
     store_w(lds + ((sb + 1 - s0) * (KS / KC) & 1) * STAGE);
@@ -1145,6 +1186,13 @@ hipError_t expand_small(const char* name, const ExpandArgs& p, hipStream_t s) {
   return MOE_LAUNCH(name, s, k<<<expand_grid(p), 256, lds, s>>>(p));
 }
 
+// Outputs of this size and more leave with non-temporal stores: the Infinity Cache (256 MB)
+// would hold them dirty and write them back under the kernels that follow.
+#ifndef STREAM_MB
+#define STREAM_MB 32
+#endif
+constexpr size_t STREAM_BYTES = (size_t)STREAM_MB << 20;
+
 template <int MB, int KS, bool NN, bool GR>
 hipError_t expand_tiles(const char* name, const ExpandArgs& p, hipStream_t s) {
   const unsigned w = 2u * 32768, u = 64u * MB * 32 * KS * 4;
@@ -1187,9 +1235,11 @@ SkinnyPlan skinny_plan(int T, int n, bool grouped, int K, int N) {
   c.bn = !c.tile ? (N <= 16 ? 16 : (N <= 32 ? 32 : 64)) : (N <= 32 ? 32 : (N <= 64 ? 64 : 128));
   c.tiles = row_tiles(T, n, grouped, c.tile ? 64 : 16);
   const int wg = c.tiles * div_up(N, c.bn);
-  const int most = div_up(K, 512);  // a step of each of 8 wavefronts, or a ring's stages
+  // at least two steps of each of 8 wavefronts, or a ring's stages
+  const int most = div_up(K, c.tile ? 512 : 1024);
   const int target = c.tile && c.bn == 128 ? 256 : 512;
-  const int want = wg > 0 ? div_up(target, wg) : 1;
+  int want = wg > 0 ? div_up(target, wg) : 1;
+  if (want > 8) want = 8;  // every part is read again by the second product
   c.S = c.few ? 1 : (want < most ? want : most);
   return c;
 }
@@ -1237,9 +1287,10 @@ ExpandPlan expand_plan(int T, int n, bool grouped, int K, int nout) {
   return c;
 }
 
-hipError_t launch_expand(const char* name, const ExpandArgs& p, const ExpandPlan& c, bool nn,
+hipError_t launch_expand(const char* name, ExpandArgs p, const ExpandPlan& c, bool nn,
                          hipStream_t s) {
   if (p.T == 0) return hipSuccess;
+  p.stream = (size_t)p.T * p.nout * 2 >= STREAM_BYTES;
   if (!p.counts) return expand_ks<true, false>(name, p, c, s);
   return nn ? expand_ks<true, true>(name, p, c, s) : expand_ks<false, true>(name, p, c, s);
 }

@@ -32,6 +32,7 @@ struct ExpandArgs {
   const int32_t* src_token;
   const int32_t* pos;  // row of each token, < 0: none (its y is its base)
   int n, T, K, S, nout, max_tiles, osplit;
+  int stream;  // set by launch_expand
   size_t R;
 };
 // bytes of the halves of `rows` rows in n groups, K values each
@@ -76,7 +77,7 @@ int wgrad_chunk_slots(int T, int n, bool grouped, int chunk_rows);
 hipError_t launch_dot(const char* name, const DotArgs& p, const SkinnyPlan& c, hipStream_t s);
 hipError_t launch_sum_parts(const char* name, const float* parts, int S, size_t n, float* out,
                             hipStream_t s);
-hipError_t launch_expand(const char* name, const ExpandArgs& p, const ExpandPlan& c, bool nn,
+hipError_t launch_expand(const char* name, ExpandArgs p, const ExpandPlan& c, bool nn,
                          hipStream_t s);
 hipError_t launch_wgrad(const char* name, WgradArgs p, int sides, hipStream_t s);
 // dst [n][C][R] from src [n][R][C]
