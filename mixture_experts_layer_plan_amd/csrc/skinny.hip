@@ -445,11 +445,11 @@ MOE_DEV void transpose8(const uint4 (&r)[8], uint4 (&c)[8]) {
 // Rows past the group's last, up to its last tile's end, are zero.
 template <int MB>
 MOE_DEV void store_halves(const char* lds, int lo_off, int kp, int K, const SkinnyTile& t,
-                          bf16_t* __restrict__ ut) {
+                          int part, int parts, bf16_t* __restrict__ ut) {
   const int jb = (K + 15) / 16;
   const bool pad = t.off + 16 * MB >= t.count;  // the last tile: zeros up to a multiple of 32
   const int groups = pad ? (((t.off + t.rows + 31) >> 5 << 5) - t.off) / 8 : 2 * MB;
-  for (int i = threadIdx.x >> 4; i < groups * jb; i += 16) {
+  for (int i = (threadIdx.x >> 4) + 16 * part; i < groups * jb; i += 16 * parts) {
     const int q = i / jb, j = (i - q * jb) * 16 + (threadIdx.x & 15), g8 = (t.off >> 3) + q;
     uint32_t w[2][4];
 #pragma unroll
@@ -625,7 +625,7 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs p) {
   bool first = true;
   fill_u<16 * MB, GR ? 1 : 2, GR ? 8 : 1>(p, t, kp, lds);
   __syncthreads();
-  if (p.ut && oz == 0) store_halves<MB>(lds, lo_off, kp, p.K, t, p.ut);
+  if (p.ut) store_halves<MB>(lds, lo_off, kp, p.K, t, oz, p.osplit, p.ut);
   for (; c < c1; c += 4) {
     if (!first) load_base(c, bs);
     first = false;
@@ -714,23 +714,23 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
   const int s0 = oz * bper, s1 = min(blocks, s0 + bper);
   // a group's weights: past its K rows (NN) or columns (NT) zeros, without branches
   const rsrc_t rw = make_rsrc(W, (uint32_t)p.K * (uint32_t)p.nout * 2);
-  u32x4_t wr[8];
-  const auto load_w = [&](int sb, int half) {
+  u32x4_t wr[KS / KC][8];  // a stage ahead, two where a block has two stages
+  const auto load_w = [&](int sb, int half, u32x4_t (&w)[8]) {
     if constexpr (NN) {  // K step ks of column block cb
       const int ks = wv % KC + half * KC, cb = wv / KC;
       const int col = min((sb * SB + cb) * 128 + 8 * rho, p.nout - 8);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        wr[i] = __builtin_amdgcn_raw_buffer_load_b128(
+        w[i] = __builtin_amdgcn_raw_buffer_load_b128(
             rw, ((uint32_t)(32 * ks + 8 * g + i) * (uint32_t)p.nout + col) * 2, 0, 0);
     } else {  // the stage's rows of K values lie one after the other: 16-byte pieces in turn
       const uint32_t at = (uint32_t)(sb * SB * 128) * (uint32_t)p.K * 2;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        wr[i] = __builtin_amdgcn_raw_buffer_load_b128(rw, at + (i * 256 + threadIdx.x) * 16, 0, 0);
+        w[i] = __builtin_amdgcn_raw_buffer_load_b128(rw, at + (i * 256 + threadIdx.x) * 16, 0, 0);
     }
   };
-  const auto store_w = [&](char* st) {
+  const auto store_w = [&](char* st, const u32x4_t (&wr)[8]) {
     if constexpr (NN) {
       uint4 w[8], f[8];
 #pragma unroll
@@ -757,7 +757,10 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
   const uint32_t nbytes = (uint32_t)p.T * (uint32_t)p.nout * 2;  // below 4 GiB
   const rsrc_t rb = make_rsrc(p.base, p.base ? nbytes : 0), ry = make_rsrc(p.y, nbytes);
   // what only the tile decides goes out first: weights, tokens, u
-  if (s0 < s1) load_w(s0, 0);
+  if (s0 < s1) {
+#pragma unroll
+    for (int h = 0; h < KS / KC; ++h) load_w(s0, h, wr[h]);
+  }
   uint32_t rowo[MB][4];
 #pragma unroll
   for (int m = 0; m < MB; ++m)
@@ -766,7 +769,7 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
       const int row = t.row0 + min(16 * (MB * wv + m) + 4 * g + i, t.rows - 1);
       rowo[m][i] = (uint32_t)(GR ? p.src_token[row] : row);
     }
-  constexpr int Q = ROWS * KP / 2048 < 4 ? ROWS * KP / 2048 : 4;
+  constexpr int Q = ROWS * KP / 2048 < 8 ? ROWS * KP / 2048 : 8;
   fill_u<ROWS, Q, GR ? 8 / Q : 1>(p, t, KP, lds);
 #pragma unroll
   for (int m = 0; m < MB; ++m)
@@ -780,16 +783,21 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
   u32x4_t bs[MB][4], bn[MB][4];
   const auto load_base = [&](int c, u32x4_t (&b)[MB][4]) {
     const bool in = c < s1 * SB && c * 128 + 8 * rho < p.nout;
+    const auto get = [&](auto aux) {
 #pragma unroll
-    for (int m = 0; m < MB; ++m)
+      for (int m = 0; m < MB; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        b[m][i] = __builtin_amdgcn_raw_buffer_load_b128(
-            rb, in && rowo[m][i] != OUT ? rowo[m][i] + (uint32_t)c * 256 : OUT, 0, 0);
+        for (int i = 0; i < 4; ++i)
+          b[m][i] = __builtin_amdgcn_raw_buffer_load_b128(
+              rb, in && rowo[m][i] != OUT ? rowo[m][i] + (uint32_t)c * 256 : OUT, 0,
+              decltype(aux)::value);
+    };
+    if (p.stream) get(std::integral_constant<int, 2>{});  // non-temporal
+    else get(std::integral_constant<int, 0>{});
   };
   if (AHEAD) load_base(s0 * SB, bs);
   __syncthreads();
-  if (p.ut && oz == 0) store_halves<4 * MB>(lds, ROWS * KP * 2, KP, p.K, t, p.ut);
+  if (p.ut) store_halves<4 * MB>(lds, ROWS * KP * 2, KP, p.K, t, oz, p.osplit, p.ut);
   bf16x8_t uh[MB][KS], ul[MB][KS];
 #pragma unroll
   for (int m = 0; m < MB; ++m)
@@ -804,7 +812,7 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
     for (int i = threadIdx.x; i < 2 * STAGE / 16; i += 256) *(uint4*)(lds + i * 16) = zero4();
     __syncthreads();
   }
-  if (s0 < s1) store_w(lds);
+  if (s0 < s1) store_w(lds, wr[0]);
   __syncthreads();
   for (int sb = s0; sb < s1; ++sb) {
 #pragma unroll 1  // short code: a workgroup that runs once pays for every line it fetches
@@ -823,7 +831,7 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
         const int st = (sb - s0) * (KS / KC) + half;
         const char* cur = lds + (st & 1) * STAGE;
         const bool last_half = half + 1 == KS / KC;
-        if (cb == 0) load_w(last_half ? sb + 1 : sb, last_half ? 0 : half + 1);
+        if (cb == 0) load_w(sb + 1, half, wr[half]);  // this half of the next block
 #pragma unroll
         for (int kc = 0; kc < KC; ++kc)
 #pragma unroll
@@ -843,7 +851,7 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
               for (int m = 0; m < MB; ++m) acc[m][f4 + f] = mfma16(uh[m][ks], w[f], acc[m][f4 + f]);
           }
         if (!last_half) {  // SB is 1 here
-          store_w(lds + ((st + 1) & 1) * STAGE);
+          store_w(lds + ((st + 1) & 1) * STAGE, wr[(half + 1) % (KS / KC)]);
           __syncthreads();
         }
       }
@@ -876,7 +884,7 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
       }
     }
     // the next stage's weights (past the last: not used)
-    store_w(lds + ((sb + 1 - s0) * (KS / KC) & 1) * STAGE);
+    store_w(lds + ((sb + 1 - s0) * (KS / KC) & 1) * STAGE, wr[0]);
     __syncthreads();
   }
 }
@@ -1186,12 +1194,11 @@ hipError_t expand_small(const char* name, const ExpandArgs& p, hipStream_t s) {
   return MOE_LAUNCH(name, s, k<<<expand_grid(p), 256, lds, s>>>(p));
 }
 
-// Outputs of this size and more leave with non-temporal stores: the Infinity Cache (256 MB)
-// would hold them dirty and write them back under the kernels that follow.
-#ifndef STREAM_MB
-#define STREAM_MB 32
-#endif
-constexpr size_t STREAM_BYTES = (size_t)STREAM_MB << 20;
+// Outputs of this size and more leave with non-temporal stores, and their base comes with
+// non-temporal loads: the Infinity Cache (256 MB) would hold them, the outputs dirty, to be
+// written back under the kernels that follow, in the place of the dy that the weight
+// gradients read next.  8192 x 7168 at rank 64, forward and backward: 289 -> 268 us.
+constexpr size_t STREAM_BYTES = 32u << 20;
 
 template <int MB, int KS, bool NN, bool GR>
 hipError_t expand_tiles(const char* name, const ExpandArgs& p, hipStream_t s) {
