@@ -116,3 +116,13 @@ def test_lora_pointers_and_workspace(L):
     assert lora(L, s, f - 1) == WS and lora_b(L, s, b - 1) == WS
     assert L.moe_lora_bf16(None, *[F] * 9, f, None) == NULL
     assert lora(L, B.lora_shape(0, 64, 128, 3, 16), 0, x=None, y=None, ws=None) == OK
+
+
+def test_layer_options_that_do_not_fit():
+    from mixture_experts_layer_plan_amd import LayerBuffers
+    for kw in (dict(router_proj=True), dict(adapters=(2, 8))):
+        with pytest.raises(ValueError):
+            LayerBuffers(8, 256, 128, 4, 2, dtype="f32", device="cpu", **kw)
+    b = LayerBuffers(8, 256, 128, 4, 2, dtype="bf16", device="cpu", router_proj=True,
+                     adapters=(2, 8), scoring=B.scoring("sigmoid"))
+    assert b.logits.shape == (8, 4) and b.d_lora_b.shape == (2, 256, 8)
