@@ -211,28 +211,34 @@ __global__ __launch_bounds__(512) void dot_kernel(DotArgs p) {
 // a ring of NS stages; the product of a stage runs while NS - 1 more are in flight.
 // Fragments loaded from memory without LDS took 121 us for the 8192 x 256 x 7168 router
 // product: 16 lanes in 16 rows keep the address unit busy for 64 cycles a KiB.
-// Row r's 16-byte chunk c lies at r * K2 + 16 (c ^ (r & (CH - 1))): the 16 rows of a
-// fragment read hit all 64 banks.
-template <int BN>
+// Row r's 16-byte chunk c lies at r * K2 + 16 (c ^ swz(r)): the 16 rows of a fragment read
+// hit all 64 banks.
+#ifndef DT_NSB
+#define DT_NSB 4
+#endif
+template <int BM, int BN>
 struct DotTile {
-  // 128 columns: 256-byte pieces and 8 wavefronts, of which two share a tile and halve K
-  static constexpr int KG = BN == 128 ? 2 : 1, BK = 64 * KG, K2 = 2 * BK, CH = K2 / 16;
-  static constexpr int WN = BN >= 64 ? 2 : 1, WM = 4 / WN;  // wavefronts along rows, columns
-  static constexpr int MB = 64 / 16 / WM, NB = BN / 16 / WN;
-  static constexpr int NS = 3, STAGE = (64 + BN) * K2;  // 36, 48, 144 KiB: 4, 3, 1 a CU
-  static constexpr int LOADS = STAGE / (4096 * KG), ALOADS = 64 * K2 / (4096 * KG);  // a wavefront
+  static constexpr int WN = BN >= 64 ? 2 : 1, WM = 4 / WN;  // wavefronts along columns, rows
+  // 128 columns: a second set of wavefronts takes half of each stage's K
+  static constexpr int KG = BN == 128 ? 2 : 1, BK = BM == 64 ? 64 * KG : 64, K2 = 2 * BK, CH = K2 / 16;
+  static constexpr int NWV = 4 * KG, NT = 64 * NWV, HS = BK / 32 / KG;  // K steps of a wavefront
+  static constexpr int MB = BM / 16 / WM, NB = BN / 16 / WN;
+  static constexpr int STAGE = (BM + BN) * K2;
+  static constexpr int NS = BM == 128 ? DT_NSB : 3;  // 36, 48, 144, 128 KiB: 4, 3, 1, 1 a CU
+  static constexpr int LOADS = STAGE / (1024 * NWV), ALOADS = BM * K2 / (1024 * NWV);  // a wavefront
+  static MOE_DEV int swz(int r) { return CH == 8 ? (r >> 1) & 7 : r & 15; }
 };
 
-// Wait until at most `ahead` (0, 1, 2) stages of L loads are in flight, then meet the
+// Wait until at most `ahead` (0 to 3) stages of L loads are in flight, then meet the
 // workgroup.  vmcnt's two high bits are bits 14 and 15 of the operand.
 template <int L>
 MOE_DEV void ring_wait_for(int ahead) {
-  static_assert(2 * L < 64, "vmcnt has 6 bits");
-  constexpr int W1 = (L & 15) | ((L >> 4) << 14) | 0x70;
-  constexpr int W2 = ((2 * L) & 15) | (((2 * L) >> 4) << 14) | 0x70;
-  if (ahead >= 2) __builtin_amdgcn_s_waitcnt(W2);
-  else if (ahead == 1) __builtin_amdgcn_s_waitcnt(W1);
-  else __builtin_amdgcn_s_waitcnt(0x70);
+  static_assert(3 * L < 64, "vmcnt has 6 bits");
+  constexpr auto vm = [](int n) { return (n & 15) | ((n >> 4) << 14) | 0x70; };
+  if (ahead >= 3) __builtin_amdgcn_s_waitcnt(vm(3 * L));
+  else if (ahead == 2) __builtin_amdgcn_s_waitcnt(vm(2 * L));
+  else if (ahead == 1) __builtin_amdgcn_s_waitcnt(vm(L));
+  else __builtin_amdgcn_s_waitcnt(vm(0));
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");  // no LDS read of the stage moves above the barrier
 }
@@ -268,10 +274,21 @@ MOE_DEV void lds_read6(const uint32_t (&a)[6], s16x8_t (&f)[6]) {
       : "memory");
 }
 
-template <int BN, bool GR>
-__global__ __launch_bounds__(256 * DotTile<BN>::KG) void dot_tile_kernel(DotArgs p) {
-  using C = DotTile<BN>;
-  constexpr int NR = C::MB + C::NB, NWV = 4 * C::KG;
+MOE_DEV void lds_read8(const uint32_t (&a)[8], s16x8_t (&f)[8]) {
+  asm volatile(
+      "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_b128 %2, %10\n\t"
+      "ds_read_b128 %3, %11\n\tds_read_b128 %4, %12\n\tds_read_b128 %5, %13\n\t"
+      "ds_read_b128 %6, %14\n\tds_read_b128 %7, %15\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3]), "=&v"(f[4]), "=&v"(f[5]),
+        "=&v"(f[6]), "=&v"(f[7])
+      : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "v"(a[4]), "v"(a[5]), "v"(a[6]), "v"(a[7])
+      : "memory");
+}
+
+template <int BM, int BN, bool GR>
+__global__ __launch_bounds__((DotTile<BM, BN>::NT)) void dot_tile_kernel(DotArgs p) {
+  using C = DotTile<BM, BN>;
+  constexpr int NR = C::MB + C::NB, NWV = C::NWV;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int nblk = (p.N + BN - 1) / BN;
@@ -279,11 +296,11 @@ __global__ __launch_bounds__(256 * DotTile<BN>::KG) void dot_tile_kernel(DotArgs
   const int id = GR ? (int)blockIdx.x : xcd_order(blockIdx.x, gridDim.x);
   const int n0 = (id % nblk) * BN, s = (id / nblk) % p.S;
   SkinnyTile t;
-  if (!skinny_tile<GR>(p.counts, p.n, p.T, 64, id / (nblk * p.S), t)) return;
+  if (!skinny_tile<GR>(p.counts, p.n, p.T, BM, id / (nblk * p.S), t)) return;
   const uint32_t K2 = (uint32_t)p.K * 2;
   const rsrc_t ra = make_rsrc(p.a, (uint32_t)p.T * K2);  // below 4 GiB, checked on the host
   const rsrc_t rb = make_rsrc(p.b + (size_t)t.a * p.N * p.K, (uint32_t)p.N * K2);
-  // load q of a wavefront brings the RP rows from RP (NWV q + wv) on of the stage (the 64
+  // load q of a wavefront brings the RP rows from RP (NWV q + wv) on of the stage (the BM
   // rows of a, then the BN of b): lane L row L / CH, chunk L % CH of LDS; out of range: zeros
   constexpr uint32_t OUT = 0xffffffffu;
   constexpr int RP = 64 / C::CH;
@@ -292,13 +309,13 @@ __global__ __launch_bounds__(256 * DotTile<BN>::KG) void dot_tile_kernel(DotArgs
 #pragma unroll
   for (int q = 0; q < C::LOADS; ++q) {
     const int r = RP * (NWV * q + wv) + lane / C::CH;
-    cq[q] = ((lane ^ r) & (C::CH - 1)) * 16;
+    cq[q] = ((lane & (C::CH - 1)) ^ C::swz(r)) * 16;
     if (q < C::ALOADS) {
       const int row = t.row0 + min(r, t.rows - 1);
       off[q] = (uint32_t)(GR ? p.src_token[row] : row) * K2;
       if (r >= t.rows) off[q] = OUT;
     } else {
-      const int n = n0 + r - 64;
+      const int n = n0 + r - BM;
       off[q] = n < p.N ? (uint32_t)n * K2 : OUT;
     }
   }
@@ -318,7 +335,8 @@ __global__ __launch_bounds__(256 * DotTile<BN>::KG) void dot_tile_kernel(DotArgs
   for (int i = 0; i < C::MB; ++i)
 #pragma unroll
     for (int j = 0; j < C::NB; ++j) acc[i][j] = (f32x4v){0.f, 0.f, 0.f, 0.f};
-  const int kg = wv / 4, wm = (wv % 4) / C::WN, wn = wv % C::WN, g = lane >> 4, rho = lane & 15;
+  const int kg = wv / 4, wm = (wv % 4) / C::WN, wn = wv % C::WN;
+  const int g = lane >> 4, rho = lane & 15;
   for (int i = 0; i < C::NS - 1 && i < nk; ++i) issue(i);
   for (int i = 0; i < nk; ++i) {
     // stage i is in (each later one has LOADS instructions), stage i - 1 no longer read
@@ -326,19 +344,20 @@ __global__ __launch_bounds__(256 * DotTile<BN>::KG) void dot_tile_kernel(DotArgs
     if (i + C::NS - 1 < nk) issue(i + C::NS - 1);
     const char* st = lds + (i % C::NS) * C::STAGE;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < C::HS; ++h) {
       uint32_t ad[NR];
       s16x8_t f[NR];
-      const int cx = ((4 * (2 * kg + h) + g) ^ (rho & (C::CH - 1))) << 4;
+      const int cx = ((4 * (C::HS * kg + h) + g) ^ C::swz(rho)) << 4;
 #pragma unroll
       for (int m = 0; m < C::MB; ++m)
         ad[m] = lds_at(st + (16 * (C::MB * wm + m) + rho) * C::K2 + cx);
 #pragma unroll
       for (int n = 0; n < C::NB; ++n)
-        ad[C::MB + n] = lds_at(st + (64 + 16 * (C::NB * wn + n) + rho) * C::K2 + cx);
+        ad[C::MB + n] = lds_at(st + (BM + 16 * (C::NB * wn + n) + rho) * C::K2 + cx);
       if constexpr (NR == 3) lds_read3(ad, f);
       else if constexpr (NR == 4) lds_read4(ad, f);
-      else lds_read6(ad, f);
+      else if constexpr (NR == 6) lds_read6(ad, f);
+      else lds_read8(ad, f);
 #pragma unroll
       for (int m = 0; m < C::MB; ++m)
 #pragma unroll
@@ -1173,13 +1192,15 @@ hipError_t dot_small(const char* name, const DotArgs& p, int tiles, hipStream_t 
   return MOE_LAUNCH(name, s, dot_kernel<NB, false><<<g, 512, 0, s>>>(p));
 }
 
-template <int BN>
+template <int BM, int BN>
 hipError_t dot_tiles(const char* name, const DotArgs& p, int tiles, hipStream_t s) {
   const unsigned g = (unsigned)((long)tiles * div_up(p.N, BN) * p.S);
-  const unsigned lds = DotTile<BN>::NS * DotTile<BN>::STAGE;
-  constexpr int NT = 256 * DotTile<BN>::KG;
-  if (p.counts) return MOE_LAUNCH(name, s, dot_tile_kernel<BN, true><<<g, NT, lds, s>>>(p));
-  return MOE_LAUNCH(name, s, dot_tile_kernel<BN, false><<<g, NT, lds, s>>>(p));
+  using C = DotTile<BM, BN>;
+  constexpr unsigned lds = C::NS * C::STAGE;
+  if constexpr (BM == 64)
+    if (p.counts)
+      return MOE_LAUNCH(name, s, dot_tile_kernel<BM, BN, true><<<g, C::NT, lds, s>>>(p));
+  return MOE_LAUNCH(name, s, dot_tile_kernel<BM, BN, false><<<g, C::NT, lds, s>>>(p));
 }
 
 unsigned expand_grid(const ExpandArgs& p) {
@@ -1234,13 +1255,17 @@ int row_tiles(int T, int n, bool grouped, int rows) {
 
 }  // namespace
 
+#ifndef DOT_BM
+#define DOT_BM 1024
+#endif
 SkinnyPlan skinny_plan(int T, int n, bool grouped, int K, int N) {
   SkinnyPlan c;
   const int groups = !grouped ? 1 : (n < T ? n : T);
   c.few = !grouped && T <= DOT_FEW;
   c.tile = T >= 32 * groups;
   c.bn = !c.tile ? (N <= 16 ? 16 : (N <= 32 ? 32 : 64)) : (N <= 32 ? 32 : (N <= 64 ? 64 : 128));
-  c.tiles = row_tiles(T, n, grouped, c.tile ? 64 : 16);
+  c.bm = !c.tile ? 16 : (c.bn == 128 && !grouped && T >= DOT_BM ? 128 : 64);
+  c.tiles = row_tiles(T, n, grouped, c.bm);
   const int wg = c.tiles * div_up(N, c.bn);
   // at least two steps of each of 8 wavefronts, or a ring's stages
   const int most = div_up(K, c.tile ? 512 : 1024);
@@ -1263,9 +1288,10 @@ hipError_t launch_dot(const char* name, const DotArgs& p, const SkinnyPlan& c, h
     if (c.bn == 32) return dot_small<2>(name, p, c.tiles, s);
     return dot_small<4>(name, p, c.tiles, s);
   }
-  if (c.bn == 32) return dot_tiles<32>(name, p, c.tiles, s);
-  if (c.bn == 64) return dot_tiles<64>(name, p, c.tiles, s);
-  return dot_tiles<128>(name, p, c.tiles, s);
+  if (c.bn == 32) return dot_tiles<64, 32>(name, p, c.tiles, s);
+  if (c.bn == 64) return dot_tiles<64, 64>(name, p, c.tiles, s);
+  if (c.bm == 64) return dot_tiles<64, 128>(name, p, c.tiles, s);
+  return dot_tiles<128, 128>(name, p, c.tiles, s);
 }
 
 hipError_t launch_sum_parts(const char* name, const float* parts, int S, size_t n, float* out,

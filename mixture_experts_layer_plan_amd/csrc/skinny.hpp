@@ -63,7 +63,7 @@ constexpr int DOT_FEW = 8;             // tokens of the dot without matrix instr
 // sizes alone, so that the order of every sum is too.  tiles: row tiles, an upper bound.
 struct SkinnyPlan {
   bool few, tile;  // dot_few_kernel; dot_tile_kernel (else dot_kernel)
-  int bn, tiles, S;
+  int bm, bn, tiles, S;
 };
 SkinnyPlan skinny_plan(int T, int n, bool grouped, int K, int N);
 struct ExpandPlan {
