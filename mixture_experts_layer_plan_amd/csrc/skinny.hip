@@ -916,9 +916,9 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
 // as the halves that `expand` left in fragment order, so that enough is in flight without
 // registers (with both in registers one tile ahead: 88 us against 235 MB of x and dy).  A
 // lane reads 8 rows of 8 columns and turns them in registers into 8 fragments along the
-// rows; row i of fragment f stands for column 8 i + f.
-//   TR = false, [J][H]: x as the M side, a lane ends with 8 neighbouring h
-//   TR = true, [H][J]: the halves as the M side, a lane ends with 4 neighbouring j
+// rows; row i of fragment f stands for column 8 i + f.  With the halves as the M side a lane
+// ends with 4 neighbouring j of 8 neighbouring h: it stores 8 h of a row (16 lanes: 128 of
+// them) for [J][H], 4 j for [H][J] (TR).
 template <int JT, int WJ>
 struct WgradTile {
   static constexpr int WK = 4 / WJ, JB = JT * WJ;       // 16-row blocks of j
@@ -1057,7 +1057,7 @@ MOE_DEV void wgrad_body(const WgradArgs& p, const WgradSide& d, int hb, int cj, 
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
           const bf16x8_t uf = __builtin_bit_cast(bf16x8_t, u[j][h]);
-          acc[j][v] = TR ? mfma16(uf, as_frag(f[v]), acc[j][v]) : mfma16(as_frag(f[v]), uf, acc[j][v]);
+          acc[j][v] = mfma16(uf, as_frag(f[v]), acc[j][v]);
         }
   }
   __syncthreads();  // every wavefront is done with the ring
@@ -1096,12 +1096,12 @@ MOE_DEV void wgrad_body(const WgradArgs& p, const WgradSide& d, int hb, int cj, 
         else *(uint2*)(out + at) = cvt4(a);
       }
     } else {
-      const int jj = (jb0 + wj * JT + j) * 16 + rho;
-      if (jj >= p.J) continue;
+      const int h = h0 + 8 * rho;
+      if (h >= d.H) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int h = h0 + 8 * (4 * g + i);
-        if (h >= d.H) continue;
+        const int jj = (jb0 + wj * JT + j) * 16 + 4 * g + i;
+        if (jj >= p.J) continue;
         float f[8];
 #pragma unroll
         for (int v = 0; v < 8; ++v) f[v] = acc[j][v][i];
