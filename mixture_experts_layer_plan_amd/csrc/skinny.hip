@@ -315,7 +315,10 @@ __global__ __launch_bounds__((DotTile<BM, BN>::NT)) void dot_tile_kernel(DotArgs
       off[q] = (uint32_t)(GR ? p.src_token[row] : row) * K2;
       if (r >= t.rows) off[q] = OUT;
     } else {
-      const int n = n0 + r - BM;
+      // row 16 f + i of a wavefront's columns holds column NB i + f: a lane ends with NB
+      // neighbours, 16 lanes with a run of 16 NB
+      const int l = r - BM, i = l & 15, f = (l >> 4) % C::NB, w = l / (16 * C::NB);
+      const int n = n0 + (16 * w + i) * C::NB + f;
       off[q] = n < p.N ? (uint32_t)n * K2 : OUT;
     }
   }
@@ -362,8 +365,8 @@ __global__ __launch_bounds__((DotTile<BM, BN>::NT)) void dot_tile_kernel(DotArgs
       for (int m = 0; m < C::MB; ++m)
 #pragma unroll
         for (int n = 0; n < C::NB; ++n)
-          acc[m][n] = mfma16(__builtin_bit_cast(bf16x8_t, f[C::MB + n]),
-                             __builtin_bit_cast(bf16x8_t, f[m]), acc[m][n]);
+          acc[m][n] = mfma16(__builtin_bit_cast(bf16x8_t, f[m]),
+                             __builtin_bit_cast(bf16x8_t, f[C::MB + n]), acc[m][n]);
     }
   }
   if constexpr (C::KG == 2) {  // join the halves of K
@@ -381,15 +384,26 @@ __global__ __launch_bounds__((DotTile<BM, BN>::NT)) void dot_tile_kernel(DotArgs
 #pragma unroll
       for (int n = 0; n < C::NB; ++n) acc[m][n] += part[m][n][lane];
   }
+  const int c0 = n0 + (16 * wn + rho) * C::NB;
 #pragma unroll
-  for (int m = 0; m < C::MB; ++m) {
-    const int r = 16 * (C::MB * wm + m) + rho;
-    if (r >= t.rows) continue;
-    float* o = p.out + ((size_t)s * p.R + t.row0 + r) * p.N;
+  for (int m = 0; m < C::MB; ++m)
 #pragma unroll
-    for (int n = 0; n < C::NB; ++n)
-      put4(o, n0 + 16 * (C::NB * wn + n) + 4 * g, p.N, acc[m][n]);
-  }
+    for (int i = 0; i < 4; ++i) {
+      const int r = 16 * (C::MB * wm + m) + 4 * g + i;
+      if (r >= t.rows || c0 >= p.N) continue;
+      float* o = p.out + ((size_t)s * p.R + t.row0 + r) * p.N + c0;
+      if (p.N % C::NB == 0) {  // the row and this run of it are aligned to the run
+        typedef float run_t __attribute__((ext_vector_type(C::NB)));
+        run_t v;
+#pragma unroll
+        for (int n = 0; n < C::NB; ++n) v[n] = acc[m][n][i];
+        *(run_t*)o = v;
+      } else {
+#pragma unroll
+        for (int n = 0; n < C::NB; ++n)
+          if (c0 + n < p.N) o[n] = acc[m][n][i];
+      }
+    }
 }
 
 // out[i] = sum over the S parts, in order
