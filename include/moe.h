@@ -261,15 +261,16 @@ moe_status moe_route_scored_backward(const moe_shape* shape, const moe_scoring* 
                                      hipStream_t stream);
 
 /* The router projection of the bf16 and MXFP8 layers: logits [T, E] (fp32) = x [T, H]
- * (bf16) * w_router [E, H]^T (bf16), products and sums in fp32.  T * H * 2 bytes below
- * 4 GiB, as in the layer calls (MOE_E_UNSUPPORTED otherwise).
+ * (bf16) * w_router [E, H]^T (bf16), products and sums in fp32.  T * H * 2 and
+ * E * H * 2 bytes below 4 GiB, as in the layer calls (MOE_E_UNSUPPORTED otherwise).
  * ws [ws_bytes >= moe_router_workspace_bytes(shape, 0)] (may be NULL if that is 0). */
 moe_status moe_router_logits_bf16(const moe_shape* shape, const void* x, const void* w_router,
                                   float* logits, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* Its backward: dw_router [E, H] (bf16, overwritten) = d_logits^T x and
  * dx [T, H] (bf16) = dx_in + d_logits w_router, summed in fp32 and rounded once;
- * dx_in bf16 [T, H], or NULL (zero), may be dx itself.  d_logits fp32 [T, E] enters the
+ * dx_in bf16 [T, H], or NULL (zero), may be dx itself; dx may not be x
+ * (MOE_E_UNSUPPORTED).  d_logits fp32 [T, E] enters the
  * products with 16 bits of mantissa (as two bf16 halves); where x or d_logits is not
  * finite, neither are the gradients it enters (inf or NaN).
  * ws [ws_bytes >= moe_router_workspace_bytes(shape, 1)]. */
@@ -483,7 +484,7 @@ moe_status moe_backward_mxfp8(const moe_shape* shape, const void* plan, const vo
  * layer that the adapters stand beside.
  *   T tokens, H_in, H_out: multiples of 8; n_adapters in [1, 1024]; rank: a multiple of
  *   8 in [8, 128] (pad smaller ranks with zero rows of A and zero columns of B);
- *   T * max(H_in, H_out) * 2 bytes below 4 GiB (MOE_E_UNSUPPORTED otherwise).
+ *   max(T, rank) * max(H_in, H_out) * 2 bytes below 4 GiB (MOE_E_UNSUPPORTED otherwise).
  *   lora_a bf16 [n_adapters, rank, H_in], lora_b bf16 [n_adapters, H_out, rank],
  *   scale fp32 [n_adapters]. */
 typedef struct {
@@ -517,7 +518,7 @@ moe_status moe_lora_bf16(const moe_lora_shape* shape, const void* plan, const vo
 /* Backward, from dy bf16 [T, H_out] and the forward's saved, with u_t = scale A x_t and
  * v_t = scale B^T dy_t over the tokens of each adapter:
  *   dx[t, :] = dx_in[t, :] + A^T v_t   (bf16 [T, H_in]; dx_in or NULL, may be dx itself,
- *                                       as base and y)
+ *                                       as base and y; dx may not be x or dy)
  *   d_lora_a = sum_t v_t (x) x_t, d_lora_b = sum_t dy_t (x) u_t   (bf16, overwritten;
  *                                       zeros for adapters without tokens) */
 moe_status moe_lora_backward_bf16(const moe_lora_shape* shape, const void* plan, const void* x,

@@ -969,7 +969,8 @@ moe_status check_router(const moe_shape* s) {
   one.k = 1;  // k, I and the minibatches are not the router's
   const moe_status rc = check_shape(&one, false);
   if (rc != MOE_OK) return rc;
-  return (uint64_t)s->T * s->H * 2 < 1ull << 32 ? MOE_OK : MOE_E_UNSUPPORTED;
+  const uint64_t rows = std::max(s->T, s->E);  // 32-bit byte offsets into x, dx and the weights
+  return rows * s->H * 2 < 1ull << 32 ? MOE_OK : MOE_E_UNSUPPORTED;
 }
 
 moe_status check_lora(const moe_lora_shape* s) {
@@ -977,8 +978,8 @@ moe_status check_lora(const moe_lora_shape* s) {
   if (s->T < 0 || s->n_adapters < 1 || s->n_adapters > MOE_MAX_E) return MOE_E_SHAPE;
   if (s->H_in < 8 || s->H_in % 8 || s->H_out < 8 || s->H_out % 8) return MOE_E_SHAPE;
   if (s->rank < 8 || s->rank > 128 || s->rank % 8) return MOE_E_SHAPE;
-  if ((uint64_t)s->T * (uint64_t)std::max(s->H_in, s->H_out) * 2 >= 1ull << 32)
-    return MOE_E_UNSUPPORTED;
+  const uint64_t rows = std::max(s->T, s->rank);  // 32-bit byte offsets, as in the layer calls
+  if (rows * (uint64_t)std::max(s->H_in, s->H_out) * 2 >= 1ull << 32) return MOE_E_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -1402,6 +1403,7 @@ moe_status moe_router_backward_bf16(const moe_shape* s, const void* x, const voi
   if (rc != MOE_OK) return rc;
   if (any_null({w_router, dw_router, ws}) || any_null_rows(s, {x, d_logits, dx})) return MOE_E_NULL;
   if (!all_aligned({x, w_router, d_logits, dx_in, dw_router, dx, ws})) return MOE_E_ALIGN;
+  if (s->T > 0 && dx == x) return MOE_E_UNSUPPORTED;  // dW reads x after dx is written
   const RouterWs W = router_ws(s, true);
   if (ws_bytes < W.total) return MOE_E_WORKSPACE;
   ExpandArgs e;
@@ -1482,6 +1484,7 @@ moe_status moe_lora_backward_bf16(const moe_lora_shape* s, const void* plan, con
     return MOE_E_NULL;
   if (!all_aligned({plan, x, lora_a, lora_b, scale, saved, dy, dx_in, dx, d_lora_a, d_lora_b, ws}))
     return MOE_E_ALIGN;
+  if (s->T > 0 && (dx == x || dx == dy)) return MOE_E_UNSUPPORTED;  // both are read after dx
   const LoraWs W = lora_ws(s, true);
   if (ws_bytes < W.total) return MOE_E_WORKSPACE;
   const moe_shape ps = lora_plan_shape(s);

@@ -213,9 +213,6 @@ __global__ __launch_bounds__(512) void dot_kernel(DotArgs p) {
 // product: 16 lanes in 16 rows keep the address unit busy for 64 cycles a KiB.
 // Row r's 16-byte chunk c lies at r * K2 + 16 (c ^ swz(r)): the 16 rows of a fragment read
 // hit all 64 banks.
-#ifndef DT_NSB
-#define DT_NSB 4
-#endif
 template <int BM, int BN>
 struct DotTile {
   static constexpr int WN = BN >= 64 ? 2 : 1, WM = 4 / WN;  // wavefronts along columns, rows
@@ -224,7 +221,7 @@ struct DotTile {
   static constexpr int NWV = 4 * KG, NT = 64 * NWV, HS = BK / 32 / KG;  // K steps of a wavefront
   static constexpr int MB = BM / 16 / WM, NB = BN / 16 / WN;
   static constexpr int STAGE = (BM + BN) * K2;
-  static constexpr int NS = BM == 128 ? DT_NSB : 3;  // 36, 48, 144, 128 KiB: 4, 3, 1, 1 a CU
+  static constexpr int NS = BM == 128 ? 4 : 3;  // 36, 48, 144, 128 KiB: 4, 3, 1, 1 a CU
   static constexpr int LOADS = STAGE / (1024 * NWV), ALOADS = BM * K2 / (1024 * NWV);  // a wavefront
   static MOE_DEV int swz(int r) { return CH == 8 ? (r >> 1) & 7 : r & 15; }
 };
@@ -1005,8 +1002,8 @@ MOE_DEV void wgrad_body(const WgradArgs& p, const WgradSide& d, int hb, int cj, 
   if (GR) {
     int32_t v[WGRAD_MAX_CHUNK / 256];
 #pragma unroll
-    for (int q = 0; q < WGRAD_MAX_CHUNK / 256; ++q)
-      v[q] = p.src_token[row0 + min((int)threadIdx.x + 256 * q, max(rows - 1, 0))];
+    for (int q = 0; q < WGRAD_MAX_CHUNK / 256; ++q)  // rows past the last repeat it
+      v[q] = rows > 0 ? p.src_token[row0 + min((int)threadIdx.x + 256 * q, rows - 1)] : 0;
 #pragma unroll
     for (int q = 0; q < WGRAD_MAX_CHUNK / 256; ++q) ((int32_t*)tok)[threadIdx.x + 256 * q] = v[q];
     __syncthreads();
@@ -1269,16 +1266,13 @@ int row_tiles(int T, int n, bool grouped, int rows) {
 
 }  // namespace
 
-#ifndef DOT_BM
-#define DOT_BM 1024
-#endif
 SkinnyPlan skinny_plan(int T, int n, bool grouped, int K, int N) {
   SkinnyPlan c;
   const int groups = !grouped ? 1 : (n < T ? n : T);
   c.few = !grouped && T <= DOT_FEW;
   c.tile = T >= 32 * groups;
   c.bn = !c.tile ? (N <= 16 ? 16 : (N <= 32 ? 32 : 64)) : (N <= 32 ? 32 : (N <= 64 ? 64 : 128));
-  c.bm = !c.tile ? 16 : (c.bn == 128 && !grouped && T >= DOT_BM ? 128 : 64);
+  c.bm = !c.tile ? 16 : (c.bn == 128 && !grouped && T >= 1024 ? 128 : 64);
   c.tiles = row_tiles(T, n, grouped, c.bm);
   const int wg = c.tiles * div_up(N, c.bn);
   // at least two steps of each of 8 wavefronts, or a ring's stages
@@ -1295,6 +1289,7 @@ hipError_t launch_dot(const char* name, const DotArgs& p, const SkinnyPlan& c, h
   if (c.few) {
     if (p.T <= 1) return MOE_LAUNCH(name, s, dot_few_kernel<1><<<(unsigned)p.N, 256, 0, s>>>(p));
     if (p.T <= 4) return MOE_LAUNCH(name, s, dot_few_kernel<4><<<(unsigned)p.N, 256, 0, s>>>(p));
+    if (p.T <= 8) return MOE_LAUNCH(name, s, dot_few_kernel<8><<<(unsigned)p.N, 256, 0, s>>>(p));
     return MOE_LAUNCH(name, s, dot_few_kernel<DOT_FEW><<<(unsigned)p.N, 256, 0, s>>>(p));
   }
   if (!c.tile) {

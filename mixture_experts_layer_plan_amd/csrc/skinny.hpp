@@ -57,7 +57,7 @@ struct WgradArgs {
 };
 
 constexpr int WGRAD_MAX_CHUNK = 1024;  // rows of one chunk (their tokens lie in LDS)
-constexpr int DOT_FEW = 8;             // tokens of the dot without matrix instructions
+constexpr int DOT_FEW = 16;            // tokens of the dot without matrix instructions
 
 // How a dot or an expand of T rows in n groups (one if not grouped) is cut up: from the
 // sizes alone, so that the order of every sum is too.  tiles: row tiles, an upper bound.

@@ -64,7 +64,7 @@ def test_router_projection(L):
     def logits(s, x=F, w=F, out=F, ws=F, n=fwd):
         return L.moe_router_logits_bf16(ctypes.byref(s), x, w, out, ws, n, None)
 
-    def back(s, x=F, w=F, dL=F, dxi=F, dw=F, dx=F, ws=F, n=bwd):
+    def back(s, x=F, w=F, dL=F, dxi=F, dw=F, dx=F + 4096, ws=F, n=bwd):
         return L.moe_router_backward_bf16(ctypes.byref(s), x, w, dL, dxi, dw, dx, ws, n, None)
 
     assert logits(s_(H=200)) == SHAPE and back(s_(H=200)) == SHAPE
@@ -77,13 +77,18 @@ def test_router_projection(L):
     assert back(s, ws=None) == NULL and back(s, dw=None) == NULL and back(s, dL=None) == NULL
     assert back(s, dxi=BAD) == ALIGN
     assert B.moe_router_workspace_bytes(s_(H=100), True) == 0
+    # 32-bit byte offsets: T H 2 and E H 2 below 4 GiB
+    assert logits(s_(T=1 << 24, H=128, k=1)) == UNSUP
+    assert logits(s_(T=1, H=1 << 27, k=1)) == UNSUP
+    assert back(s, x=F, dx=F) == UNSUP                                     # dx over x
 
 
 def lora(L, s, n, plan=F, x=F, a=F, b=F, sc=F, base=F, y=F, saved=None, ws=F):
     return L.moe_lora_bf16(ctypes.byref(s), plan, x, a, b, sc, base, y, saved, ws, n, None)
 
 
-def lora_b(L, s, n, plan=F, x=F, a=F, b=F, sc=F, saved=F, dy=F, dxi=F, dx=F, da=F, db=F, ws=F):
+def lora_b(L, s, n, plan=F, x=F, a=F, b=F, sc=F, saved=F, dy=F + 4096, dxi=F, dx=F + 8192, da=F, db=F,
+           ws=F):
     return L.moe_lora_backward_bf16(ctypes.byref(s), plan, x, a, b, sc, saved, dy, dxi, dx, da, db,
                                     ws, n, None)
 
@@ -93,7 +98,8 @@ def lora_b(L, s, n, plan=F, x=F, a=F, b=F, sc=F, saved=F, dy=F, dxi=F, dx=F, da=
                                        ((4, 64, 64, 0, 8), SHAPE), ((4, 64, 64, 1025, 8), SHAPE),
                                        ((4, 64, 64, 2, 4), SHAPE), ((4, 64, 64, 2, 12), SHAPE),
                                        ((4, 64, 64, 2, 136), SHAPE),
-                                       ((1 << 20, 64, 4096, 2, 8), UNSUP)])
+                                       ((1 << 20, 64, 4096, 2, 8), UNSUP),
+                                       ((1, 64, 1 << 28, 2, 8), UNSUP)])
 def test_lora_shapes(L, args, code):
     s = B.lora_shape(*args)
     assert lora(L, s, 1 << 40) == code and lora_b(L, s, 1 << 40) == code
@@ -114,6 +120,7 @@ def test_lora_pointers_and_workspace(L):
         assert lora(L, s, f, **{arg: BAD}) == ALIGN
     assert lora_b(L, s, b, dxi=BAD) == ALIGN
     assert lora(L, s, f - 1) == WS and lora_b(L, s, b - 1) == WS
+    assert lora_b(L, s, b, dx=F) == UNSUP and lora_b(L, s, b, dx=F + 4096) == UNSUP  # x, dy
     assert L.moe_lora_bf16(None, *[F] * 9, f, None) == NULL
     assert lora(L, B.lora_shape(0, 64, 128, 3, 16), 0, x=None, y=None, ws=None) == OK
 
