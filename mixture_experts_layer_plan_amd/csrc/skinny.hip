@@ -544,7 +544,18 @@ MOE_DEV void fill_u(const ExpandArgs& p, const SkinnyTile& t, int kp, char* lds)
           }
         }
       }
-    } else {  // the router's dL: one part, rows of any length
+    } else if ((p.K & 3) == 0) {  // the router's dL: one part, a last piece of 4
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int i = min(i0 + q * 256, items - 1);
+        const bool two = 8 * (i % ch) + 4 < p.K;
+        const float4 a = *(const float4*)u[q];
+        const float4 b = *(const float4*)(u[q] + (in[q] && two ? 4 : 0));
+        f[q][0] = a.x; f[q][1] = a.y; f[q][2] = a.z; f[q][3] = a.w;
+        f[q][4] = two ? b.x : 0.0f; f[q][5] = two ? b.y : 0.0f;
+        f[q][6] = two ? b.z : 0.0f; f[q][7] = two ? b.w : 0.0f;
+      }
+    } else {  // rows of any length
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         const int i = min(i0 + q * 256, items - 1), left = p.K - 8 * (i % ch);
@@ -1320,9 +1331,10 @@ ExpandPlan expand_plan(int T, int n, bool grouped, int K, int nout) {
     c.osplit = w < most ? w : most;
   } else {
     c.ks = K <= 32 ? 1 : (K <= 64 ? 2 : (K <= 128 ? 4 : 8));
-    c.mb = c.ks < 8 && T >= 128 * groups ? 2 : 1;
-    c.tiles = row_tiles(T, n, grouped, 64 * c.mb);
     const int stages = div_up(nout, c.ks >= 4 ? 128 : 512 / c.ks);
+    // 128 rows a tile halve the weights' way through LDS; 64 where that leaves CUs idle
+    c.mb = c.ks < 8 && T >= 128 * groups && row_tiles(T, n, grouped, 128) * stages >= 512 ? 2 : 1;
+    c.tiles = row_tiles(T, n, grouped, 64 * c.mb);
     const int w = c.tiles > 0 ? 512 / c.tiles : 1;  // one round of workgroups, 2 a CU
     c.osplit = w < 1 ? 1 : (w < stages ? w : stages);
   }
