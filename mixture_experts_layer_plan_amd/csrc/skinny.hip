@@ -114,8 +114,9 @@ MOE_DEV bool skinny_tile(const int32_t* counts, int n, int T, int bm, int tile, 
   return t.rows > 0;
 }
 
-// Workgroup i runs on XCD i mod 8: give each XCD a contiguous run of the work, so that
-// the column blocks and K parts of a row tile share that XCD's L2.
+// Workgroup i runs on XCD i mod 8: give each XCD a contiguous run of the work, so that the
+// column blocks and K parts of a row tile share that XCD's L2 (for work of one size; tiles
+// that turn out empty would leave the last XCD idle).
 MOE_DEV int xcd_order(int id, int total) {
   const int per = total / N_XCD, rem = total % N_XCD, x = id % N_XCD, local = id / N_XCD;
   return x < rem ? x * (per + 1) + local : rem * (per + 1) + (x - rem) * per + local;
@@ -206,13 +207,20 @@ __global__ __launch_bounds__(512) void dot_kernel(DotArgs p) {
   for (int j = 0; j < NB; ++j) put4(o, n0 + 16 * j + 4 * (lane >> 4), p.N, acc[j]);
 }
 
-// Many rows: a workgroup of 4 wavefronts forms 64 rows x BN columns over one of S parts of
-// K.  Both operands reach LDS by direct loads of K2-byte row pieces, 16 bytes a lane, into
-// a ring of NS stages; the product of a stage runs while NS - 1 more are in flight.
-// Fragments loaded from memory without LDS took 121 us for the 8192 x 256 x 7168 router
-// product: 16 lanes in 16 rows keep the address unit busy for 64 cycles a KiB.
-// Row r's 16-byte chunk c lies at r * K2 + 16 (c ^ swz(r)): the 16 rows of a fragment read
-// hit all 64 banks.
+// Many rows: a workgroup forms BM rows x BN columns over one of S parts of K, S chosen to
+// fill the chip.  Both operands reach LDS by direct loads of K2-byte row pieces, 16 bytes a
+// lane, into a ring of NS stages; the product of a stage runs while NS - 1 more are in
+// flight.  Row r's 16-byte chunk c lies at r * K2 + 16 (c ^ swz(r)): the 16 rows of a
+// fragment read hit all 64 banks.
+// Measured: fragments loaded from memory without LDS took 121 us for the 8192 x 256 x 7168
+// router product (16 lanes in 16 rows keep the address unit busy for 64 cycles a KiB), 64 x
+// 128 tiles 53 us, 128 x 128 tiles with two sets of wavefronts 45 us and 6.5 us for the sum
+// of the two parts; bound by the LDS reads and the waits around them, not by the direct
+// loads (a deeper ring changes nothing).  Rank 64 over 8192 rows of 7168 (117 MB): 33 to 37
+// us against 20 to 31 us for the plain read, as much as the writes of the kernel before
+// still have to leave the Infinity Cache; the rest is the start of the workgroups (about 9
+// us for one stage).  S = 3 there: with 2 parts the tiles do not spread evenly (43 us), and
+// each further part costs the second product 1 to 2 us.
 template <int BM, int BN>
 struct DotTile {
   static constexpr int WN = BN >= 64 ? 2 : 1, WM = 4 / WN;  // wavefronts along columns, rows
@@ -414,9 +422,10 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict_
   out[i] = v;
 }
 
-// The dot of a few tokens (at most TB): a workgroup per column, its row of b read once
-// and multiplied with every token's, without matrix instructions (which would leave
-// 16 - T of 16 rows idle and need a second launch to join the parts of K).
+// The dot of a few tokens (at most TB): a workgroup per column, its row of b read once and
+// multiplied with every token's, without matrix instructions (which would leave 16 - T of 16
+// rows idle and need a second launch to join the parts of K).  One token, 256 x 7168: 2.8 us
+// against 5.3 + 4.0 us; 3.7 MB, so the launch and one round trip to memory are all of it.
 template <int TB>
 __global__ __launch_bounds__(256) void dot_few_kernel(DotArgs p) {
   __shared__ float part[4][TB];
@@ -606,10 +615,12 @@ MOE_DEV void copy_ungrouped(const ExpandArgs& p, int b) {
 // stands for output column 8 i + f of a 128-column block: a lane ends with 8 neighbouring
 // outputs of 4 rows, and 16 lanes with 256 bytes of one row, so that base and y move in
 // whole lines without a trip through LDS.  (With the weights as the M side a store's 16
-// lanes lie in 16 rows: 92 us against 53 us for 8192 rows of 7168 at rank 64.)
+// lanes lie in 16 rows: 92 us against 57 us for 8192 rows of 7168 at rank 64.)
 
 // Few rows (16 MB a tile): each wavefront takes 128-column blocks of one of `osplit` parts
-// of the columns; the weights come straight from memory, one K step of 32 ahead.
+// of the columns; the weights come straight from memory, one K step of 32 ahead.  Bound by
+// its chain of dependent loads (the group, its tokens and parts of u, base): 5.5 us for one
+// token, 6.5 us for 96 tokens of 32 adapters (rank 16, 2048 columns).
 template <int MB, bool NN, bool GR>
 __global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs p) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -731,9 +742,15 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs p) {
 // Many rows (64 MB a tile, 16 MB a wavefront): u stays in registers (KS K steps of 32) and
 // the weights of SB column blocks pass through LDS in fragment order, shared by the four
 // wavefronts, double-buffered: loaded from memory in whole lines while the blocks before
-// are multiplied, turned in registers (NN) or by where they are written (NT).  base is read
-// where it is needed: reading it a block ahead, between the stores, took the plain copy of
-// this pattern from 48 us (8192 x 7168) to 73, and to 90 four blocks ahead.
+// are multiplied, turned in registers (NN) or by where they are written (NT).  K over 128
+// (the router's dx) passes in halves of 128 with 64-row tiles, so that two workgroups fit a
+// CU (58 us with all of K in LDS and one, 45 us with two; T = 4096, H = 7168, E = 256).
+// Every load and store of the loop is a buffer access whose range does the masking: with
+// branches around them the compiler waits for all that is in flight, stores included, which
+// took a plain copy of this pattern from 48 to 73 us (8192 x 7168).
+// 8192 rows of 7168 at rank 64: 56 to 57 us for 235 MB, against 45 to 48 us for that copy;
+// the router's dx is bound by its LDS reads (every fragment is read by four wavefronts) and
+// by the start of its workgroups, which put 64 rows of d_logits in LDS first (15 us).
 template <int MB, int KS, bool NN, bool GR>
 __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(ExpandArgs p) {
   constexpr int SB = KS >= 4 ? 1 : 4 / KS;  // column blocks of a stage
@@ -936,8 +953,10 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
 // 32-row tiles, whose sums are joined in LDS at the end.  Both operands reach LDS by direct
 // loads into a ring of 32-row tiles, x as whole 256-byte pieces of its rows, the short one
 // as the halves that `expand` left in fragment order, so that enough is in flight without
-// registers (with both in registers one tile ahead: 88 us against 235 MB of x and dy).  A
-// lane reads 8 rows of 8 columns and turns them in registers into 8 fragments along the
+// registers (8192 rows of 7168 at rank 64, x and dy: 235 MB in 58 us; with both in registers
+// one tile ahead 88 us).  The router's (256 x 7168 over 4096 rows) takes 38 us, bound by its
+// LDS reads and the turning, which eight wavefronts repeat for 32 rows of j each; 64 rows
+// each leave one wavefront a SIMD and take 46 us.  A lane reads 8 rows of 8 columns and turns them in registers into 8 fragments along the
 // rows; row i of fragment f stands for column 8 i + f.  With the halves as the M side a lane
 // ends with 4 neighbouring j of 8 neighbouring h: it stores 8 h of a row (16 lanes: 128 of
 // them) for [J][H], 4 j for [H][J] (TR).
@@ -946,7 +965,7 @@ struct WgradTile {
   static constexpr int WK = 4 / WJ, JB = JT * WJ;       // 16-row blocks of j
   static constexpr int UB = JB < 2 ? 4096 : JB * 2048;  // bytes of halves a tile
   static constexpr int STAGE = WK * (8192 + UB);        // a tile for each wavefront along K
-  static constexpr int NS = 3;  // 76, 52, 76 KiB with the tokens: 2, 3, 2 a CU
+  static constexpr int NS = STAGE <= 16384 ? 4 : 3;  // 76, 68, 76 KiB with the tokens: 2 a CU
   static constexpr int LOADS = WK * (2 + UB / 4096);    // per wavefront and stage
   static constexpr int TOK = 4 * WGRAD_MAX_CHUNK;
   static constexpr int LDS = NS * STAGE + TOK;
@@ -1288,9 +1307,20 @@ SkinnyPlan skinny_plan(int T, int n, bool grouped, int K, int N) {
   const int wg = c.tiles * div_up(N, c.bn);
   // at least two steps of each of 8 wavefronts, or a ring's stages
   const int most = div_up(K, c.tile ? 512 : 1024);
-  const int target = c.tile && c.bn == 128 ? 256 : 512;
-  int want = wg > 0 ? div_up(target, wg) : 1;
-  if (want > 8) want = 8;  // every part is read again by the second product
+  int want = 1;  // at most 8: every part is read again by the second product
+  if (c.bm == 128) {
+    // One workgroup a CU: whole rounds of 256, against the sum of the parts, which takes
+    // about 1/64 of a round for each part of 64 tiles (4096 x 384 x 7168: 59 -> 44 us).
+    float least = 0.0f;
+    for (int S = 1; S <= 8; ++S) {
+      const float cost = (float)div_up(wg * S, 256) / S + (float)wg * S / 4096;
+      if (S == 1 || cost < least) least = cost, want = S;
+    }
+  } else {
+    const int target = c.tile ? (c.bn == 128 ? 256 : 384) : 512;
+    want = wg > 0 ? div_up(target, wg) : 1;
+    if (want > 8) want = 8;
+  }
   c.S = c.few ? 1 : (want < most ? want : most);
   return c;
 }
