@@ -217,14 +217,14 @@ moe_status moe_router_backward_f32(const moe_shape* shape, const float* x,
  * experts and s_e = sigmoid(l_e) (MOE_SCORE_SIGMOID) or the softmax of l over all E
  * experts (MOE_SCORE_SOFTMAX), the choice value of an expert is c_e = s_e + bias_e.
  * The experts form n_groups groups of E / n_groups neighbours; a group's score is the
- * sum of its group_top largest c (1 or 2; of fewer where it has fewer experts in
- * play), the topk_groups best groups stay, and the k largest c of their experts are
+ * sum of its group_top largest c (1 or 2; of fewer where fewer of its experts are in
+ * play with a bias above -inf), the topk_groups best groups stay, and the k largest c of their experts are
  * chosen, in descending order; ties go to the lowest group and to the lowest id.
  * The weight of a chosen expert is scale * s_e, divided by the sum of the chosen s if
  * renormalise is set: the bias moves the choice alone, as balancing the experts' load
- * needs, not the output.
+ * needs, not the output; a bias of -inf makes an expert the last choice.
  * Limits: n_groups <= 64 and a divisor of E, 1 <= topk_groups <= n_groups,
- * k <= topk_groups * E / n_groups, scale finite. */
+ * k <= topk_groups * E / n_groups, scale finite; T below 2^26 (MOE_E_UNSUPPORTED). */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 typedef struct {
   int32_t score; /* moe_score */
@@ -262,7 +262,9 @@ moe_status moe_route_scored_backward(const moe_shape* shape, const moe_scoring* 
 
 /* The router projection of the bf16 and MXFP8 layers: logits [T, E] (fp32) = x [T, H]
  * (bf16) * w_router [E, H]^T (bf16), products and sums in fp32.  T * H * 2 and
- * E * H * 2 bytes below 4 GiB, as in the layer calls (MOE_E_UNSUPPORTED otherwise).
+ * E * H * 2 bytes, E rounded up to 128, below 4 GiB, as in the layer calls
+ * (MOE_E_UNSUPPORTED otherwise).  Here and below the order of a sum depends on the sizes,
+ * T among them, and on nothing else.
  * ws [ws_bytes >= moe_router_workspace_bytes(shape, 0)] (may be NULL if that is 0). */
 moe_status moe_router_logits_bf16(const moe_shape* shape, const void* x, const void* w_router,
                                   float* logits, void* ws, size_t ws_bytes, hipStream_t stream);
@@ -484,7 +486,8 @@ moe_status moe_backward_mxfp8(const moe_shape* shape, const void* plan, const vo
  * layer that the adapters stand beside.
  *   T tokens, H_in, H_out: multiples of 8; n_adapters in [1, 1024]; rank: a multiple of
  *   8 in [8, 128] (pad smaller ranks with zero rows of A and zero columns of B);
- *   max(T, rank) * max(H_in, H_out) * 2 bytes below 4 GiB (MOE_E_UNSUPPORTED otherwise).
+ *   max(T, 128) * max(H_in, H_out) * 2 bytes below 4 GiB and T below 2^26
+ *   (MOE_E_UNSUPPORTED otherwise).
  *   lora_a bf16 [n_adapters, rank, H_in], lora_b bf16 [n_adapters, H_out, rank],
  *   scale fp32 [n_adapters]. */
 typedef struct {

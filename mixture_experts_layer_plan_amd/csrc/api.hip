@@ -923,8 +923,12 @@ moe_status scratch_of_current_device(void** out) {
 
 // ------------------------------------------------------- router projection, adapters
 
+// A wavefront a token in one launch: T * 64 threads below 2^32.
+constexpr int MAX_WAVE_ROWS = 1 << 26;
+
 moe_status check_scoring(const moe_shape* s, const moe_scoring* sc) {
   if (!sc) return MOE_E_NULL;
+  if (s->T >= MAX_WAVE_ROWS) return MOE_E_UNSUPPORTED;
   if (sc->score != MOE_SCORE_SOFTMAX && sc->score != MOE_SCORE_SIGMOID) return MOE_E_SHAPE;
   if (sc->n_groups < 1 || sc->n_groups > 64 || s->E % sc->n_groups) return MOE_E_SHAPE;
   if (sc->topk_groups < 1 || sc->topk_groups > sc->n_groups) return MOE_E_SHAPE;
@@ -969,7 +973,9 @@ moe_status check_router(const moe_shape* s) {
   one.k = 1;  // k, I and the minibatches are not the router's
   const moe_status rc = check_shape(&one, false);
   if (rc != MOE_OK) return rc;
-  const uint64_t rows = std::max(s->T, s->E);  // 32-bit byte offsets into x, dx and the weights
+  // 32-bit byte offsets into x, dx and the weights, whose last K step of 32 to 128 rows is
+  // addressed whole
+  const uint64_t rows = std::max(s->T, (s->E + 127) / 128 * 128);
   return rows * s->H * 2 < 1ull << 32 ? MOE_OK : MOE_E_UNSUPPORTED;
 }
 
@@ -978,7 +984,8 @@ moe_status check_lora(const moe_lora_shape* s) {
   if (s->T < 0 || s->n_adapters < 1 || s->n_adapters > MOE_MAX_E) return MOE_E_SHAPE;
   if (s->H_in < 8 || s->H_in % 8 || s->H_out < 8 || s->H_out % 8) return MOE_E_SHAPE;
   if (s->rank < 8 || s->rank > 128 || s->rank % 8) return MOE_E_SHAPE;
-  const uint64_t rows = std::max(s->T, s->rank);  // 32-bit byte offsets, as in the layer calls
+  if (s->T >= MAX_WAVE_ROWS) return MOE_E_UNSUPPORTED;
+  const uint64_t rows = std::max(s->T, 128);  // 32-bit byte offsets, as in check_router
   if (rows * (uint64_t)std::max(s->H_in, s->H_out) * 2 >= 1ull << 32) return MOE_E_UNSUPPORTED;
   return MOE_OK;
 }

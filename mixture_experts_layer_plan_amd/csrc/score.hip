@@ -81,8 +81,8 @@ MOE_DEV double wave_sum_f64(double v) {
 
 // exp(x) for x <= 0 in double, of N values at once (the constants are loaded once):
 // x = n ln 2 + r with |r| <= ln 2 / 2, the Taylor series of exp(r) to r^13 / 13! (the rest
-// is below 2^-57), scaled by 2^n.  Below -700, where a score is zero to double precision
-// beside any other choice value, 0.
+// is below 2^-57), scaled by 2^n (down to the subnormals).  Below -746, past the smallest
+// double, 0.
 template <int N>
 MOE_DEV void exp_neg(double (&x)[N]) {
   constexpr double C[14] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040,
@@ -103,7 +103,7 @@ MOE_DEV void exp_neg(double (&x)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const double e = ldexp(p[i], (int)n[i]);
-    x[i] = x[i] < -700.0 ? 0.0 : e;
+    x[i] = x[i] < -746.0 ? 0.0 : e;
   }
 }
 
@@ -211,10 +211,17 @@ MOE_DEV void row_softmax_stats(const float (&l)[NPL], float& top, float& sum) {
   sum = dpp_sum_f32(z);
 }
 
-// MODE 0: the logits decide; 1, 2: choice values of sigmoid, softmax scores, in double.  A choice that rounds is a choice that
-// may differ: near the border of the top k two fp32 scores are often equal where the
-// scores are not.  Without bias and groups both score functions keep the order of the
-// logits, which then decide, exactly, without forming a score.
+// MODE 0: the logits decide; 1, 2: choice values of sigmoid, softmax scores, in double.  A
+// choice that rounds is a choice that may differ: near the border of the top k two fp32
+// scores are often equal where the scores are not.  Without bias and groups both score
+// functions keep the order of the logits, which then decide, exactly, without forming a
+// score.
+// Bound by the vector unit, not by memory: one token 4.5 us, of which the launch is half and
+// the rest a chain (row, exp, group scores, k maxima of 64 lanes); 8192 tokens of 256
+// experts in 8 groups, k = 8: 13 us for 8.9 MB, where the double exp is a third and the k
+// rounds of the choice most of the rest.  The order-preserving integer keys are why a
+// maximum is 4 row shifts and not a round trip through LDS a step (20 us), and lanes sorted
+// once why a round looks at one key of each lane.
 template <int NPL, int MODE>
 __global__ __launch_bounds__(256) void route_scored_kernel(const float* __restrict__ logits,
                                                            const float* __restrict__ bias, int T,
@@ -421,7 +428,8 @@ __global__ __launch_bounds__(256) void route_scored_kernel(const float* __restri
 //                          sigmoid scores; 0 elsewhere
 //   sigmoid                g_j s_j (1 - s_j); 0 elsewhere
 //   softmax                s_e (g_e - sum_i s_i g_i) for every expert, g = 0 off the choice
-// The row is put together in LDS and written once.
+// The row is put together in LDS and written once.  8192 x 256, k = 8: 6.8 us for 8.9 MB (a
+// chain as above: the choice, its logits, the sums, the row).
 template <int NPL>
 __global__ __launch_bounds__(256) void route_scored_backward_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,

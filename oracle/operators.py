@@ -34,7 +34,9 @@ def route_scored(logits, k, score="softmax", bias=None, n_groups=1, topk_groups=
         c = {e: (L[t, e] if bias is None and n_groups == 1 else np.exp(ls[e]) + b[e]) for e in play}
         gs = []
         for g in range(n_groups):
-            mem = sorted((c[e] for e in play if e // per == g), reverse=True)[:group_top]
+            # a bias of -inf leaves its expert out of the group's score
+            mem = sorted((c[e] for e in play if e // per == g and c[e] > -np.inf),
+                         reverse=True)[:group_top]
             gs.append((-sum(mem) if mem else np.inf, g))
         kept = {g for _, g in sorted(gs)[:topk_groups]}
         sel = sorted((e for e in play if e // per in kept), key=lambda e: (-c[e], e))[:k]

@@ -133,3 +133,13 @@ def test_layer_options_that_do_not_fit():
     b = LayerBuffers(8, 256, 128, 4, 2, dtype="bf16", device="cpu", router_proj=True,
                      adapters=(2, 8), scoring=B.scoring("sigmoid"))
     assert b.logits.shape == (8, 4) and b.d_lora_b.shape == (2, 256, 8)
+
+
+def test_sizes_past_a_launch_or_32_bit_offsets(L):
+    sc = B.scoring()
+    assert route(L, s_(T=1 << 26, k=1), sc) == UNSUP and route_b(L, s_(T=1 << 26, k=1), sc) == UNSUP
+    # the last K step is addressed whole: ranks and experts count to the next 128
+    s = B.lora_shape(1, 64, 1 << 24, 2, 8)
+    assert lora(L, s, 1 << 40) == UNSUP and lora_b(L, s, 1 << 40) == UNSUP
+    assert lora(L, B.lora_shape(1 << 26, 8, 8, 2, 8), 1 << 40) == UNSUP
+    assert L.moe_router_logits_bf16(ctypes.byref(s_(T=1, E=8, H=1 << 24)), F, F, F, F, 1 << 40, None) == UNSUP

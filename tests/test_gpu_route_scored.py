@@ -242,3 +242,30 @@ def test_replays_in_a_graph_on_another_stream(B):
         B.moe_route_scored_backward(s, sc, v, i2, dw, d2, st)
         st.synchronize()
         assert digest(i2, w2, d2) == got
+
+
+@pytest.mark.parametrize("E,G", [(16, 4), (256, 8), (60, 4), (1024, 32)])
+def test_biases_of_minus_inf(B, E, G):
+    say(f"route_scored bias -inf E={E} G={G}")
+    rng = np.random.default_rng(E)
+    L = rng.standard_normal((50, E))
+    bias = rng.standard_normal(E) * 0.1
+    bias[rng.random(E) < 0.6] = -np.inf
+    bias[:E // G] = -np.inf                       # a whole group
+    bias[E // G:2 * E // G - 1] = -np.inf         # all but one
+    for top in (1, 2):
+        for keep in (1, 2, G):
+            check(B, L, min(8, keep * E // G), bias, score="sigmoid", n_groups=G, topk_groups=keep,
+                  group_top=top)
+
+
+def test_choice_among_scores_near_the_smallest_double(B):
+    """Scores from 1e-300 through the subnormals: still in their order (the logits are 2
+    apart, so that a subnormal of two units differs from its neighbour)."""
+    say("route_scored tiny scores")
+    L = -(690.0 + 2.0 * np.arange(24, dtype=np.float32))[None, ::-1].copy()
+    idx = run(B, L, 6, None, dict(score="sigmoid", n_groups=4, topk_groups=2, group_top=2))[0]
+    assert idx.tolist() == [[23, 22, 21, 20, 19, 18]]
+    M = np.concatenate([L, np.zeros((1, 1)), np.full((1, 23), -np.inf)], 1).astype(np.float32)
+    idx = run(B, M, 5, None, dict(score="softmax", n_groups=4, topk_groups=4))[0]
+    assert idx.tolist() == [[24, 23, 22, 21, 20]]

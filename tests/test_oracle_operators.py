@@ -109,3 +109,15 @@ def test_lora_autograd_and_tokens_without_an_adapter():
     for got, t in zip((dx, da, db), ts):
         np.testing.assert_allclose(got, t.grad.numpy(), rtol=1e-11, atol=1e-14)
     assert not da[1].any() and not db[1].any()
+
+
+def test_a_bias_of_minus_inf_is_the_last_choice():
+    inf = np.inf
+    L = np.zeros((1, 8))
+    b = np.array([0.0, -inf, -1.0, -1.0, -inf, -inf, -2.0, -inf])
+    kw = dict(score="sigmoid", bias=b, n_groups=4, group_top=2)
+    # group scores: 0.5 (one expert left), -1 (two), none, -1.5
+    assert oracle.route_scored(L, 2, topk_groups=1, **kw)[0].tolist() == [[0, 1]]
+    assert oracle.route_scored(L, 4, topk_groups=2, **kw)[0].tolist() == [[0, 2, 3, 1]]
+    idx, w = oracle.route_scored(L, 8, topk_groups=4, **kw)
+    assert idx.tolist() == [[0, 2, 3, 6, 1, 4, 5, 7]] and np.allclose(w, 1 / 8)
