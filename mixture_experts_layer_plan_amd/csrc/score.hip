@@ -216,12 +216,12 @@ MOE_DEV void row_softmax_stats(const float (&l)[NPL], float& top, float& sum) {
 // scores are often equal where the scores are not.  Without bias and groups both score
 // functions keep the order of the logits, which then decide, exactly, without forming a
 // score.
-// Bound by the vector unit, not by memory: one token 4.5 us, of which the launch is half and
-// the rest a chain (row, exp, group scores, k maxima of 64 lanes); 8192 tokens of 256
-// experts in 8 groups, k = 8: 13 us for 8.9 MB, where the double exp is a third and the k
-// rounds of the choice most of the rest.  The order-preserving integer keys are why a
-// maximum is 4 row shifts and not a round trip through LDS a step (20 us), and lanes sorted
-// once why a round looks at one key of each lane.
+// Bound by the vector unit, not by memory: 8192 tokens of 256 experts in 8 groups, k = 8,
+// take 13 us for 8.9 MB and 766 vector instructions a token, whose issue alone is 11.6 us
+// (8 wavefronts a SIMD).  One token: 4.5 us, of which the launch is half and the rest a
+// chain (row, exp, group scores, k maxima of 64 lanes).  Row shifts for the maxima instead
+// of a round trip through LDS a step, lanes sorted once so that a round looks at one key of
+// each, and the vectorised exp took it there from 20 us (and 7.6 us).
 template <int NPL, int MODE>
 __global__ __launch_bounds__(256) void route_scored_kernel(const float* __restrict__ logits,
                                                            const float* __restrict__ bias, int T,

@@ -215,12 +215,16 @@ __global__ __launch_bounds__(512) void dot_kernel(DotArgs p) {
 // Measured: fragments loaded from memory without LDS took 121 us for the 8192 x 256 x 7168
 // router product (16 lanes in 16 rows keep the address unit busy for 64 cycles a KiB), 64 x
 // 128 tiles 53 us, 128 x 128 tiles with two sets of wavefronts 45 us and 6.5 us for the sum
-// of the two parts; bound by the LDS reads and the waits around them, not by the direct
-// loads (a deeper ring changes nothing).  Rank 64 over 8192 rows of 7168 (117 MB): 33 to 37
-// us against 20 to 31 us for the plain read, as much as the writes of the kernel before
-// still have to leave the Infinity Cache; the rest is the start of the workgroups (about 9
-// us for one stage).  S = 3 there: with 2 parts the tiles do not spread evenly (43 us), and
-// each further part costs the second product 1 to 2 us.
+// of the two parts.  Bound by what passes through a CU's L1: the direct loads alone, without
+// a product or a store, take 39 us, x alone 23 us and the weights, which come from L2, 12 us
+// (each 64 rows x 128 columns less of tile costs 235 MB more and 13 us); fragments read one
+// step ahead of their products, 3 or 5 stages, and K from another start in each tile change
+// nothing.  128 x 256 tiles with 4 parts would save 4 us of loads and cost 4 us of parts.
+// Rank 64 over 8192 rows of 7168 (117 MB): 33 to 37 us against 20 to 31 us for the plain
+// read, as much as the writes of the kernel before still have to leave the Infinity Cache;
+// the rest is the start of the workgroups (about 9 us for one stage).  S = 3 there: with 2
+// parts the tiles do not spread evenly (43 us), and each further part costs the second
+// product 1 to 2 us.
 template <int BM, int BN>
 struct DotTile {
   static constexpr int WN = BN >= 64 ? 2 : 1, WM = 4 / WN;  // wavefronts along columns, rows
@@ -411,7 +415,8 @@ __global__ __launch_bounds__((DotTile<BM, BN>::NT)) void dot_tile_kernel(DotArgs
     }
 }
 
-// out[i] = sum over the S parts, in order
+// out[i] = sum over the S parts, in order.  Bound by memory: 25 MB in 6.5 us (8192 x 256, two
+// parts), 21 MB in 5.2 us.
 __global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict__ parts, int S,
                                                         size_t n, float* __restrict__ out) {
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
@@ -512,7 +517,7 @@ MOE_DEV void store_halves(const char* lds, int lo_off, int kp, int K, const Skin
 
 // u of a row tile into LDS: its S parts summed, scaled and split, zeros past K and past
 // the tile's rows; kp = K rounded up to 32.
-// Q pieces of 8 and U parts are in flight at a time.
+// Q pieces of 8 and U parts are in flight at a time: one wait for memory, not one a part.
 template <int ROWS, int Q, int U>
 MOE_DEV void fill_u(const ExpandArgs& p, const SkinnyTile& t, int kp, char* lds) {
   const float sc = p.scale ? p.scale[t.a] : 1.0f;
@@ -956,7 +961,8 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
 // registers (8192 rows of 7168 at rank 64, x and dy: 235 MB in 58 us; with both in registers
 // one tile ahead 88 us).  The router's (256 x 7168 over 4096 rows) takes 38 us, bound by its
 // LDS reads and the turning, which eight wavefronts repeat for 32 rows of j each; 64 rows
-// each leave one wavefront a SIMD and take 46 us.  A lane reads 8 rows of 8 columns and turns them in registers into 8 fragments along the
+// each leave one wavefront a SIMD and take 46 us.  A lane reads 8 rows of 8 columns and
+// turns them in registers into 8 fragments along the
 // rows; row i of fragment f stands for column 8 i + f.  With the halves as the M side a lane
 // ends with 4 neighbouring j of 8 neighbouring h: it stores 8 h of a row (16 lanes: 128 of
 // them) for [J][H], 4 j for [H][J] (TR).
@@ -1169,6 +1175,7 @@ __global__ __launch_bounds__(256) void wgrad_kernel(WgradArgs p) {
 }
 
 // Gradients of the groups with several chunks: the sum of the chunks' parts, in order.
+// Bound by memory: 256 x 7168, 4 parts, 33 MB in 6.3 us.
 template <bool GR>
 __global__ __launch_bounds__(256) void wgrad_sum_kernel(WgradArgs p) {
   const WgradSide d = p.side[blockIdx.z];
@@ -1196,7 +1203,9 @@ __global__ __launch_bounds__(256) void wgrad_sum_kernel(WgradArgs p) {
 }
 
 // ------------------------------------------------------------------- transpose
-// dst [n][C][R] = src [n][R][C] transposed (R and C multiples of 8); 64 x 64 tiles.
+// dst [n][C][R] = src [n][R][C] transposed (R and C multiples of 8); 64 x 64 tiles, rows of
+// 66 values in LDS so that a column's reads spread over the banks.  8 x 7168 x 64: 4.7 us,
+// half of it the launch.
 __global__ __launch_bounds__(256) void transpose_kernel(const bf16_t* __restrict__ src_all,
                                                         bf16_t* __restrict__ dst_all, int R, int C) {
   __shared__ bf16_t t[64][66];
@@ -1310,7 +1319,7 @@ SkinnyPlan skinny_plan(int T, int n, bool grouped, int K, int N) {
   int want = 1;  // at most 8: every part is read again by the second product
   if (c.bm == 128) {
     // One workgroup a CU: whole rounds of 256, against the sum of the parts, which takes
-    // about 1/64 of a round for each part of 64 tiles (4096 x 384 x 7168: 59 -> 44 us).
+    // about 1/64 of a round for each part of 64 tiles (4096 x 384 x 7168: 59 -> 49 us).
     float least = 0.0f;
     for (int S = 1; S <= 8; ++S) {
       const float cost = (float)div_up(wg * S, 256) / S + (float)wg * S / 4096;
