@@ -508,7 +508,8 @@ size_t moe_lora_saved_bytes(const moe_lora_shape* shape);
 size_t moe_lora_workspace_bytes(const moe_lora_shape* shape, int backward);
 
 /* Forward.  base bf16 [T, H_out], or NULL (zero), may be y itself: rows of tokens
- * without an adapter are then left as they are, otherwise they get their base.  Both
+ * without an adapter are then left as they are, otherwise they get their base; y may not
+ * be x (MOE_E_UNSUPPORTED).  Both
  * products are summed in fp32, u = A x is kept to 16 bits of mantissa between them, and
  * y bf16 [T, H_out] is rounded once.  Where x, A or B is not finite, neither are the
  * results it enters (inf or NaN); a token without an adapter may hold anything.

@@ -1001,7 +1001,8 @@ moe_shape lora_plan_shape(const moe_lora_shape* s) {
 }
 
 // forward: the K parts of u; backward: the K parts of v, B transposed, the halves of v
-// along the rows, the chunks' parts of dA and dB
+// along the rows, the chunks' parts of dA and dB.  (One launch for both products leaves the
+// parts unused.)
 struct LoraWs {
   size_t parts, bt, vt, pa, pb, total;
   int chunk;
@@ -1043,7 +1044,7 @@ moe_status lora_pair(const moe_lora_shape* s, const PlanView& v, const void* x, 
   d.N = s->rank;
   d.S = p.S;
   d.R = s->T;
-  MOE_TRY(launch_dot(dot_name, d, p, st));
+  if (!p.fused) MOE_TRY(launch_dot(dot_name, d, p, st));
   ExpandArgs e;
   e.u = parts;
   e.w = (const bf16_t_host*)second;
@@ -1059,10 +1060,14 @@ moe_status lora_pair(const moe_lora_shape* s, const PlanView& v, const void* x, 
   e.K = s->rank;
   e.S = p.S;
   e.nout = nout;
+  e.R = s->T;
+  if (p.fused) {
+    MOE_TRY(launch_dot_expand(expand_name, d, e, nn, st));
+    return MOE_OK;
+  }
   const ExpandPlan c = expand_plan(s->T, s->n_adapters, true, s->rank, nout);
   e.max_tiles = c.tiles;
   e.osplit = c.osplit;
-  e.R = s->T;
   MOE_TRY(launch_expand(expand_name, e, c, nn, st));
   return MOE_OK;
 }
@@ -1474,6 +1479,7 @@ moe_status moe_lora_bf16(const moe_lora_shape* s, const void* plan, const void* 
   const LoraWs W = lora_ws(s, false);
   if (ws_bytes < W.total) return MOE_E_WORKSPACE;
   if (s->T == 0) return MOE_OK;
+  if (y == x) return MOE_E_UNSUPPORTED;  // rows of x are read beside y's being written
   const moe_shape ps = lora_plan_shape(s);
   return lora_pair(s, view_plan(&ps, plan), x, s->H_in, lora_a, "lora_shrink", lora_b, false,
                    s->H_out, "lora_expand", scale, base, y, at<float>(ws, W.parts), saved, st);

@@ -487,13 +487,13 @@ MOE_DEV void transpose8(const uint4 (&r)[8], uint4 (&c)[8]) {
 // The halves of u along the rows, in the order of wgrad's fragments (K = 32 rows):
 // [32-row tile][16 values of j][hi, lo][lane: j = lane % 16, rows 8 (lane / 16) .. + 7][8].
 // Rows past the group's last, up to its last tile's end, are zero.
-template <int MB>
+template <int MB, int NT = 256>
 MOE_DEV void store_halves(const char* lds, int lo_off, int kp, int K, const SkinnyTile& t,
                           int part, int parts, bf16_t* __restrict__ ut) {
   const int jb = (K + 15) / 16;
   const bool pad = t.off + 16 * MB >= t.count;  // the last tile: zeros up to a multiple of 32
   const int groups = pad ? (((t.off + t.rows + 31) >> 5 << 5) - t.off) / 8 : 2 * MB;
-  for (int i = (threadIdx.x >> 4) + 16 * part; i < groups * jb; i += 16 * parts) {
+  for (int i = (threadIdx.x >> 4) + NT / 16 * part; i < groups * jb; i += NT / 16 * parts) {
     const int q = i / jb, j = (i - q * jb) * 16 + (threadIdx.x & 15), g8 = (t.off >> 3) + q;
     uint32_t w[2][4];
 #pragma unroll
@@ -599,9 +599,8 @@ MOE_DEV void fill_u(const ExpandArgs& p, const SkinnyTile& t, int kp, char* lds)
 }
 
 // Rows without a group: the base alone, a token per wavefront, 8 KiB in flight.
-constexpr int COPY_TOKENS = 4;
 MOE_DEV void copy_ungrouped(const ExpandArgs& p, int b) {
-  const int lane = threadIdx.x & 63, tok = b * COPY_TOKENS + (int)(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, tok = b * (int)(blockDim.x >> 6) + (int)(threadIdx.x >> 6);
   if (tok >= p.T || p.pos[tok] >= 0) return;
   const size_t o = (size_t)tok * p.nout;
 #pragma unroll 1
@@ -624,19 +623,12 @@ MOE_DEV void copy_ungrouped(const ExpandArgs& p, int b) {
 
 // Few rows (16 MB a tile): each wavefront takes 128-column blocks of one of `osplit` parts
 // of the columns; the weights come straight from memory, one K step of 32 ahead.  Bound by
-// its chain of dependent loads (the group, its tokens and parts of u, base): 5.5 us for one
-// token, 6.5 us for 96 tokens of 32 adapters (rank 16, 2048 columns).
-template <int MB, bool NN, bool GR>
-__global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs p) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
+// its chain of dependent loads (the group, its tokens and parts of u, base): both products of
+// 96 tokens of 32 adapters take 14 us (rank 32, 7168 to 2048 columns), half of it here.
+// `fill` puts u's halves into LDS (as fill_u) by way of all NW wavefronts.
+template <int MB, bool NN, bool GR, int NW, class F>
+MOE_DEV void expand_columns(const ExpandArgs& p, const SkinnyTile& t, int oz, char* lds, const F& fill) {
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  if (GR && (int)blockIdx.x >= p.max_tiles * p.osplit) {
-    copy_ungrouped(p, blockIdx.x - p.max_tiles * p.osplit);
-    return;
-  }
-  const int tile = blockIdx.x / p.osplit, oz = blockIdx.x % p.osplit;
-  SkinnyTile t;
-  if (!skinny_tile<GR>(p.counts, p.n, p.T, 16 * MB, tile, t)) return;
   const int ksteps = (p.K + 31) / 32, kp = 32 * ksteps, lo_off = 16 * MB * kp * 2;
   const int g = lane >> 4, rho = lane & 15;
   size_t rowo[MB][4];
@@ -680,10 +672,10 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs p) {
     load_base(c, bs);  // later blocks': at their start, after the stores before them
   }
   bool first = true;
-  fill_u<16 * MB, GR ? 1 : 2, GR ? 8 : 1>(p, t, kp, lds);
+  fill(kp);
   __syncthreads();
-  if (p.ut) store_halves<MB>(lds, lo_off, kp, p.K, t, oz, p.osplit, p.ut);
-  for (; c < c1; c += 4) {
+  if (p.ut) store_halves<MB, 64 * NW>(lds, lo_off, kp, p.K, t, oz, p.osplit, p.ut);
+  for (; c < c1; c += NW) {
     if (!first) load_base(c, bs);
     first = false;
     f32x4v acc[MB][8];
@@ -714,14 +706,14 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs p) {
         for (int m = 0; m < MB; ++m) acc[m][f] = mfma16(h[m], as_frag(w[f]), acc[m][f]);
       }
     };
-    const bool more = c + 4 < c1;
+    const bool more = c + NW < c1;
     for (int ks = 0; ks < ksteps; ks += 2) {
       if (ks + 1 < ksteps) load_w(c, ks + 1, wf1);
-      else if (more) load_w(c + 4, 0, wf1);
+      else if (more) load_w(c + NW, 0, wf1);
       step(ks, wf0);
       if (ks + 1 < ksteps) {
         if (ks + 2 < ksteps) load_w(c, ks + 2, wf0);
-        else if (more) load_w(c + 4, 0, wf0);
+        else if (more) load_w(c + NW, 0, wf0);
         step(ks + 1, wf1);
       } else {
 #pragma unroll
@@ -742,6 +734,121 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs p) {
         }
     }
   }
+}
+
+template <int MB, bool NN, bool GR>
+__global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs p) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  if (GR && (int)blockIdx.x >= p.max_tiles * p.osplit) {
+    copy_ungrouped(p, blockIdx.x - p.max_tiles * p.osplit);
+    return;
+  }
+  const int tile = blockIdx.x / p.osplit, oz = blockIdx.x % p.osplit;
+  SkinnyTile t;
+  if (!skinny_tile<GR>(p.counts, p.n, p.T, 16 * MB, tile, t)) return;
+  expand_columns<MB, NN, GR, 4>(p, t, oz, lds, [&](int kp) {
+    fill_u<16 * MB, GR ? 1 : 2, GR ? 8 : 1>(p, t, kp, lds);
+  });
+}
+
+// Both products of few grouped rows in one launch (rank <= 16): every workgroup of a 16-row
+// tile forms the tile's u anew and then its part of the columns.  The tile's rows of a and the
+// group's of b come as whole KiB by direct loads into a ring of 512-deep stages, of which each
+// of the 8 wavefronts takes two K steps (fragments straight from memory keep the address unit
+// busy: 13 us for one token).  Bound by the chain of its stages, 14 of about 0.4 us for 7168
+// (a ring of 7 is no faster).  Against the two launches, in a captured graph, 7168 columns in:
+// one token 9.4 and 9.1 us (2048: 6.5 and 7.7), 96 tokens of 32 adapters 10.6 and 11.7 us, 256
+// of 64 18.9 and 24.6, 1000 of 100 (4096) 18.6 and 24.5; called one by one it also saves the
+// host's second launch.  Rank 32 lost for few tiles (one token 11.6 and 10.8 us).
+constexpr int DOT_EXPAND_STAGE = 32768, DOT_EXPAND_STAGES = 4, DOT_EXPAND_U = 2048;
+template <bool NN>
+__global__ __launch_bounds__(512) void dot_expand_kernel(DotArgs d, ExpandArgs p) {
+  constexpr int NW = 8, NS = DOT_EXPAND_STAGES;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  if ((int)blockIdx.x >= p.max_tiles * p.osplit) {
+    copy_ungrouped(p, blockIdx.x - p.max_tiles * p.osplit);
+    return;
+  }
+  const int tile = blockIdx.x / p.osplit, oz = blockIdx.x % p.osplit;
+  SkinnyTile t;
+  if (!skinny_tile<true>(p.counts, p.n, p.T, 16, tile, t)) return;
+  char* ring = lds + DOT_EXPAND_U;  // behind u's halves
+  expand_columns<1, NN, true, NW>(p, t, oz, lds, [&](int kp) {
+    const uint32_t K2 = (uint32_t)d.K * 2;
+    const rsrc_t ra = make_rsrc(d.a, (uint32_t)d.T * K2);  // below 4 GiB
+    const rsrc_t rb = make_rsrc(d.b + (size_t)t.a * d.N * d.K, (uint32_t)d.N * K2);
+    // this wavefront's rows, wv and wv + 8: nx of a's are the tile's.  A stage: 16 rows of a
+    // (those past the tile are not loaded), 16 of b; chunk c of row r lies at c ^ r.
+    const int nx = (wv < t.rows) + (wv + 8 < t.rows);
+    uint32_t xo[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      xo[q] = (uint32_t)d.src_token[t.row0 + min(wv + 8 * q, t.rows - 1)] * K2;
+    const int stages = (d.K + 511) / 512;
+    const auto issue = [&](int i) {
+      char* st = ring + (i % NS) * DOT_EXPAND_STAGE;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int r = wv + 8 * q;
+        const uint32_t k2 = (uint32_t)i * 1024 + ((lane ^ r) << 4);
+        if (q < nx) dma16_buf(ra, k2 < K2 ? xo[q] + k2 : 0xffffffffu, 0u, st + r * 1024);
+        dma16_buf(rb, k2 < K2 && r < d.N ? (uint32_t)r * K2 + k2 : 0xffffffffu, 0u,
+                  st + 16384 + r * 1024);
+      }
+    };
+    const auto wait = [&](int ahead) {  // 2 + nx loads a stage
+      if (nx == 0) ring_wait_for<2>(ahead);
+      else if (nx == 1) ring_wait_for<3>(ahead);
+      else ring_wait_for<4>(ahead);
+    };
+    const int g = lane >> 4, m = lane & 15, mr = min(m, t.rows - 1);  // past the tile: its last row
+    f32x4v acc = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < NS - 1 && i < stages; ++i) issue(i);
+    for (int i = 0; i < stages; ++i) {
+      wait(min(NS - 2, stages - 1 - i));
+      if (i + NS - 1 < stages) issue(i + NS - 1);
+      const char* st = ring + (i % NS) * DOT_EXPAND_STAGE;
+      uint32_t ad[4];
+      s16x8_t f[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int ch = 4 * (2 * wv + h) + g;
+        ad[2 * h] = lds_at(st + mr * 1024 + ((ch ^ mr) << 4));
+        ad[2 * h + 1] = lds_at(st + 16384 + m * 1024 + ((ch ^ m) << 4));
+      }
+      lds_read4(ad, f);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)  // columns as the M side: a lane gets 4 neighbours
+        acc = mfma16(__builtin_bit_cast(bf16x8_t, f[2 * h + 1]),
+                     __builtin_bit_cast(bf16x8_t, f[2 * h]), acc);
+    }
+    __syncthreads();  // every wavefront is done with the ring
+    f32x4v(*part)[64] = (f32x4v(*)[64])ring;
+    part[wv][lane] = acc;
+    __syncthreads();
+    if (wv < kp / 16) {  // 4 columns of a row a lane, zeros from 16 on
+      const float sc = p.scale ? p.scale[t.a] : 1.0f;
+      f32x4v v = {0.f, 0.f, 0.f, 0.f};
+      if (wv == 0)
+#pragma unroll
+        for (int q = 0; q < NW; ++q) v += part[q][lane];
+      v *= sc;
+      if (m >= t.rows) v = (f32x4v){0.f, 0.f, 0.f, 0.f};
+      const int c = 16 * wv + 4 * g;
+      const uint2 hi = cvt4(v);
+      f32x4v lo;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = i < 2 ? hi.x : hi.y;
+        const float f = __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+        lo[i] = fabsf(f) < INFINITY ? v[i] - f : 0.0f;
+      }
+      char* o = lds + u_chunk(m, c >> 3, kp) + (c & 7) * 2;
+      *(uint2*)o = hi;
+      *(uint2*)(o + 16 * kp * 2) = cvt4(lo);
+    }
+  });
 }
 
 // Many rows (64 MB a tile, 16 MB a wavefront): u stays in registers (KS K steps of 32) and
@@ -1253,8 +1360,8 @@ hipError_t dot_tiles(const char* name, const DotArgs& p, int tiles, hipStream_t 
   return MOE_LAUNCH(name, s, dot_tile_kernel<BM, BN, false><<<g, C::NT, lds, s>>>(p));
 }
 
-unsigned expand_grid(const ExpandArgs& p) {
-  const long extra = p.counts && p.base != p.y ? div_up(p.T, COPY_TOKENS) : 0;
+unsigned expand_grid(const ExpandArgs& p, int waves = 4) {
+  const long extra = p.counts && p.base != p.y ? div_up(p.T, waves) : 0;  // copy_ungrouped
   return (unsigned)((long)p.max_tiles * p.osplit + extra);
 }
 
@@ -1310,6 +1417,7 @@ SkinnyPlan skinny_plan(int T, int n, bool grouped, int K, int N) {
   const int groups = !grouped ? 1 : (n < T ? n : T);
   c.few = !grouped && T <= DOT_FEW;
   c.tile = T >= 32 * groups;
+  c.fused = grouped && !c.tile && N <= 16 && row_tiles(T, n, true, 16) <= FUSED_TILES;
   c.bn = !c.tile ? (N <= 16 ? 16 : (N <= 32 ? 32 : 64)) : (N <= 32 ? 32 : (N <= 64 ? 64 : 128));
   c.bm = !c.tile ? 16 : (c.bn == 128 && !grouped && T >= 1024 ? 128 : 64);
   c.tiles = row_tiles(T, n, grouped, c.bm);
@@ -1330,7 +1438,7 @@ SkinnyPlan skinny_plan(int T, int n, bool grouped, int K, int N) {
     want = wg > 0 ? div_up(target, wg) : 1;
     if (want > 8) want = 8;
   }
-  c.S = c.few ? 1 : (want < most ? want : most);
+  c.S = c.few || c.fused ? 1 : (want < most ? want : most);
   return c;
 }
 
@@ -1386,6 +1494,17 @@ hipError_t launch_expand(const char* name, ExpandArgs p, const ExpandPlan& c, bo
   p.stream = (size_t)p.T * p.nout * 2 >= STREAM_BYTES;
   if (!p.counts) return expand_ks<true, false>(name, p, c, s);
   return nn ? expand_ks<true, true>(name, p, c, s) : expand_ks<false, true>(name, p, c, s);
+}
+
+hipError_t launch_dot_expand(const char* name, const DotArgs& d, ExpandArgs p, bool nn, hipStream_t s) {
+  if (p.T == 0) return hipSuccess;
+  p.stream = 0;
+  p.max_tiles = row_tiles(p.T, p.n, true, 16);
+  const int most = div_up(div_up(p.nout, 128), 8), w = p.max_tiles < 256 ? 256 / p.max_tiles : 1;
+  p.osplit = w < most ? w : most;
+  const unsigned g = expand_grid(p, 8), lds = DOT_EXPAND_U + DOT_EXPAND_STAGES * DOT_EXPAND_STAGE;
+  if (nn) return MOE_LAUNCH(name, s, dot_expand_kernel<true><<<g, 512, lds, s>>>(d, p));
+  return MOE_LAUNCH(name, s, dot_expand_kernel<false><<<g, 512, lds, s>>>(d, p));
 }
 
 int wgrad_chunk(int T, int hblocks, int J) {

@@ -58,11 +58,13 @@ struct WgradArgs {
 
 constexpr int WGRAD_MAX_CHUNK = 1024;  // rows of one chunk (their tokens lie in LDS)
 constexpr int DOT_FEW = 16;            // tokens of the dot without matrix instructions
+constexpr int FUSED_TILES = 256;       // 16-row tiles of both products in one launch
 
 // How a dot or an expand of T rows in n groups (one if not grouped) is cut up: from the
 // sizes alone, so that the order of every sum is too.  tiles: row tiles, an upper bound.
 struct SkinnyPlan {
   bool few, tile;  // dot_few_kernel; dot_tile_kernel (else dot_kernel)
+  bool fused;      // launch_dot_expand for both products
   int bm, bn, tiles, S;
 };
 SkinnyPlan skinny_plan(int T, int n, bool grouped, int K, int N);
@@ -79,6 +81,8 @@ hipError_t launch_sum_parts(const char* name, const float* parts, int S, size_t 
                             hipStream_t s);
 hipError_t launch_expand(const char* name, ExpandArgs p, const ExpandPlan& c, bool nn,
                          hipStream_t s);
+// Both products of few grouped rows (SkinnyPlan::fused); p.u and p.S are not used.
+hipError_t launch_dot_expand(const char* name, const DotArgs& d, ExpandArgs p, bool nn, hipStream_t s);
 hipError_t launch_wgrad(const char* name, WgradArgs p, int sides, hipStream_t s);
 // dst [n][C][R] from src [n][R][C]
 hipError_t launch_transpose(const char* name, int n, const bf16_t* src, bf16_t* dst, int R, int C,

@@ -143,3 +143,8 @@ def test_sizes_past_a_launch_or_32_bit_offsets(L):
     assert lora(L, s, 1 << 40) == UNSUP and lora_b(L, s, 1 << 40) == UNSUP
     assert lora(L, B.lora_shape(1 << 26, 8, 8, 2, 8), 1 << 40) == UNSUP
     assert L.moe_router_logits_bf16(ctypes.byref(s_(T=1, E=8, H=1 << 24)), F, F, F, F, 1 << 40, None) == UNSUP
+
+
+def test_lora_output_over_its_input(L):
+    s = B.lora_shape(70, 64, 64, 3, 16)
+    assert lora(L, s, B.moe_lora_workspace_bytes(s, False), x=F, y=F) == UNSUP

@@ -213,3 +213,17 @@ def test_graph_replay_and_other_stream(B):
         step(b2, c2["idx"].cuda(), c2["x"].cuda(), st)
         st.synchronize()
         assert digest(*b1[4:]) == digest(*b2[4:]), i
+
+
+@pytest.mark.parametrize("T,hi,ho,n,r", [(1, 4104, 1032, 1, 16), (31, 2504, 200, 1, 8), (50, 4104, 264, 20, 16),
+                                         (17, 512, 2056, 2, 16), (40, 520, 136, 1024, 8), (900, 72, 600, 100, 16)])
+def test_few_rows_of_many_values(B, T, hi, ho, n, r):
+    """Both products in one launch: several stages along K, a last one of 8 values, full and
+    ragged 16-row tiles, several parts of the columns."""
+    say(f"lora few T={T} {hi}->{ho} n={n} r={r}")
+    c = case(T, hi, ho, n, r)
+    got = run(B, c)
+    verify(c, got)
+    assert digest(*run(B, c, base="inplace", fill=0)) == digest(*got)
+    assert digest(run(B, c, train=False)[0]) == digest(got[0])
+    assert digest(*run(B, c, base="none")) == digest(*run(B, c, base="none", fill=0))
