@@ -30,12 +30,18 @@ MOE_DEV uint32_t lane_u(uint32_t v, int lane) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
 }
 MOE_DEV uint32_t max_u(uint32_t a, uint32_t b) { return a > b ? a : b; }
+// of two scalars, by the scalar unit (the compiler would move them to the vector unit)
+MOE_DEV uint32_t max_s(uint32_t a, uint32_t b) {
+  uint32_t m;
+  asm("s_max_u32 %0, %1, %2" : "=s"(m) : "s"(a), "s"(b) : "scc");
+  return m;
+}
 MOE_DEV uint32_t wave_max_u32(uint32_t v) {
   v = max_u(row_u32<0x111>(v), v);
   v = max_u(row_u32<0x112>(v), v);
   v = max_u(row_u32<0x114>(v), v);
   v = max_u(row_u32<0x118>(v), v);
-  return max_u(max_u(lane_u(v, 15), lane_u(v, 31)), max_u(lane_u(v, 47), lane_u(v, 63)));
+  return max_s(max_s(lane_u(v, 15), lane_u(v, 31)), max_s(lane_u(v, 47), lane_u(v, 63)));
 }
 // Order-preserving map of fp32 to 32 bits, above 0 for numbers and infinities
 MOE_DEV uint32_t ordered_u32(float v) {
@@ -217,11 +223,12 @@ MOE_DEV void row_softmax_stats(const float (&l)[NPL], float& top, float& sum) {
 // functions keep the order of the logits, which then decide, exactly, without forming a
 // score.
 // Bound by the vector unit, not by memory: 8192 tokens of 256 experts in 8 groups, k = 8,
-// take 13 us for 8.9 MB and 766 vector instructions a token, whose issue alone is 11.6 us
-// (8 wavefronts a SIMD).  One token: 4.5 us, of which the launch is half and the rest a
+// take 12 us for 8.9 MB and 707 vector instructions a token, 150 of them in 64 bits at half
+// rate, whose issue alone is about 11 us (8 wavefronts a SIMD).  One token: 4.5 us, of which the launch is half and the rest a
 // chain (row, exp, group scores, k maxima of 64 lanes).  Row shifts for the maxima instead
 // of a round trip through LDS a step, lanes sorted once so that a round looks at one key of
-// each, and the vectorised exp took it there from 20 us (and 7.6 us).
+// each, and the vectorised exp took it there from 20 us (and 7.6 us); scalar maxima across
+// the rows and a shift for a lane's group saved 60 instructions of 766.
 template <int NPL, int MODE>
 __global__ __launch_bounds__(256) void route_scored_kernel(const float* __restrict__ logits,
                                                            const float* __restrict__ bias, int T,
@@ -305,7 +312,8 @@ __global__ __launch_bounds__(256) void route_scored_kernel(const float* __restri
         }
       }
       const double gs = (sc.group_top == 2 && b2 > -INFINITY) ? b1 + b2 : b1;
-      const int step = sc.lanes ? sc.lanes : 1, me = lane / step;  // lane g * step scores group g
+      // lane g * step scores group g; step is a power of two
+      const int step = sc.lanes ? sc.lanes : 1, me = lane >> __builtin_ctz(step);
       int better = 0;
       for (int g = 0; g < sc.n_groups; ++g) {
         const double o = __hiloint2double(lane_i(__double2hiint(gs), g * step),
