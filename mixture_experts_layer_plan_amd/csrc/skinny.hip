@@ -220,11 +220,10 @@ __global__ __launch_bounds__(512) void dot_kernel(DotArgs p) {
 // (each 64 rows x 128 columns less of tile costs 235 MB more and 13 us); fragments read one
 // step ahead of their products, 3 or 5 stages, and K from another start in each tile change
 // nothing.  128 x 256 tiles with 4 parts would save 4 us of loads and cost 4 us of parts.
-// Rank 64 over 8192 rows of 7168 (117 MB): 33 to 37 us against 20 to 31 us for the plain
-// read, as much as the writes of the kernel before still have to leave the Infinity Cache;
-// the rest is the start of the workgroups (about 9 us for one stage).  S = 3 there: with 2
-// parts the tiles do not spread evenly (43 us), and each further part costs the second
-// product 1 to 2 us.
+// Rank 64 over 8192 rows of 7168 (117 MB, 8 adapters): 31 to 33 us against 20 to 31 us for the
+// plain read, as much as the writes of the kernel before still have to leave the Infinity
+// Cache; the rest is the start of the workgroups.  S = 3 there: with 2 or 4 parts the tiles do
+// not spread evenly (38, 40 us), and each further part costs the second product 1 to 2 us.
 template <int BM, int BN>
 struct DotTile {
   static constexpr int WN = BN >= 64 ? 2 : 1, WM = 4 / WN;  // wavefronts along columns, rows
@@ -233,7 +232,8 @@ struct DotTile {
   static constexpr int NWV = 4 * KG, NT = 64 * NWV, HS = BK / 32 / KG;  // K steps of a wavefront
   static constexpr int MB = BM / 16 / WM, NB = BN / 16 / WN;
   static constexpr int STAGE = (BM + BN) * K2;
-  static constexpr int NS = BM == 128 ? 4 : 3;  // 36, 48, 144, 128 KiB: 4, 3, 1, 1 a CU
+  // BM x 32, 64, 128: 36, 48, 144 KiB for 64 rows, -, 72, 128 for 128: 4, 3, 1, -, 2, 1 a CU
+  static constexpr int NS = BM == 128 && BN == 128 ? 4 : 3;
   static constexpr int LOADS = STAGE / (1024 * NWV), ALOADS = BM * K2 / (1024 * NWV);  // a wavefront
   static MOE_DEV int swz(int r) { return CH == 8 ? (r >> 1) & 7 : r & 15; }
 };
@@ -1354,7 +1354,7 @@ hipError_t dot_tiles(const char* name, const DotArgs& p, int tiles, hipStream_t 
   const unsigned g = (unsigned)((long)tiles * div_up(p.N, BN) * p.S);
   using C = DotTile<BM, BN>;
   constexpr unsigned lds = C::NS * C::STAGE;
-  if constexpr (BM == 64)
+  if constexpr (BM == 64 || BN == 64)
     if (p.counts)
       return MOE_LAUNCH(name, s, dot_tile_kernel<BM, BN, true><<<g, C::NT, lds, s>>>(p));
   return MOE_LAUNCH(name, s, dot_tile_kernel<BM, BN, false><<<g, C::NT, lds, s>>>(p));
@@ -1419,7 +1419,14 @@ SkinnyPlan skinny_plan(int T, int n, bool grouped, int K, int N) {
   c.tile = T >= 32 * groups;
   c.fused = grouped && !c.tile && N <= 16 && row_tiles(T, n, true, 16) <= FUSED_TILES;
   c.bn = !c.tile ? (N <= 16 ? 16 : (N <= 32 ? 32 : 64)) : (N <= 32 ? 32 : (N <= 64 ? 64 : 128));
-  c.bm = !c.tile ? 16 : (c.bn == 128 && !grouped && T >= 1024 ? 128 : 64);
+  // 128 rows halve the weights' way through a CU's L1: at 64 columns where that outweighs the
+  // longer start (8192 rows of 7168: rank 64 of 8 adapters 35 -> 32 us, E = 64 29 -> 25; 4096
+  // rows the same; 8192 rows of 2048 12 -> 13, 1024 of 7168 11 -> 12), not at 32, where x is
+  // most of it (rank 16: 92 -> 95 us with the second product), nor at 128 for groups, whose
+  // ragged tiles then leave CUs idle (rank 128: 66 -> 74 us)
+  const bool tall = c.bn == 64 ? (int64_t)T * K >= 1 << 25 && T >= 128 * groups
+                               : c.bn == 128 && !grouped && T >= 1024;
+  c.bm = !c.tile ? 16 : (tall ? 128 : 64);
   c.tiles = row_tiles(T, n, grouped, c.bm);
   const int wg = c.tiles * div_up(N, c.bn);
   // at least two steps of each of 8 wavefronts, or a ring's stages
@@ -1455,9 +1462,12 @@ hipError_t launch_dot(const char* name, const DotArgs& p, const SkinnyPlan& c, h
     if (c.bn == 32) return dot_small<2>(name, p, c.tiles, s);
     return dot_small<4>(name, p, c.tiles, s);
   }
-  if (c.bn == 32) return dot_tiles<64, 32>(name, p, c.tiles, s);
-  if (c.bn == 64) return dot_tiles<64, 64>(name, p, c.tiles, s);
-  if (c.bm == 64) return dot_tiles<64, 128>(name, p, c.tiles, s);
+  if (c.bm == 64) {
+    if (c.bn == 32) return dot_tiles<64, 32>(name, p, c.tiles, s);
+    if (c.bn == 64) return dot_tiles<64, 64>(name, p, c.tiles, s);
+    return dot_tiles<64, 128>(name, p, c.tiles, s);
+  }
+  if (c.bn == 64) return dot_tiles<128, 64>(name, p, c.tiles, s);
   return dot_tiles<128, 128>(name, p, c.tiles, s);
 }
 

@@ -227,3 +227,13 @@ def test_few_rows_of_many_values(B, T, hi, ho, n, r):
     assert digest(*run(B, c, base="inplace", fill=0)) == digest(*got)
     assert digest(run(B, c, train=False)[0]) == digest(got[0])
     assert digest(*run(B, c, base="none")) == digest(*run(B, c, base="none", fill=0))
+
+
+@pytest.mark.parametrize("T,hi,ho,n,r", [(9000, 3736, 64, 3, 64), (6000, 64, 5600, 2, 40)])
+def test_many_rows_of_many_values(B, T, hi, ho, n, r):
+    """T * H past 2^25: the first product in 128-row tiles, ragged ones among them."""
+    say(f"lora many T={T} {hi}->{ho} n={n} r={r}")
+    c = case(T, hi, ho, n, r)
+    got = run(B, c)
+    verify(c, got)
+    assert digest(*run(B, c, base="inplace", fill=0)) == digest(*got)

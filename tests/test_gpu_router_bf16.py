@@ -162,3 +162,17 @@ def test_binding_refuses(B):
         B.moe_router_logits_bf16(s, x.cuda()[:2], w.cuda(), out, None)
     with pytest.raises(ValueError):
         B.moe_router_logits_bf16(s, x.cuda().t().contiguous().t(), w.cuda(), out, None)
+
+
+def test_many_rows_of_many_values(B):
+    """T * H past 2^25 at E <= 64: 128-row tiles, a ragged last one."""
+    T, H, E = 6100, 5632, 60
+    say(f"router bf16 T={T} H={H} E={E}")
+    g = torch.Generator().manual_seed(5)
+    x, w = rand(g, T, H), rand(g, E, H, std=0.05)
+    s = B.shape(T, H, 128, E, 1)
+    logits, ok = rows_guarded(T, E, torch.float32)
+    ws = torch.full((B.moe_router_workspace_bytes(s, False),), 255, dtype=torch.uint8, device="cuda")
+    B.moe_router_logits_bf16(s, x.cuda(), w.cuda(), logits, ws)
+    ok()
+    check(logits, oracle.router_logits(x, w), dot_bound(x, w), "logits")
