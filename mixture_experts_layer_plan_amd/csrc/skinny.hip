@@ -759,7 +759,9 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs p) {
 // (a ring of 7 is no faster).  Against the two launches, in a captured graph, 7168 columns in:
 // one token 9.4 and 9.1 us (2048: 6.5 and 7.7), 96 tokens of 32 adapters 10.6 and 11.7 us, 256
 // of 64 18.9 and 24.6, 1000 of 100 (4096) 18.6 and 24.5; called one by one it also saves the
-// host's second launch.  Rank 32 lost for few tiles (one token 11.6 and 10.8 us).
+// host's second launch.  It loses at rank 32 for few tiles (one token 11.6 and 10.8 us) and
+// where K is long and few tiles fill the chip (16384 values, 96 tokens of 32 adapters 24.6 and
+// 16.3 us; 512 of 128 29.6 and 37.1).
 constexpr int DOT_EXPAND_STAGE = 32768, DOT_EXPAND_STAGES = 4, DOT_EXPAND_U = 2048;
 template <bool NN>
 __global__ __launch_bounds__(512) void dot_expand_kernel(DotArgs d, ExpandArgs p) {
@@ -1417,7 +1419,9 @@ SkinnyPlan skinny_plan(int T, int n, bool grouped, int K, int N) {
   const int groups = !grouped ? 1 : (n < T ? n : T);
   c.few = !grouped && T <= DOT_FEW;
   c.tile = T >= 32 * groups;
-  c.fused = grouped && !c.tile && N <= 16 && row_tiles(T, n, true, 16) <= FUSED_TILES;
+  // dot_expand_kernel: one workgroup's stages along K against parts of K on many
+  const int tiles16 = row_tiles(T, n, grouped, 16);
+  c.fused = grouped && !c.tile && N <= 16 && tiles16 <= FUSED_TILES && (K <= 8192 || tiles16 >= 128);
   c.bn = !c.tile ? (N <= 16 ? 16 : (N <= 32 ? 32 : 64)) : (N <= 32 ? 32 : (N <= 64 ? 64 : 128));
   // 128 rows halve the weights' way through a CU's L1: at 64 columns where that outweighs the
   // longer start (8192 rows of 7168: rank 64 of 8 adapters 35 -> 32 us, E = 64 29 -> 25; 4096

@@ -237,3 +237,13 @@ def test_many_rows_of_many_values(B, T, hi, ho, n, r):
     got = run(B, c)
     verify(c, got)
     assert digest(*run(B, c, base="inplace", fill=0)) == digest(*got)
+
+
+@pytest.mark.parametrize("T,hi,ho,n", [(3, 8200, 64, 2), (130, 8200, 72, 130)])
+def test_more_values_than_one_workgroup_takes(B, T, hi, ho, n):
+    """Past 8192 values a row the products are two launches for few tiles, one for many."""
+    say(f"lora long rows T={T} {hi}->{ho} n={n}")
+    c = case(T, hi, ho, n, 16)
+    got = run(B, c)
+    verify(c, got)
+    assert digest(run(B, c, train=False)[0]) == digest(got[0])
