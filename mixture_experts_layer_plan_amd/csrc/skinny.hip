@@ -980,7 +980,9 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
       ul[m][ks] = as_frag(*(const uint4*)(a + ROWS * KP * 2));
     }
   __syncthreads();
-  if (!NN && (p.K & 31)) {  // K values that no store below writes
+  // K values that no store below writes (of K = 96 a whole step): u is zero there, and zero
+  // times what an earlier workgroup left in LDS may be NaN
+  if (!NN && p.K < KP) {
     for (int i = threadIdx.x; i < 2 * STAGE / 16; i += 256) *(uint4*)(lds + i * 16) = zero4();
     __syncthreads();
   }
