@@ -280,7 +280,8 @@ moe_status moe_router_backward_bf16(const moe_shape* shape, const void* x, const
                                     const float* d_logits, const void* dx_in, void* dw_router,
                                     void* dx, void* ws, size_t ws_bytes, hipStream_t stream);
 
-/* Scratch bytes of the two (T, H, E are used; k and I are not); 0 for shapes they refuse. */
+/* Scratch bytes of the two (T, H, E are used; k and I are not); 0 for shapes they refuse.
+ * The backward's are enough for the forward too. */
 size_t moe_router_workspace_bytes(const moe_shape* shape, int backward);
 
 /* ------------------------------------------------------------------ plan */
@@ -503,7 +504,7 @@ moe_status moe_lora_plan(const moe_lora_shape* shape, const int32_t* adapter_idx
                          hipStream_t stream);
 
 /* Bytes of what the forward keeps for the backward, and of scratch of the forward
- * (backward = 0) or the backward; 0 for shapes they refuse. */
+ * (backward = 0) or the backward, which is enough for both; 0 for shapes they refuse. */
 size_t moe_lora_saved_bytes(const moe_lora_shape* shape);
 size_t moe_lora_workspace_bytes(const moe_lora_shape* shape, int backward);
 

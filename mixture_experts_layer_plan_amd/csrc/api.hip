@@ -964,6 +964,7 @@ RouterWs router_ws(const moe_shape* s, bool backward) {
     L.wparts = c.take(s->T > L.chunk ? wgrad_chunk_slots(s->T, 1, false, L.chunk) * E * H * 4 : 0);
   }
   L.total = c.off;
+  if (backward) L.total = std::max(L.total, router_ws(s, false).total);  // one buffer for both
   return L;
 }
 
@@ -1023,6 +1024,8 @@ LoraWs lora_ws(const moe_lora_shape* s, bool backward) {
     L.pb = c.take(slots * r * ho * 4);
   }
   L.total = c.off;
+  // one buffer for both passes: the forward's parts can be more (H_in long, H_out short)
+  if (backward) L.total = std::max(L.total, lora_ws(s, false).total);
   return L;
 }
 

@@ -1,6 +1,7 @@
 """Host-side refusals of scored routing, the bf16 router projection and the low-rank
 adapters (the fake pointers are never dereferenced: every call here is refused)."""
 import ctypes
+import random
 
 import pytest
 
@@ -148,3 +149,21 @@ def test_sizes_past_a_launch_or_32_bit_offsets(L):
 def test_lora_output_over_its_input(L):
     s = B.lora_shape(70, 64, 64, 3, 16)
     assert lora(L, s, B.moe_lora_workspace_bytes(s, False), x=F, y=F) == UNSUP
+
+
+def test_the_backwards_workspace_serves_the_forward():
+    """A training step keeps one workspace, of the backward's size, for both passes."""
+    rng = random.Random(1)
+
+    def log_int(hi):
+        return round(hi ** rng.random())
+    shapes = [(97, 4992, 272, 3, 64), (110, 6712, 240, 3, 64), (100, 7168, 128, 1, 64), (0, 8, 8, 1, 8)]
+    shapes += [(log_int(20000), 8 * log_int(1000), 8 * log_int(1000), log_int(1024), 8 * log_int(16))
+               for _ in range(4000)]
+    for a in shapes:
+        s = B.lora_shape(*a)
+        assert B.moe_lora_workspace_bytes(s, True) >= B.moe_lora_workspace_bytes(s, False) >= 0, a
+    for T, H, E in [(64, 7168, 256), (20, 7168, 4)] + [(log_int(20000), 128 * log_int(60), log_int(1024))
+                                                       for _ in range(4000)]:
+        s = B.shape(T, H, 128, E, 1)
+        assert B.moe_router_workspace_bytes(s, True) >= B.moe_router_workspace_bytes(s, False), (T, H, E)
