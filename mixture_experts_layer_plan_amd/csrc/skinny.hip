@@ -13,6 +13,7 @@
 // two bf16 halves (hi = round(v), lo = round(v - hi): 16 bits of the 24-bit mantissa, an
 // error of 2^-17 against the 2^-9 of the bf16 result), so that it costs two matrix
 // instructions and no accuracy.
+#include <algorithm>
 #include <type_traits>
 
 #include "gemm_common.hpp"
@@ -598,20 +599,25 @@ MOE_DEV void fill_u(const ExpandArgs& p, const SkinnyTile& t, int kp, char* lds)
   }
 }
 
-// Rows without a group: the base alone, a token per wavefront, 8 KiB in flight.
-MOE_DEV void copy_ungrouped(const ExpandArgs& p, int b) {
-  const int lane = threadIdx.x & 63, tok = b * (int)(blockDim.x >> 6) + (int)(threadIdx.x >> 6);
-  if (tok >= p.T || p.pos[tok] >= 0) return;
-  const size_t o = (size_t)tok * p.nout;
+// Rows without a group: the base alone, a token per wavefront and 8 KiB in flight, by the
+// workgroups behind the tiles' (at most COPY_GROUPS, which then take several tokens).
+constexpr int COPY_GROUPS = 1 << 22;
+MOE_DEV void copy_ungrouped(const ExpandArgs& p) {
+  const int lane = threadIdx.x & 63, waves = (int)(blockDim.x >> 6);
+  const int first = p.max_tiles * p.osplit, step = ((int)gridDim.x - first) * waves;
+  for (int tok = ((int)blockIdx.x - first) * waves + (int)(threadIdx.x >> 6); tok < p.T; tok += step) {
+    if (p.pos[tok] >= 0) continue;
+    const size_t o = (size_t)tok * p.nout;
 #pragma unroll 1
-  for (int c = lane * 8; c < p.nout; c += 8 * 512) {
-    uint4 v[8];
+    for (int c = lane * 8; c < p.nout; c += 8 * 512) {
+      uint4 v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i] = p.base && c + i * 512 < p.nout ? *(const uint4*)(p.base + o + c + i * 512) : zero4();
+      for (int i = 0; i < 8; ++i)
+        v[i] = p.base && c + i * 512 < p.nout ? *(const uint4*)(p.base + o + c + i * 512) : zero4();
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i * 512 < p.nout) *(uint4*)(p.y + o + c + i * 512) = v[i];
+      for (int i = 0; i < 8; ++i)
+        if (c + i * 512 < p.nout) *(uint4*)(p.y + o + c + i * 512) = v[i];
+    }
   }
 }
 
@@ -740,7 +746,7 @@ template <int MB, bool NN, bool GR>
 __global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs p) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   if (GR && (int)blockIdx.x >= p.max_tiles * p.osplit) {
-    copy_ungrouped(p, blockIdx.x - p.max_tiles * p.osplit);
+    copy_ungrouped(p);
     return;
   }
   const int tile = blockIdx.x / p.osplit, oz = blockIdx.x % p.osplit;
@@ -769,7 +775,7 @@ __global__ __launch_bounds__(512) void dot_expand_kernel(DotArgs d, ExpandArgs p
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   if ((int)blockIdx.x >= p.max_tiles * p.osplit) {
-    copy_ungrouped(p, blockIdx.x - p.max_tiles * p.osplit);
+    copy_ungrouped(p);
     return;
   }
   const int tile = blockIdx.x / p.osplit, oz = blockIdx.x % p.osplit;
@@ -874,7 +880,7 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   if (GR && (int)blockIdx.x >= p.max_tiles * p.osplit) {
-    copy_ungrouped(p, blockIdx.x - p.max_tiles * p.osplit);
+    copy_ungrouped(p);
     return;
   }
   const int tile = blockIdx.x / p.osplit, oz = blockIdx.x % p.osplit;
@@ -1364,8 +1370,10 @@ hipError_t dot_tiles(const char* name, const DotArgs& p, int tiles, hipStream_t 
   return MOE_LAUNCH(name, s, dot_tile_kernel<BM, BN, false><<<g, C::NT, lds, s>>>(p));
 }
 
+// below 2^32 threads: 4 T of the tiles (T < 2^26) and 2^30 or 2^31 of the copies
 unsigned expand_grid(const ExpandArgs& p, int waves = 4) {
-  const long extra = p.counts && p.base != p.y ? div_up(p.T, waves) : 0;  // copy_ungrouped
+  const long extra =  // copy_ungrouped
+      p.counts && p.base != p.y ? std::min(div_up(p.T, waves), COPY_GROUPS) : 0;
   return (unsigned)((long)p.max_tiles * p.osplit + extra);
 }
 

@@ -135,3 +135,37 @@ def test_many_large_adapters(B):
     dA[few.cuda()] = 0
     dB[few.cuda()] = 0
     assert not dA.any() and not dB.any()
+
+
+def test_base_of_more_tokens_than_one_launch_has_wavefronts(B):
+    """Close to 2^26 tokens, all but the ends without an adapter: their base is copied."""
+    T, hi, ho, n, r = 66_000_000, 8, 16, 2, 8
+    say(f"lora T={T} {hi}->{ho}")
+    s = B.lora_shape(T, hi, ho, n, r)
+    c = dict(x=rand(2 * N, hi), a=rand(n, r, hi, std=hi ** -0.5), b=rand(n, ho, r, std=0.25),
+             scale=torch.tensor([0.5, 2.0]), dy=rand(2 * N, ho, seed=5))
+    few = (torch.arange(2 * N) % n).to(torch.int32)
+    idx = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    idx[:N], idx[T - N:] = few[:N].cuda(), few[N:].cuda()
+    g = torch.Generator(device="cuda").manual_seed(6)
+    base, dx_in = (torch.randn((T, h), generator=g, device="cuda", dtype=torch.bfloat16) for h in (ho, hi))
+    x, dy = ends(T, c["x"]), ends(T, c["dy"])
+    y, dx = torch.full_like(base, 7), torch.full_like(dx_in, 7)
+    a, b, sc = c["a"].cuda(), c["b"].cuda(), c["scale"].cuda()
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    plan, saved = (torch.empty(f(s), **u8) for f in (B.moe_lora_plan_bytes, B.moe_lora_saved_bytes))
+    ws = torch.empty(B.moe_lora_workspace_bytes(s, True), **u8)
+    da, db = torch.empty_like(a), torch.empty_like(b)
+    B.moe_lora_plan(s, idx, plan)
+    B.moe_lora_bf16(s, plan, x, a, b, sc, base, y, saved, ws)
+    B.moe_lora_backward_bf16(s, plan, x, a, b, sc, saved, dy, dx_in, dx, da, db, ws)
+    assert torch.equal(y[N:T - N], base[N:T - N]) and torch.equal(dx[N:T - N], dx_in[N:T - N])
+    i, yb, xb = few.numpy(), both(base), both(dx_in)
+    u, uerr, yerr = lora_bounds(i, c["x"], c["a"], c["b"], c["scale"], yb)
+    ref = oracle.lora(i, c["x"], c["a"], c["b"], c["scale"], yb)
+    check(both(y), ref, bf16_of(ref, yerr), "y")
+    v, verr, xerr = lora_bounds(i, c["dy"], c["b"].transpose(1, 2), c["a"].transpose(1, 2), c["scale"], xb)
+    rdx, rda, rdb = oracle.lora_backward(i, c["x"], c["a"], c["b"], c["scale"], c["dy"], xb)
+    check(both(dx), rdx, bf16_of(rdx, xerr), "dx")
+    check(da, rda, bf16_of(rda, outer_bound(i, n, v, verr, c["x"])), "da")
+    check(db, rdb, bf16_of(rdb, outer_bound(i, n, u, uerr, c["dy"]).transpose(0, 2, 1)), "db")
