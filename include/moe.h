@@ -224,7 +224,7 @@ moe_status moe_router_backward_f32(const moe_shape* shape, const float* x,
  * renormalise is set: the bias moves the choice alone, as balancing the experts' load
  * needs, not the output; a bias of -inf makes an expert the last choice.
  * Limits: n_groups <= 64 and a divisor of E, 1 <= topk_groups <= n_groups,
- * k <= topk_groups * E / n_groups, scale finite; T below 2^26 (MOE_E_UNSUPPORTED). */
+ * k <= topk_groups * E / n_groups, scale finite; T <= 2^26 - 4 (MOE_E_UNSUPPORTED). */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 typedef struct {
   int32_t score; /* moe_score */

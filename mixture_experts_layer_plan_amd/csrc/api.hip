@@ -923,12 +923,13 @@ moe_status scratch_of_current_device(void** out) {
 
 // ------------------------------------------------------- router projection, adapters
 
-// A wavefront a token in one launch: T * 64 threads below 2^32.
-constexpr int MAX_WAVE_ROWS = 1 << 26;
+// Scored routing takes a wavefront a token, four a workgroup, in one launch: below 2^32
+// threads.  The adapters' launches stay below that up to 2^26 tokens.
+constexpr int MAX_ROUTED = (1 << 26) - 4, MAX_ADAPTED = (1 << 26) - 1;
 
 moe_status check_scoring(const moe_shape* s, const moe_scoring* sc) {
   if (!sc) return MOE_E_NULL;
-  if (s->T >= MAX_WAVE_ROWS) return MOE_E_UNSUPPORTED;
+  if (s->T > MAX_ROUTED) return MOE_E_UNSUPPORTED;
   if (sc->score != MOE_SCORE_SOFTMAX && sc->score != MOE_SCORE_SIGMOID) return MOE_E_SHAPE;
   if (sc->n_groups < 1 || sc->n_groups > 64 || s->E % sc->n_groups) return MOE_E_SHAPE;
   if (sc->topk_groups < 1 || sc->topk_groups > sc->n_groups) return MOE_E_SHAPE;
@@ -985,7 +986,7 @@ moe_status check_lora(const moe_lora_shape* s) {
   if (s->T < 0 || s->n_adapters < 1 || s->n_adapters > MOE_MAX_E) return MOE_E_SHAPE;
   if (s->H_in < 8 || s->H_in % 8 || s->H_out < 8 || s->H_out % 8) return MOE_E_SHAPE;
   if (s->rank < 8 || s->rank > 128 || s->rank % 8) return MOE_E_SHAPE;
-  if (s->T >= MAX_WAVE_ROWS) return MOE_E_UNSUPPORTED;
+  if (s->T > MAX_ADAPTED) return MOE_E_UNSUPPORTED;
   const uint64_t rows = std::max(s->T, 128);  // 32-bit byte offsets, as in check_router
   if (rows * (uint64_t)std::max(s->H_in, s->H_out) * 2 >= 1ull << 32) return MOE_E_UNSUPPORTED;
   return MOE_OK;

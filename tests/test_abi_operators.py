@@ -167,3 +167,10 @@ def test_the_backwards_workspace_serves_the_forward():
                                                        for _ in range(4000)]:
         s = B.shape(T, H, 128, E, 1)
         assert B.moe_router_workspace_bytes(s, True) >= B.moe_router_workspace_bytes(s, False), (T, H, E)
+
+
+def test_routing_that_would_fill_a_launch_exactly(L):
+    """Four tokens a workgroup of 256 threads: from 2^26 - 3 tokens on, 2^32 threads."""
+    sc = B.scoring()
+    for T in ((1 << 26) - 3, (1 << 26) - 1):
+        assert route(L, s_(T=T, k=1), sc) == UNSUP and route_b(L, s_(T=T, k=1), sc) == UNSUP
