@@ -11,7 +11,7 @@
 //
 // x, dy and the weights are bf16.  u, v and dL are fp32 and enter the second product as
 // two bf16 halves (hi = round(v), lo = round(v - hi): 16 bits of the 24-bit mantissa, an
-// error of 2^-17 against the 2^-9 of the bf16 result), so that it costs two matrix
+// error of 2^-17 against the 2^-8 of the bf16 result), so that it costs two matrix
 // instructions and no accuracy.
 #include <algorithm>
 #include <type_traits>
