@@ -271,8 +271,8 @@ moe_status moe_router_logits_bf16(const moe_shape* shape, const void* x, const v
 
 /* Its backward: dw_router [E, H] (bf16, overwritten) = d_logits^T x and
  * dx [T, H] (bf16) = dx_in + d_logits w_router, summed in fp32 and rounded once;
- * dx_in bf16 [T, H], or NULL (zero), may be dx itself; dx may not be x
- * (MOE_E_UNSUPPORTED).  d_logits fp32 [T, E] enters the
+ * dx_in bf16 [T, H], or NULL (zero), may be dx itself; dx may share no bytes with x, nor
+ * with a dx_in that begins elsewhere (MOE_E_UNSUPPORTED).  d_logits fp32 [T, E] enters the
  * products with 16 bits of mantissa (as two bf16 halves); where x or d_logits is not
  * finite, neither are the gradients it enters (inf or NaN).
  * ws [ws_bytes >= moe_router_workspace_bytes(shape, 1)]. */
@@ -509,8 +509,8 @@ size_t moe_lora_saved_bytes(const moe_lora_shape* shape);
 size_t moe_lora_workspace_bytes(const moe_lora_shape* shape, int backward);
 
 /* Forward.  base bf16 [T, H_out], or NULL (zero), may be y itself: rows of tokens
- * without an adapter are then left as they are, otherwise they get their base; y may not
- * be x (MOE_E_UNSUPPORTED).  Both
+ * without an adapter are then left as they are, otherwise they get their base; y may
+ * share no bytes with x, nor with a base that begins elsewhere (MOE_E_UNSUPPORTED).  Both
  * products are summed in fp32, u = A x is kept to 16 bits of mantissa between them, and
  * y bf16 [T, H_out] is rounded once.  Where x, A or B is not finite, neither are the
  * results it enters (inf or NaN); a token without an adapter may hold anything.
@@ -523,7 +523,7 @@ moe_status moe_lora_bf16(const moe_lora_shape* shape, const void* plan, const vo
 /* Backward, from dy bf16 [T, H_out] and the forward's saved, with u_t = scale A x_t and
  * v_t = scale B^T dy_t over the tokens of each adapter:
  *   dx[t, :] = dx_in[t, :] + A^T v_t   (bf16 [T, H_in]; dx_in or NULL, may be dx itself,
- *                                       as base and y; dx may not be x or dy)
+ *                                       as base and y; dx shares no bytes with x or dy)
  *   d_lora_a = sum_t v_t (x) x_t, d_lora_b = sum_t dy_t (x) u_t   (bf16, overwritten;
  *                                       zeros for adapters without tokens) */
 moe_status moe_lora_backward_bf16(const moe_lora_shape* shape, const void* plan, const void* x,

@@ -927,6 +927,16 @@ moe_status scratch_of_current_device(void** out) {
 // threads.  The adapters' launches stay below that up to 2^26 tokens.
 constexpr int MAX_ROUTED = (1 << 26) - 4, MAX_ADAPTED = (1 << 26) - 1;
 
+// Whether an output shares bytes with an input that is still read while it is written (an
+// output over its own base is read and written row by row: the same pointer is fine).
+bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
+  return a && b && p < q + nb && q < p + na;
+}
+bool overlap_base(const void* y, const void* base, uint64_t n) {
+  return y != base && overlap(y, n, base, n);
+}
+
 moe_status check_scoring(const moe_shape* s, const moe_scoring* sc) {
   if (!sc) return MOE_E_NULL;
   if (s->T > MAX_ROUTED) return MOE_E_UNSUPPORTED;
@@ -1419,9 +1429,10 @@ moe_status moe_router_backward_bf16(const moe_shape* s, const void* x, const voi
   if (rc != MOE_OK) return rc;
   if (any_null({w_router, dw_router, ws}) || any_null_rows(s, {x, d_logits, dx})) return MOE_E_NULL;
   if (!all_aligned({x, w_router, d_logits, dx_in, dw_router, dx, ws})) return MOE_E_ALIGN;
-  if (s->T > 0 && dx == x) return MOE_E_UNSUPPORTED;  // dW reads x after dx is written
   const RouterWs W = router_ws(s, true);
   if (ws_bytes < W.total) return MOE_E_WORKSPACE;
+  const uint64_t nx = (uint64_t)s->T * s->H * 2;  // dW reads x after dx is written
+  if (overlap(dx, nx, x, nx) || overlap_base(dx, dx_in, nx)) return MOE_E_UNSUPPORTED;
   ExpandArgs e;
   memset(&e, 0, sizeof(e));
   const ExpandPlan c = expand_plan(s->T, 1, false, s->E, s->H);
@@ -1483,7 +1494,9 @@ moe_status moe_lora_bf16(const moe_lora_shape* s, const void* plan, const void* 
   const LoraWs W = lora_ws(s, false);
   if (ws_bytes < W.total) return MOE_E_WORKSPACE;
   if (s->T == 0) return MOE_OK;
-  if (y == x) return MOE_E_UNSUPPORTED;  // rows of x are read beside y's being written
+  const uint64_t nx = (uint64_t)s->T * s->H_in * 2, ny = (uint64_t)s->T * s->H_out * 2;
+  // rows of x are read beside y's being written
+  if (overlap(y, ny, x, nx) || overlap_base(y, base, ny)) return MOE_E_UNSUPPORTED;
   const moe_shape ps = lora_plan_shape(s);
   return lora_pair(s, view_plan(&ps, plan), x, s->H_in, lora_a, "lora_shrink", lora_b, false,
                    s->H_out, "lora_expand", scale, base, y, at<float>(ws, W.parts), saved, st);
@@ -1501,9 +1514,12 @@ moe_status moe_lora_backward_bf16(const moe_lora_shape* s, const void* plan, con
     return MOE_E_NULL;
   if (!all_aligned({plan, x, lora_a, lora_b, scale, saved, dy, dx_in, dx, d_lora_a, d_lora_b, ws}))
     return MOE_E_ALIGN;
-  if (s->T > 0 && (dx == x || dx == dy)) return MOE_E_UNSUPPORTED;  // both are read after dx
   const LoraWs W = lora_ws(s, true);
   if (ws_bytes < W.total) return MOE_E_WORKSPACE;
+  const uint64_t nx = (uint64_t)s->T * s->H_in * 2, ny = (uint64_t)s->T * s->H_out * 2;
+  // x and dy are read after dx
+  if (overlap(dx, nx, x, nx) || overlap(dx, nx, dy, ny) || overlap_base(dx, dx_in, nx))
+    return MOE_E_UNSUPPORTED;
   const moe_shape ps = lora_plan_shape(s);
   const PlanView v = view_plan(&ps, plan);
   bf16_t_host* vt = at<bf16_t_host>(ws, W.vt);

@@ -174,3 +174,22 @@ def test_routing_that_would_fill_a_launch_exactly(L):
     sc = B.scoring()
     for T in ((1 << 26) - 3, (1 << 26) - 1):
         assert route(L, s_(T=T, k=1), sc) == UNSUP and route_b(L, s_(T=T, k=1), sc) == UNSUP
+
+
+def test_outputs_that_share_bytes_with_their_inputs(L):
+    """An output begins inside an input, or an input inside an output, by one row."""
+    s = B.lora_shape(70, 64, 128, 3, 16)
+    nx, ny = 70 * 64 * 2, 70 * 128 * 2
+    f, b = B.moe_lora_workspace_bytes(s, False), B.moe_lora_workspace_bytes(s, True)
+    X, Y, FAR = 0x1000000, 0x2000000, 0x3000000
+    for x, y in ((X, X + nx - 128), (X + ny - 256, X)):
+        assert lora(L, s, f, x=x, y=y, base=FAR) == UNSUP
+    for base in (Y + 256, Y - 256):
+        assert lora(L, s, f, x=X, y=Y, base=base) == UNSUP
+    for kw in (dict(x=X + 128, dy=Y, dxi=FAR), dict(x=Y, dy=X - ny + 128, dxi=FAR),
+               dict(x=Y, dy=FAR, dxi=X - 128)):
+        assert lora_b(L, s, b, dx=X, **kw) == UNSUP
+    r = s_()
+    n, ws = 64 * 256 * 2, B.moe_router_workspace_bytes(r, True)
+    for x, dxi in ((X + n - 512, FAR), (X - 512, None), (FAR, X + 512)):
+        assert L.moe_router_backward_bf16(ctypes.byref(r), x, F, F, dxi, F, X, F, ws, None) == UNSUP
