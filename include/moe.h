@@ -241,7 +241,7 @@ typedef struct {
  * An expert whose logit is -inf or NaN is out of play for that token; slots left over
  * when fewer than k are in play get expert -1 and weight 0, which moe_plan leaves out
  * (setting its err_flag).  A NaN in bias or a logit of +inf with softmax scores gives
- * unspecified (in-range, distinct) experts and weights for its tokens.  Choice values
+ * unspecified experts (distinct ones in range, or -1) and weights for its tokens.  Choice values
  * are compared in double precision; without bias and groups the logits themselves
  * decide, which is the same order, exactly.  The weights are computed in fp32 from
  * ratios that neither overflow nor underflow for finite logits. */

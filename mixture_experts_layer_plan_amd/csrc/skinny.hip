@@ -216,9 +216,12 @@ __global__ __launch_bounds__(512) void dot_kernel(DotArgs p) {
 // Measured: fragments loaded from memory without LDS took 121 us for the 8192 x 256 x 7168
 // router product (16 lanes in 16 rows keep the address unit busy for 64 cycles a KiB), 64 x
 // 128 tiles 53 us, 128 x 128 tiles with two sets of wavefronts 45 us and 6.5 us for the sum
-// of the two parts.  Bound by what passes through a CU's L1: the direct loads alone, without
-// a product or a store, take 39 us, x alone 23 us and the weights, which come from L2, 12 us
-// (each 64 rows x 128 columns less of tile costs 235 MB more and 13 us); fragments read one
+// of the two parts.  Of those 45 us the direct loads alone, without a product or a store, take
+// 39: 470 MB out of L2 (10 TB/s, where direct loads from L2 reach 29), 147 MB of them from
+// memory (3.2 TB/s).  x alone takes 23 us and the weights, which come from L2, 12: the two add
+// up instead of overlapping (each 64 rows x 128 columns less of tile costs 235 MB more and 13
+// us).  Nothing is full, the matrix units are 26 % busy; that a CU's L1 answers in order, so
+// that the weights wait behind x, would explain it and has not been shown.  Fragments read one
 // step ahead of their products, 3 or 5 stages, and K from another start in each tile change
 // nothing.  128 x 256 tiles with 4 parts would save 4 us of loads and cost 4 us of parts.
 // Rank 64 over 8192 rows of 7168 (117 MB, 8 adapters): 31 to 33 us against 20 to 31 us for the
@@ -869,8 +872,9 @@ __global__ __launch_bounds__(512) void dot_expand_kernel(DotArgs d, ExpandArgs p
 // branches around them the compiler waits for all that is in flight, stores included, which
 // took a plain copy of this pattern from 48 to 73 us (8192 x 7168).
 // 8192 rows of 7168 at rank 64: 56 to 57 us for 235 MB, against 45 to 48 us for that copy;
-// the router's dx is bound by its LDS reads (every fragment is read by four wavefronts) and
-// by the start of its workgroups, which put 64 rows of d_logits in LDS first (15 us).
+// the router's dx (46 us) spends 15 us on the start of its workgroups, which put 64 rows of
+// d_logits in LDS first; after that nothing is full (matrix units 26 % busy, vector issue 23 %,
+// 160 MB to and from memory), a wavefront reads its fragments, multiplies and stores in a row.
 template <int MB, int KS, bool NN, bool GR>
 __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(ExpandArgs p) {
   constexpr int SB = KS >= 4 ? 1 : 4 / KS;  // column blocks of a stage
@@ -1076,13 +1080,14 @@ __global__ __launch_bounds__(256, MB * KS <= 8 ? 2 : 1) void expand_tile_kernel(
 // loads into a ring of 32-row tiles, x as whole 256-byte pieces of its rows, the short one
 // as the halves that `expand` left in fragment order, so that enough is in flight without
 // registers (8192 rows of 7168 at rank 64, x and dy: 235 MB in 58 us; with both in registers
-// one tile ahead 88 us).  The router's (256 x 7168 over 4096 rows) takes 38 us, bound by its
-// LDS reads and the turning, which eight wavefronts repeat for 32 rows of j each; 64 rows
-// each leave one wavefront a SIMD and take 46 us.  A lane reads 8 rows of 8 columns and
-// turns them in registers into 8 fragments along the
-// rows; row i of fragment f stands for column 8 i + f.  With the halves as the M side a lane
-// ends with 4 neighbouring j of 8 neighbouring h: it stores 8 h of a row (16 lanes: 128 of
-// them) for [J][H], 4 j for [H][J] (TR).
+// one tile ahead 88 us).  The router's (256 x 7168 over 4096 rows) takes 37 us, in which
+// nothing is full (matrix units 32 % busy, vector issue 24 %, 352 MB out of L2, 124 MB to and
+// from memory): each wavefront waits for its reads, turns them and multiplies in a row, two
+// wavefronts a SIMD, and eight repeat the turning for 32 rows of j each; 64 rows each leave
+// one wavefront a SIMD and take 46 us.  A lane reads 8 rows of 8 columns and turns them in
+// registers into 8 fragments along the rows; row i of fragment f stands for column 8 i + f.
+// With the halves as the M side a lane ends with 4 neighbouring j of 8 neighbouring h: it
+// stores 8 h of a row (16 lanes: 128 of them) for [J][H], 4 j for [H][J] (TR).
 template <int JT, int WJ>
 struct WgradTile {
   static constexpr int WK = 4 / WJ, JB = JT * WJ;       // 16-row blocks of j

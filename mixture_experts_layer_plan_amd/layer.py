@@ -17,7 +17,7 @@ Options of ``LayerBuffers`` beside the layer's shape:
                [n, rank, H], ``lora_b`` bf16 [n, H, rank], ``lora_scale`` fp32 [n] and
                ``adapter_idx`` int32 [T] (-1: no adapter); the gradients are ``d_lora_a`` and
                ``d_lora_b``.  y and dx are rounded to bf16 before the adapters' terms join
-               them, and again after.
+               them, and again after; dx a third time when the router's term joins it.
 """
 from __future__ import annotations
 
