@@ -532,6 +532,185 @@ moe_status moe_lora_backward_bf16(const moe_lora_shape* shape, const void* plan,
                                   void* d_lora_a, void* d_lora_b, void* ws, size_t ws_bytes,
                                   hipStream_t stream);
 
+/* ----------------------------------------- norm in front of the layer, bf16/f32
+ * With h the row that is normalised, joined with the residual stream,
+ *   h = x + residual, rounded once to the element type (h = x where residual is NULL)
+ *   y = (h - mean) / sqrt(variance + eps) * w + b, rounded once,
+ * over the H values of a row: mean and variance of h (MOE_NORM_LAYER), or 0 and the mean
+ * of h^2 (MOE_NORM_RMS).  Sums are in fp32, the variance from the differences to the mean.
+ *   0 <= T; H a multiple of 8 in [8, 16384]; eps in (0, 1]
+ * Where a value of a row is not finite, its rows of y and dx are not valid (NaN among them),
+ * nor are dw and db; other rows are. */
+typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
+typedef struct {
+  int32_t T, H;
+  int32_t kind; /* moe_norm_kind */
+  float eps;
+} moe_norm_shape;
+
+/* Forward.
+ *   x, residual [T, H]  in (residual may be NULL)
+ *   w, b [H]            in, of the element type; NULL: 1 and 0
+ *   h [T, H]            out, with residual and only with it; it may be x or residual itself
+ *   y [T, H]            out; it may be x or residual itself, but shares no bytes with h
+ *   stats fp32 [T, 2]   out: mean (0 for RMS) and 1 / sqrt(variance + eps) of each row, which
+ *                       the backward reads
+ * Outputs that share bytes with an input that begins elsewhere: MOE_E_UNSUPPORTED. */
+moe_status moe_norm_bf16(const moe_norm_shape* shape, const void* x, const void* residual,
+                         const void* w, const void* b, void* h, void* y, float* stats,
+                         hipStream_t stream);
+moe_status moe_norm_f32(const moe_norm_shape* shape, const float* x, const float* residual,
+                        const float* w, const float* b, float* h, float* y, float* stats,
+                        hipStream_t stream);
+
+/* Backward, from the forward's h (its x where there was no residual), w and stats:
+ *   dx [T, H] = dh_in + gradient of h (the gradient of x and of residual alike), rounded
+ *               once; dh_in [T, H], what reaches h on the residual stream, or NULL (zero)
+ *   dw, db [H]  overwritten, rounded once from fp32 sums over the rows (zeros with T == 0);
+ *               NULL: not wanted
+ * dx may be dy or dh_in itself, and shares no bytes with h (MOE_E_UNSUPPORTED otherwise, as
+ * for a dy or dh_in that begins elsewhere in dx).
+ * ws [ws_bytes >= moe_norm_workspace_bytes(shape)], read only with dw or db. */
+moe_status moe_norm_backward_bf16(const moe_norm_shape* shape, const void* h, const void* w,
+                                  const float* stats, const void* dy, const void* dh_in, void* dx,
+                                  void* dw, void* db, void* ws, size_t ws_bytes,
+                                  hipStream_t stream);
+moe_status moe_norm_backward_f32(const moe_norm_shape* shape, const float* h, const float* w,
+                                 const float* stats, const float* dy, const float* dh_in,
+                                 float* dx, float* dw, float* db, void* ws, size_t ws_bytes,
+                                 hipStream_t stream);
+
+/* Scratch bytes of the backward; 0 for shapes it refuses. */
+size_t moe_norm_workspace_bytes(const moe_norm_shape* shape);
+
+/* ------------------------------------------------------- balance of the experts
+ * The tokens of a batch form n_seq sequences, sequence i being the tokens
+ * [seq_start[i], seq_start[i + 1]); tokens before the first and behind the last belong to
+ * none (padding).  A token counts if one of its topk_idx at least is an expert, so that a
+ * token that the plan leaves out (-1) has no part.  With N_i the tokens of sequence i that
+ * count, n the number of sequences with such tokens, c_ie the pairs of sequence i on expert
+ * e, and p_te the token's scores as shares of their sum over the experts (softmax of the
+ * logits, or sigmoids over their sum):
+ *   loss = coef / n * sum_i E / (k N_i^2) * sum_e c_ie * sum_{t in i} p_te
+ * which is coef where all experts have the same load.  n_seq = 1 balances the batch as a
+ * whole.  An expert whose logit is -inf or NaN has no share; a logit of +inf with softmax
+ * scores gives unspecified (possibly NaN) losses and gradients.
+ *   n_seq in [1, 2^20], coef finite; T <= 2^26 - 4 (MOE_E_UNSUPPORTED otherwise); of the
+ *   shape, T, E and k are used. */
+typedef struct {
+  int32_t score; /* moe_score */
+  int32_t n_seq;
+  float coef;
+} moe_balance;
+
+/* Loss and counts.
+ *   logits    fp32 [T, E], topk_idx int32 [T, k]  in (ids outside [0, E): no expert)
+ *   seq_start int32 [n_seq + 1]  in, ascending, or NULL with n_seq = 1 (all tokens); entries
+ *             that do not ascend give unspecified results
+ *   loss      fp32 [1]          out
+ *   counts    int32 [n_seq, E]  out: c_ie
+ *   scales    fp32 [n_seq]      out: coef E / (k N_i^2 n), 0 for sequences without tokens;
+ *             the backward reads them
+ *   ws [ws_bytes >= moe_balance_workspace_bytes(shape, balance)] */
+moe_status moe_balance_loss(const moe_shape* shape, const moe_balance* balance,
+                            const float* logits, const int32_t* topk_idx,
+                            const int32_t* seq_start, float* loss, int32_t* counts, float* scales,
+                            void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Gradient of the logits; the counts have none.
+ *   d_logits [t, e] = d_in [t, e] + d_loss * scales_i * p_te (c_ie - sum_j p_tj c_ij), times
+ *                     1 - sigmoid for sigmoid scores; rows of tokens without a part: d_in
+ *   d_loss fp32 [1] or NULL (1); d_in fp32 [T, E] or NULL (zero).  d_logits may be d_in (the
+ *   routing's gradient, joined in place) or logits itself; it shares no bytes with one that
+ *   begins elsewhere (MOE_E_UNSUPPORTED). */
+moe_status moe_balance_loss_backward(const moe_shape* shape, const moe_balance* balance,
+                                     const float* logits, const int32_t* topk_idx,
+                                     const int32_t* seq_start, const int32_t* counts,
+                                     const float* scales, const float* d_loss, const float* d_in,
+                                     float* d_logits, hipStream_t stream);
+
+/* Scratch bytes of the loss; 0 for shapes it refuses. */
+size_t moe_balance_workspace_bytes(const moe_shape* shape, const moe_balance* balance);
+
+/* ------------------------------------------------------------------- AdamW step
+ * One step over many tensors in one launch.  For every element, with g the gradient times
+ * grad_scale:
+ *   m' = beta1 m + (1 - beta1) g,  v' = beta2 v + (1 - beta2) g^2
+ *   p' = p - lr (m' corr1 / (sqrt(v' corr2) + eps) + weight_decay p),  corr = 1 / (1 - beta^step)
+ * all in fp32.  All tensors of a table have the same types:
+ *   p_type, g_type  MOE_F32 or MOE_BF16, of the parameters and of the gradients
+ *   master          1: bf16 parameters are copies, rounded to nearest, of fp32 masters that
+ *                   the step reads and writes.  bf16 parameters without masters are rounded
+ *                   at random to one of their two neighbours, in proportion to the
+ *                   distances, as lr * update is mostly less than half a step of theirs
+ *   state_bits      32: m and v are fp32.  8: a byte each, with a scale byte (E8M0, 2^(b - 127),
+ *                   255: NaN) for every 32 neighbouring elements of a tensor; m in E4M3, v in
+ *                   5 exponent and 3 mantissa bits without a sign (code c > 0 stands for
+ *                   (1 + c%8 / 8) 2^(c/8 - 31)).  Both are rounded at random; v > 0 does not
+ *                   become 0.  A block that holds a value that is not finite, or one of 2^126
+ *                   and more, becomes NaN as a whole.  Zeroed buffers are the start (of 32
+ *                   bits too).
+ * The random bits come from the step's seed and the element's place alone: the same call
+ * gives the same bits, another step takes another seed.
+ *   n_tensors in [1, MOE_ADAMW_MAX_TENSORS]; elements: the sum of the tensors' n;
+ *   elements / 8192 + n_tensors < 2^24 (MOE_E_UNSUPPORTED otherwise) */
+#define MOE_ADAMW_MAX_TENSORS 65536
+typedef struct {
+  int64_t elements;
+  int32_t n_tensors;
+  int32_t p_type, g_type; /* moe_dtype: MOE_F32 or MOE_BF16 */
+  int32_t master;         /* 0 or 1 */
+  int32_t state_bits;     /* 32 or 8 */
+} moe_adamw_shape;
+
+/* One tensor of n elements, n of any value (0: the pointers may be NULL).  Each output may
+ * be its own input (a step in place) or lie elsewhere (a step that can be taken back).  param
+ * is not read with masters; master, master_out only with masters, the scales [(n + 31) / 32]
+ * only with state_bits = 8 (NULL otherwise). */
+typedef struct {
+  const void *grad, *param, *m, *v;
+  const float* master;
+  const uint8_t *m_scale, *v_scale;
+  void *param_out, *m_out, *v_out;
+  float* master_out;
+  uint8_t *m_scale_out, *v_scale_out;
+  int64_t n;
+  float weight_decay;
+  int32_t reserved;
+} moe_adamw_tensor;
+
+/* Writes the table that the steps read, from `tensors`, an array in HOST memory that is read
+ * before the call returns; once for as long as the tensors stay where they are.  No output
+ * may share bytes with another output or with an input other than its own, of any tensor
+ * (MOE_E_UNSUPPORTED).  table [moe_adamw_table_bytes(shape)]. */
+size_t moe_adamw_table_bytes(const moe_adamw_shape* shape);
+moe_status moe_adamw_table(const moe_adamw_shape* shape, const moe_adamw_tensor* tensors,
+                           void* table, hipStream_t stream);
+
+/* A step's scalars as the kernel takes them (fp32, each rounded once from double). */
+typedef struct {
+  float lr, beta1, one_minus_beta1, beta2, one_minus_beta2, eps, corr1, corr2, grad_scale;
+  uint32_t seed;
+} moe_adamw_hyper;
+
+/* Fills `out` (host memory): step >= 1, 0 <= beta < 1, eps in [1e-30, 1], lr and grad_scale
+ * finite. */
+moe_status moe_adamw_hyper_of(double lr, double beta1, double beta2, double eps, int64_t step,
+                              double grad_scale, uint32_t seed, moe_adamw_hyper* out);
+
+/* The step.  Its scalars come from host memory (hyper, read before the call returns) or from
+ * device memory (hyper_dev, read by the kernel: a captured graph replays with what lies there
+ * then, and grad_scale may be the work of an earlier kernel); the other is NULL. */
+moe_status moe_adamw_step(const moe_adamw_shape* shape, const void* table,
+                          const moe_adamw_hyper* hyper, const moe_adamw_hyper* hyper_dev,
+                          hipStream_t stream);
+
+/* The values that the codes of 8-bit states stand for, out bf16 [n] (exact for values from
+ * bf16's smallest normal number up). */
+typedef enum { MOE_ADAMW_M = 0, MOE_ADAMW_V = 1 } moe_adamw_state;
+moe_status moe_adamw_values(int32_t which, int64_t n, const uint8_t* codes, const uint8_t* scales,
+                            void* out, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

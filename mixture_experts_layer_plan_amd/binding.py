@@ -58,7 +58,39 @@ class moe_lora_shape(ctypes.Structure):
                 ("n_adapters", ctypes.c_int32), ("rank", ctypes.c_int32)]
 
 
+class moe_norm_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class moe_balance(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_seq", ctypes.c_int32), ("coef", ctypes.c_float)]
+
+
+class moe_adamw_shape(ctypes.Structure):
+    _fields_ = [("elements", ctypes.c_int64), ("n_tensors", ctypes.c_int32),
+                ("p_type", ctypes.c_int32), ("g_type", ctypes.c_int32),
+                ("master", ctypes.c_int32), ("state_bits", ctypes.c_int32)]
+
+
+class moe_adamw_tensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "grad", "param", "m", "v", "master", "m_scale", "v_scale", "param_out", "m_out", "v_out",
+        "master_out", "m_scale_out", "v_scale_out")] + \
+        [("n", ctypes.c_int64), ("weight_decay", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class moe_adamw_hyper(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_float) for n in (
+        "lr", "beta1", "one_minus_beta1", "beta2", "one_minus_beta2", "eps", "corr1", "corr2",
+        "grad_scale")] + [("seed", ctypes.c_uint32)]
+
+
 _P = ctypes.c_void_p
+_NS = ctypes.POINTER(moe_norm_shape)
+_BA = ctypes.POINTER(moe_balance)
+_AS = ctypes.POINTER(moe_adamw_shape)
+_AH = ctypes.POINTER(moe_adamw_hyper)
 _S = ctypes.POINTER(moe_shape)
 _SC = ctypes.POINTER(moe_scoring)
 _LS = ctypes.POINTER(moe_lora_shape)
@@ -95,6 +127,20 @@ _SIGS = {
     "moe_lora_workspace_bytes": (_Z, [_LS, _I]),
     "moe_lora_bf16": (_I, [_LS] + [_P] * 9 + [_Z, _P]),
     "moe_lora_backward_bf16": (_I, [_LS] + [_P] * 12 + [_Z, _P]),
+    "moe_norm_bf16": (_I, [_NS] + [_P] * 8),
+    "moe_norm_f32": (_I, [_NS] + [_P] * 8),
+    "moe_norm_backward_bf16": (_I, [_NS] + [_P] * 9 + [_Z, _P]),
+    "moe_norm_backward_f32": (_I, [_NS] + [_P] * 9 + [_Z, _P]),
+    "moe_norm_workspace_bytes": (_Z, [_NS]),
+    "moe_balance_loss": (_I, [_S, _BA] + [_P] * 7 + [_Z, _P]),
+    "moe_balance_loss_backward": (_I, [_S, _BA] + [_P] * 9),
+    "moe_balance_workspace_bytes": (_Z, [_S, _BA]),
+    "moe_adamw_table_bytes": (_Z, [_AS]),
+    "moe_adamw_table": (_I, [_AS, ctypes.POINTER(moe_adamw_tensor), _P, _P]),
+    "moe_adamw_hyper_of": (_I, [ctypes.c_double] * 4 + [ctypes.c_int64, ctypes.c_double,
+                                                       ctypes.c_uint32, _AH]),
+    "moe_adamw_step": (_I, [_AS, _P, _AH, _P, _P]),
+    "moe_adamw_values": (_I, [ctypes.c_int32, ctypes.c_int64, _P, _P, _P, _P]),
     "moe_plan": (_I, [_S, _P, _P, _P]),
     "moe_dispatch_bf16": (_I, [_S, _P, _P, _P, _P]),
     "moe_dispatch_f32": (_I, [_S, _P, _P, _P, _P]),
@@ -509,6 +555,151 @@ def moe_lora_backward_bf16(s, plan, x, lora_a, lora_b, scale, saved, dy, dx_in, 
           _buf(saved, sb, d), _here(dy, _BF16, T * ho, d), _here(dx_in, _BF16, T * hi, d),
           _here(dx, _BF16, T * hi, d), _here(d_lora_a, _BF16, na, d),
           _here(d_lora_b, _BF16, nb, d), *_ws(ws, d), _stream(stream))
+
+
+# ---------------------------------- norm, balance of the experts, AdamW step
+MOE_NORM_LAYER, MOE_NORM_RMS = 0, 1
+NORMS = {"layer": MOE_NORM_LAYER, "rms": MOE_NORM_RMS}
+MOE_ADAMW_M, MOE_ADAMW_V = 0, 1
+MOE_ADAMW_MAX_TENSORS = 65536
+
+
+def norm_shape(T, H, kind="layer", eps=1e-5) -> moe_norm_shape:
+    if kind not in NORMS:
+        raise ValueError(f"unsupported norm {kind!r}")
+    return moe_norm_shape(int(T), int(H), NORMS[kind], float(eps))
+
+
+def _norm(name, dt, s, x, residual, w, b, h, y, stats, stream):
+    n, H, d = s.T * s.H, s.H, _dev()
+    _call(name, ctypes.byref(s), _here(x, dt, n, d), _here(residual, dt, n, d), _here(w, dt, H, d),
+          _here(b, dt, H, d), _here(h, dt, n, d), _here(y, dt, n, d), _here(stats, _F32, 2 * s.T, d),
+          _stream(stream))
+
+
+def _norm_backward(name, dt, s, h, w, stats, dy, dh_in, dx, dw, db, ws, stream):
+    n, H, d = s.T * s.H, s.H, _dev()
+    _call(name, ctypes.byref(s), _here(h, dt, n, d), _here(w, dt, H, d),
+          _here(stats, _F32, 2 * s.T, d), _here(dy, dt, n, d), _here(dh_in, dt, n, d),
+          _here(dx, dt, n, d), _here(dw, dt, H, d), _here(db, dt, H, d), *_ws(ws, d),
+          _stream(stream))
+
+
+def moe_norm_bf16(s, x, residual, w, b, h, y, stats, stream=None):
+    _norm("moe_norm_bf16", _BF16, s, x, residual, w, b, h, y, stats, stream)
+
+
+def moe_norm_f32(s, x, residual, w, b, h, y, stats, stream=None):
+    _norm("moe_norm_f32", _F32, s, x, residual, w, b, h, y, stats, stream)
+
+
+def moe_norm_backward_bf16(s, h, w, stats, dy, dh_in, dx, dw, db, ws, stream=None):
+    _norm_backward("moe_norm_backward_bf16", _BF16, s, h, w, stats, dy, dh_in, dx, dw, db, ws, stream)
+
+
+def moe_norm_backward_f32(s, h, w, stats, dy, dh_in, dx, dw, db, ws, stream=None):
+    _norm_backward("moe_norm_backward_f32", _F32, s, h, w, stats, dy, dh_in, dx, dw, db, ws, stream)
+
+
+def moe_norm_workspace_bytes(s: moe_norm_shape) -> int:
+    return lib().moe_norm_workspace_bytes(ctypes.byref(s))
+
+
+def balance(score="softmax", coef=0.01, n_seq=1) -> moe_balance:
+    if score not in SCORES:
+        raise ValueError(f"unsupported score {score!r}")
+    return moe_balance(SCORES[score], int(n_seq), float(coef))
+
+
+def moe_balance_workspace_bytes(s: moe_shape, ba: moe_balance) -> int:
+    return lib().moe_balance_workspace_bytes(ctypes.byref(s), ctypes.byref(ba))
+
+
+def moe_balance_loss(s, ba, logits, topk_idx, seq_start, loss, counts, scales, ws, stream=None):
+    T, E, k, n, d = s.T, s.E, s.k, ba.n_seq, _dev()
+    _call("moe_balance_loss", ctypes.byref(s), ctypes.byref(ba), _here(logits, _F32, T * E, d),
+          _here(topk_idx, torch.int32, T * k, d), _here(seq_start, torch.int32, n + 1, d),
+          _here(loss, _F32, 1, d), _here(counts, torch.int32, n * E, d), _here(scales, _F32, n, d),
+          *_ws(ws, d), _stream(stream))
+
+
+def moe_balance_loss_backward(s, ba, logits, topk_idx, seq_start, counts, scales, d_loss, d_in,
+                              d_logits, stream=None):
+    T, E, k, n, d = s.T, s.E, s.k, ba.n_seq, _dev()
+    _call("moe_balance_loss_backward", ctypes.byref(s), ctypes.byref(ba),
+          _here(logits, _F32, T * E, d), _here(topk_idx, torch.int32, T * k, d),
+          _here(seq_start, torch.int32, n + 1, d), _here(counts, torch.int32, n * E, d),
+          _here(scales, _F32, n, d), _here(d_loss, _F32, 1, d), _here(d_in, _F32, T * E, d),
+          _here(d_logits, _F32, T * E, d), _stream(stream))
+
+
+def adamw_shape(elements, n_tensors, p_type="bf16", g_type="bf16", master=False,
+                state_bits=32) -> moe_adamw_shape:
+    for t in (p_type, g_type):
+        if t not in ("bf16", "f32"):
+            raise ValueError(f"unsupported type {t!r}")
+    return moe_adamw_shape(int(elements), int(n_tensors), DTYPES[p_type], DTYPES[g_type],
+                           int(bool(master)), int(state_bits))
+
+
+def adamw_hyper(lr, beta1=0.9, beta2=0.95, eps=1e-8, step=1, grad_scale=1.0, seed=0) -> moe_adamw_hyper:
+    """A step's scalars; ``bytes(...)`` of it is what a device copy holds."""
+    out = moe_adamw_hyper()
+    _call("moe_adamw_hyper_of", float(lr), float(beta1), float(beta2), float(eps), int(step),
+          float(grad_scale), int(seed) & 0xFFFFFFFF, ctypes.byref(out))
+    return out
+
+
+def moe_adamw_table_bytes(s: moe_adamw_shape) -> int:
+    return lib().moe_adamw_table_bytes(ctypes.byref(s))
+
+
+def moe_adamw_table(s, tensors, table, stream=None):
+    """``tensors``: a dict for each, with ``grad``, ``param``, ``m``, ``v`` and, where the shape
+    has them, ``master``, ``m_scale`` and ``v_scale``; ``weight_decay`` (0 if absent); and for an
+    output elsewhere than over its input its name with ``_out``.  The table holds their
+    addresses: they have to stay where they are."""
+    d = _dev()
+    if len(tensors) != s.n_tensors:
+        raise ValueError(f"expected {s.n_tensors} tensors, got {len(tensors)}")
+    types = {MOE_F32: _F32, MOE_BF16: _BF16}
+    state = _F32 if s.state_bits == 32 else torch.uint8
+    kinds = {"param": types[s.p_type], "m": state, "v": state}
+    if s.master:
+        kinds["master"] = _F32
+    if s.state_bits == 8:
+        kinds["m_scale"] = kinds["v_scale"] = torch.uint8
+    arr = (moe_adamw_tensor * s.n_tensors)()
+    for a, t in zip(arr, tensors):
+        unknown = set(t) - {"grad", "weight_decay"} - set(kinds) - {k + "_out" for k in kinds}
+        if unknown:
+            raise ValueError(f"no place for {sorted(unknown)} in this shape")
+        a.n = n = t["grad"].numel()
+        a.weight_decay = t.get("weight_decay", 0.0)
+        a.grad = _here(t["grad"], types[s.g_type], n, d)
+        for k, dt in kinds.items():
+            m = (n + 31) // 32 if k.endswith("scale") else n
+            setattr(a, k, _here(t[k], dt, m, d))
+            setattr(a, k + "_out", _here(t.get(k + "_out", t[k]), dt, m, d))
+    _call("moe_adamw_table", ctypes.byref(s), arr, _buf(table, moe_adamw_table_bytes(s), d),
+          _stream(stream))
+
+
+def moe_adamw_step(s, table, hyper, stream=None):
+    """``hyper``: an ``adamw_hyper`` of this step, or a device tensor of the bytes of one."""
+    d = _dev()
+    dev = isinstance(hyper, torch.Tensor)
+    _call("moe_adamw_step", ctypes.byref(s), _buf(table, moe_adamw_table_bytes(s), d),
+          None if dev else ctypes.byref(hyper),
+          _buf(hyper, ctypes.sizeof(moe_adamw_hyper), d) if dev else None, _stream(stream))
+
+
+def moe_adamw_values(which, codes, scales, out, stream=None):
+    """``which``: "m" or "v"."""
+    n, d = codes.numel(), _dev()
+    _call("moe_adamw_values", {"m": MOE_ADAMW_M, "v": MOE_ADAMW_V}[which], n,
+          _here(codes, torch.uint8, n, d), _here(scales, torch.uint8, (n + 31) // 32, d),
+          _here(out, _BF16, n, d), _stream(stream))
 
 
 # ------------------------------------------------------------ kernel timing

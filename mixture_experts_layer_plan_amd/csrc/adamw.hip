@@ -1,0 +1,324 @@
+// One AdamW step over many tensors in one launch.  For every element, with g the gradient
+// times grad_scale:
+//   m' = beta1 m + (1 - beta1) g            each product and sum rounded to fp32
+//   v' = beta2 v + ((1 - beta2) g) g
+//   p' = p - lr ((m' corr1) / (sqrt(v' corr2) + eps) + weight_decay p)
+// with corr = 1 / (1 - beta^step).  The states' sums are not contracted, so that their 8-bit
+// codes are the same wherever the formula is evaluated in fp32.
+//
+// States of 8 bits: blocks of 32 neighbouring elements of a tensor share a power of two, an
+// E8M0 byte.  m is E4M3; v, which is never negative, has 5 exponent and 3 mantissa bits
+// (code c > 0 stands for (1 + c%8 / 8) 2^(c/8 - 31), 0 for 0), as its range is that of g
+// squared.  Both are rounded to one of their two neighbours at random, in proportion to the
+// distances, so that the average over steps is the state: rounded to nearest, a v would
+// stay where it is while a step moves it by less than half a code (6 %), and with beta2 =
+// 0.999 a step moves it by 0.1 %.  A power-of-two scale keeps codes on the grid from step to
+// step, so that the variance that a step adds is |v' - v| times the distance of two codes,
+// not its square.  v > 0 never becomes 0: the smallest code is its floor, as a denominator
+// that vanishes would throw the weight far off.
+//
+// bf16 parameters without a master are rounded at random as well: to nearest, a weight would
+// stay where it is while lr is below 2^-9 of it.
+//
+// 32 random bits per element come from the step's seed, the tensor's place in the table and
+// the element's place in the tensor through mix32 below: m takes the low half, v the high
+// half, p their difference by xor (pairwise independent).
+#include "common.hpp"
+#include "internal.hpp"
+#include "step.hpp"
+
+namespace moe {
+namespace {
+
+// Mixes the bits of x: two multiplications by the fractions of the square roots of 19 and 3
+// between shifts (every bit of x turns every bit of the result with probability 0.49 to 0.51).
+MOE_DEV uint32_t mix32(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x5BE0CD19u;
+  x ^= x >> 15;
+  x *= 0xBB67AE85u;
+  return x ^ (x >> 16);
+}
+
+MOE_DEV float max_of_four_lanes(float v) {
+  const auto swap = [](float x, int ctrl_is_pair) {
+    const int i = __float_as_int(x);
+    return __int_as_float(ctrl_is_pair ? __builtin_amdgcn_update_dpp(0, i, 0xB1, 0xf, 0xf, true)
+                                       : __builtin_amdgcn_update_dpp(0, i, 0x4E, 0xf, 0xf, true));
+  };
+  v = fmaxf(v, swap(v, 1));
+  return fmaxf(v, swap(v, 0));
+}
+
+// The scale byte of a block whose largest magnitude is `top`: the smallest 2^(e - 127) with
+// top <= largest code * scale; CARRY is what carries into the exponent past that code's
+// mantissa, SHIFT its exponent.  255 (NaN) where the state is not finite or past 2^126.
+template <uint32_t CARRY, int SHIFT>
+MOE_DEV uint32_t scale_byte(float top) {
+  const uint32_t u = __float_as_uint(top);
+  if (!(top < 8.5070592e37f)) return 255u;
+  const int e = (int)((u + CARRY) >> 23) - SHIFT;
+  return e < 1 ? 1u : (uint32_t)e;
+}
+// 2^(127 - e), e in [1, 253]
+MOE_DEV float inverse_scale(uint32_t e) { return __uint_as_float((254u - e) << 23); }
+// 2^(e - 127); +0 for e = 0 (a buffer of zeros: codes of zero), inf for 255
+MOE_DEV float scale_of(uint32_t e) { return __uint_as_float(e << 23); }
+
+constexpr uint32_t M_CARRY = 0x1FFFFFu, V_CARRY = 0x0FFFFFu;  // past 1.75 (448), past 1.875
+constexpr int M_SHIFT = 8, V_SHIFT = 0;
+
+MOE_DEV uint32_t encode_m(float m, float inv, uint32_t r16) {
+  const float y = fabsf(m) * inv;
+  const bool low = y < 0x1p-6f;  // below the normal codes the distance stays 2^-9
+  const float z = low ? y + 0x1p-6f : y;
+  const uint32_t c = ((__float_as_uint(z) + (r16 << 4 | 8u)) >> 20) - (low ? 968u : 960u);
+  return c | (__float_as_uint(m) >> 31 << 7);
+}
+MOE_DEV uint32_t encode_v(float v, float inv, uint32_t r16) {
+  const uint32_t c = (__float_as_uint(v * inv) + (r16 << 4 | 8u)) >> 20;
+  return v > 0.0f ? (c > 769u ? c : 769u) - 768u : 0u;
+}
+MOE_DEV float decode_v(uint32_t c) { return c ? __uint_as_float((c + 768u) << 20) : 0.0f; }
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+// four E4M3 codes of one word
+MOE_DEV void decode_m4(uint32_t w, float* f) {
+  const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+  const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+  f[0] = lo.x; f[1] = lo.y; f[2] = hi.x; f[3] = hi.y;
+}
+
+MOE_DEV float round_bf16_at_random(float p, uint32_t r) {
+  const uint32_t u = __float_as_uint(p);
+  if ((u & 0x7f800000u) == 0x7f800000u) return p;  // inf and NaN as they are
+  return __uint_as_float((u + (r & 0xffffu)) & 0xffff0000u);
+}
+
+MOE_DEV void update_state(float& m, float& v, float& g, const AdamwHyper& h) {
+#pragma clang fp contract(off)
+  g = g * h.grad_scale;
+  m = m * h.beta1 + g * h.one_minus_beta1;
+  v = v * h.beta2 + (g * h.one_minus_beta2) * g;
+}
+
+template <bool F32>
+MOE_DEV void load8(const void* p, int64_t i, int cnt, float* f) {
+  if (cnt == 8) {
+    if (F32) {
+      const float4 a = *(const float4*)((const float*)p + i), b = *(const float4*)((const float*)p + i + 4);
+      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    } else {
+      unpack8(*(const uint4*)((const bf16_t*)p + i), f);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    f[j] = 0.0f;
+    if (j < cnt) f[j] = F32 ? ((const float*)p)[i + j] : bf16_to_f32(((const bf16_t*)p)[i + j]);
+  }
+}
+template <bool F32>
+MOE_DEV void store8(void* p, int64_t i, int cnt, const float* f) {
+  if (cnt == 8) {
+    if (F32) {
+      *(float4*)((float*)p + i) = make_float4(f[0], f[1], f[2], f[3]);
+      *(float4*)((float*)p + i + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+      *(uint4*)((bf16_t*)p + i) = pack8(f);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (j < cnt) {
+      if (F32) ((float*)p)[i + j] = f[j];
+      else ((bf16_t*)p)[i + j] = f32_to_bf16(f[j]);
+    }
+  }
+}
+// eight codes; zeros past the end
+MOE_DEV uint2 load_codes(const void* p, int64_t i, int cnt) {
+  if (cnt == 8) return *(const uint2*)((const uint8_t*)p + i);
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < cnt) w[j >> 2] |= (uint32_t)((const uint8_t*)p)[i + j] << (8 * (j & 3));
+  return make_uint2(w[0], w[1]);
+}
+MOE_DEV void store_codes(void* p, int64_t i, int cnt, uint2 v) {
+  if (cnt == 8) {
+    *(uint2*)((uint8_t*)p + i) = v;
+    return;
+  }
+  const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < cnt) ((uint8_t*)p)[i + j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+}
+
+// The tensor of a tile: the last entry of first[0 .. n) that is <= tile and whose tensor has
+// tiles (first ascends; a tensor without elements has none).  64 entries a step.
+MOE_DEV int tensor_of(const int32_t* first, int n, int tile) {
+  int lo = 0, hi = n;  // first[lo] <= tile < first[hi]
+  while (hi - lo > 1) {
+    const int step = (hi - lo - 1 + 63) / 64;
+    const int i = lo + ((int)(threadIdx.x & 63) + 1) * step;
+    const int ones = __popcll(ballot64(i < hi && first[i] <= tile));
+    const int nhi = lo + (ones + 1) * step;
+    hi = nhi < hi ? nhi : hi;
+    lo += ones * step;
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+template <bool P32, bool G32, bool MASTER, bool EIGHT>
+__global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
+  const int tile = blockIdx.x;
+  if (tile >= a.first[a.n_tensors]) return;
+  const int id = tensor_of(a.first, a.n_tensors, tile);
+  const AdamwDesc d = a.desc[id];
+  const AdamwHyper h = a.hyper_dev ? *a.hyper_dev : a.hyper;
+  const int64_t tile0 = (int64_t)(tile - a.first[id]) * ADAMW_TILE;
+  // (a tile starts at a multiple of 2^13, so the high word of the place is the tile's)
+  const uint32_t key = mix32(mix32((uint32_t)id + 1u) + h.seed) + (uint32_t)(tile0 >> 32) * 0x3C6EF373u;
+#pragma unroll 1
+  for (int it = 0; it < ADAMW_TILE / 2048; ++it) {
+    const int64_t i = tile0 + it * 2048 + (int)threadIdx.x * 8;
+    if (tile0 + it * 2048 >= d.n) break;
+    const int64_t left = d.n - i;
+    const int cnt = left >= 8 ? 8 : left > 0 ? (int)left : 0;
+    float g[8], p[8], m[8], v[8];
+    uint32_t r[8];
+    load8<G32>(d.grad, i, cnt, g);
+    if (MASTER) load8<true>(d.master, i, cnt, p);
+    else load8<P32>(d.param, i, cnt, p);
+    if (EIGHT) {
+      const uint2 mc = load_codes(d.m, i, cnt), vc = load_codes(d.v, i, cnt);
+      const uint32_t me = cnt ? d.m_scale[i >> 5] : 0u, ve = cnt ? d.v_scale[i >> 5] : 0u;
+      decode_m4(mc.x, m);
+      decode_m4(mc.y, m + 4);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m[j] *= scale_of(me);
+        v[j] = decode_v(((j < 4 ? vc.x : vc.y) >> (8 * (j & 3))) & 255u) * scale_of(ve);
+      }
+    } else {
+      load8<true>(d.m, i, cnt, m);
+      load8<true>(d.v, i, cnt, v);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      update_state(m[j], v[j], g[j], h);
+      // reciprocal and root of one unit: the quotient is far below the weight it is added to
+      const float u = m[j] * h.corr1 * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[j] * h.corr2) + h.eps);
+      p[j] = fmaf(-h.lr, fmaf(d.weight_decay, p[j], u), p[j]);
+      if (EIGHT || (!P32 && !MASTER)) r[j] = mix32((uint32_t)(i + j) ^ key);
+    }
+    if (MASTER) store8<true>(d.master_out, i, cnt, p);
+    if (!P32 && !MASTER) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[j] = round_bf16_at_random(p[j], r[j] ^ (r[j] >> 16));
+    }
+    store8<P32>(d.param_out, i, cnt, p);
+    if (EIGHT) {
+      float mt = 0.0f, vt = 0.0f;
+      bool finite = true;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        mt = fmaxf(mt, fabsf(m[j]));
+        vt = fmaxf(vt, v[j]);
+        finite = finite && m[j] - m[j] == 0.0f && v[j] - v[j] == 0.0f;
+      }
+      if (!finite) mt = vt = __builtin_inff();
+      mt = max_of_four_lanes(mt);
+      vt = max_of_four_lanes(vt);
+      const uint32_t me = scale_byte<M_CARRY, M_SHIFT>(mt), ve = scale_byte<V_CARRY, V_SHIFT>(vt);
+      const float mi = inverse_scale(me), vi = inverse_scale(ve);
+      uint32_t mw[2] = {0, 0}, vw[2] = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        mw[j >> 2] |= encode_m(m[j], mi, r[j] & 0xffffu) << (8 * (j & 3));
+        vw[j >> 2] |= encode_v(v[j], vi, r[j] >> 16) << (8 * (j & 3));
+      }
+      // a block that is not finite: codes of zero under a scale of inf, which is NaN
+      store_codes(d.m_out, i, cnt, me == 255u ? make_uint2(0, 0) : make_uint2(mw[0], mw[1]));
+      store_codes(d.v_out, i, cnt, ve == 255u ? make_uint2(0, 0) : make_uint2(vw[0], vw[1]));
+      if (cnt && (threadIdx.x & 3) == 0) {
+        ((uint8_t*)d.m_scale_out)[i >> 5] = (uint8_t)me;
+        ((uint8_t*)d.v_scale_out)[i >> 5] = (uint8_t)ve;
+      }
+    } else {
+      store8<true>(d.m_out, i, cnt, m);
+      store8<true>(d.v_out, i, cnt, v);
+    }
+  }
+}
+
+__global__ __launch_bounds__(64) void adamw_table_kernel(AdamwChunk c, AdamwDesc* desc, int32_t* first) {
+  const int i = threadIdx.x;
+  if (i < c.count) {
+    desc[c.base + i] = c.d[i];
+    first[c.base + i] = c.first[i];
+  }
+  if (i == 0 && c.base + c.count == c.n_tensors) first[c.n_tensors] = c.tiles;
+}
+
+// The values that codes stand for, as bf16 (exact: at most 4 significant bits, down to the
+// type's smallest normal number).
+template <bool V>
+__global__ __launch_bounds__(256) void adamw_values_kernel(int64_t n, const uint8_t* codes,
+                                                           const uint8_t* scales, bf16_t* out) {
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 2048) {
+    const int cnt = n - i >= 8 ? 8 : (int)(n - i);
+    const uint2 c = load_codes(codes, i, cnt);
+    const float s = scale_of(scales[i >> 5]);
+    float f[8];
+    if (V) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = decode_v(((j < 4 ? c.x : c.y) >> (8 * (j & 3))) & 255u) * s;
+    } else {
+      decode_m4(c.x, f);
+      decode_m4(c.y, f + 4);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] *= s;
+    }
+    store8<false>(out, i, cnt, f);
+  }
+}
+
+template <bool P32, bool G32, bool MASTER>
+hipError_t adamw_as(const AdamwArgs& p, bool eight, hipStream_t s) {
+  if (eight)
+    return MOE_LAUNCH("adamw", s, adamw_kernel<P32, G32, MASTER, true><<<p.tiles, 256, 0, s>>>(p));
+  return MOE_LAUNCH("adamw", s, adamw_kernel<P32, G32, MASTER, false><<<p.tiles, 256, 0, s>>>(p));
+}
+
+}  // namespace
+
+hipError_t launch_adamw_table(const AdamwChunk& c, AdamwDesc* desc, int32_t* first, hipStream_t s) {
+  return MOE_LAUNCH("adamw_table", s, adamw_table_kernel<<<1, 64, 0, s>>>(c, desc, first));
+}
+
+hipError_t launch_adamw(const AdamwArgs& p, bool f32, bool g32, bool master, bool eight,
+                        hipStream_t s) {
+  if (p.tiles == 0) return hipSuccess;
+  if (f32) return g32 ? adamw_as<true, true, false>(p, eight, s) : adamw_as<true, false, false>(p, eight, s);
+  if (master) return g32 ? adamw_as<false, true, true>(p, eight, s) : adamw_as<false, false, true>(p, eight, s);
+  return g32 ? adamw_as<false, true, false>(p, eight, s) : adamw_as<false, false, false>(p, eight, s);
+}
+
+hipError_t launch_adamw_values(bool v, int64_t n, const uint8_t* codes, const uint8_t* scales,
+                               void* out, hipStream_t s) {
+  if (n == 0) return hipSuccess;
+  const int64_t want = (n + 2047) / 2048;
+  const int grid = want < 65536 ? (int)want : 65536;
+  if (v)
+    return MOE_LAUNCH("adamw_values", s,
+                      adamw_values_kernel<true><<<grid, 256, 0, s>>>(n, codes, scales, (bf16_t*)out));
+  return MOE_LAUNCH("adamw_values", s,
+                    adamw_values_kernel<false><<<grid, 256, 0, s>>>(n, codes, scales, (bf16_t*)out));
+}
+
+}  // namespace moe

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "../../include/moe.h"
+#include "api_common.hpp"
 #include "internal.hpp"
 #include "skinny.hpp"
 
@@ -92,22 +93,6 @@ SideStream* side_stream() {
   return nullptr;
 }
 
-constexpr size_t ALIGN = 256;
-
-size_t up(size_t v) { return (v + ALIGN - 1) / ALIGN * ALIGN; }
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-// Carves consecutive 256-byte-aligned regions out of one buffer.
-struct Carve {
-  size_t off = 0;
-  size_t take(size_t bytes) {
-    const size_t o = off;
-    off += up(bytes);
-    return o;
-  }
-};
-
 // The bf16 GEMMs address activation rows and one expert's weights with 32-bit
 // byte offsets from a base: every such operand must be smaller than 4 GiB.
 bool bf16_offsets_fit(const moe_shape* s) {
@@ -116,21 +101,6 @@ bool bf16_offsets_fit(const moe_shape* s) {
   const uint64_t lim = 1ull << 32;
   return R * w * 2 < lim && (uint64_t)s->I * s->H * 2 < lim &&
          (uint64_t)s->I_shared * s->H * 2 < lim;
-}
-
-moe_status check_shape(const moe_shape* s, bool need_gemm_dims) {
-  if (!s) return MOE_E_NULL;
-  if (s->T < 0 || s->E < 1 || s->E > MOE_MAX_E || s->k < 1 || s->k > s->E || s->k > MOE_MAX_K)
-    return MOE_E_SHAPE;
-  if ((int64_t)s->T * s->k >= (int64_t)1 << 31) return MOE_E_SHAPE;
-  if (s->H < 128 || s->H % 128) return MOE_E_SHAPE;
-  if (s->flags & ~(MOE_REPLAY | MOE_FUSED_FORWARD)) return MOE_E_SHAPE;
-  if (need_gemm_dims) {
-    if (s->I < 128 || s->I % 128) return MOE_E_SHAPE;
-    if (s->I_shared < 0 || s->I_shared % 128) return MOE_E_SHAPE;
-    if (s->T_minibatch < 0) return MOE_E_SHAPE;
-  }
-  return MOE_OK;
 }
 
 // Minibatches: T_minibatch in (0, T) splits the tokens into ceil(T / T_minibatch)
@@ -172,15 +142,6 @@ moe_plan_layout plan_layout(const moe_shape* s) {
   L.T_minibatch = minibatch_tokens(s);
   L.total_bytes = L.sub_plan_bytes * L.n_minibatch;
   return L;
-}
-
-template <typename P>
-P* at(void* base, size_t off) {
-  return (P*)((char*)base + off);
-}
-template <typename P>
-const P* at(const void* base, size_t off) {
-  return (const P*)((const char*)base + off);
 }
 
 struct PlanView {
@@ -296,31 +257,6 @@ BwdWs bwd_ws(const moe_shape* s, moe_dtype dt) {
   L.dxs = c.take(s->I_shared ? T * s->H * es : 0);
   L.total = c.off;
   return L;
-}
-
-moe_status hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_E_HIP; }
-
-#define MOE_TRY(expr)                         \
-  do {                                        \
-    const hipError_t e_ = (expr);             \
-    if (e_ != hipSuccess) return MOE_E_HIP;   \
-  } while (0)
-
-bool all_aligned(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (p && !aligned16(p)) return false;
-  return true;
-}
-
-bool any_null(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (!p) return true;
-  return false;
-}
-
-// Arrays whose size is a multiple of T may be NULL when T == 0.
-bool any_null_rows(const moe_shape* s, std::initializer_list<const void*> ps) {
-  return s->T > 0 && any_null(ps);
 }
 
 moe_status forward_impl(moe_dtype dt, const moe_shape* s, const void* plan, const void* x,
@@ -926,16 +862,6 @@ moe_status scratch_of_current_device(void** out) {
 // Scored routing takes a wavefront a token, four a workgroup, in one launch: below 2^32
 // threads.  The adapters' launches stay below that up to 2^26 tokens.
 constexpr int MAX_ROUTED = (1 << 26) - 4, MAX_ADAPTED = (1 << 26) - 1;
-
-// Whether an output shares bytes with an input that is still read while it is written (an
-// output over its own base is read and written row by row: the same pointer is fine).
-bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
-  const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
-  return a && b && p < q + nb && q < p + na;
-}
-bool overlap_base(const void* y, const void* base, uint64_t n) {
-  return y != base && overlap(y, n, base, n);
-}
 
 moe_status check_scoring(const moe_shape* s, const moe_scoring* sc) {
   if (!sc) return MOE_E_NULL;

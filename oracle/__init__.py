@@ -31,3 +31,7 @@ from .mx import (  # noqa: F401
 from .operators import (  # noqa: F401
     route_scored, route_scored_backward, router_backward, lora, lora_backward,
 )
+from .step import (  # noqa: F401
+    norm, norm_backward, balance, balance_backward, random_bits, adamw_states, adamw_param,
+    encode_state, decode_state, round_bf16_at_random,
+)
