@@ -653,7 +653,7 @@ size_t moe_balance_workspace_bytes(const moe_shape* shape, const moe_balance* ba
  * The random bits come from the step's seed and the element's place alone: the same call
  * gives the same bits, another step takes another seed.
  *   n_tensors in [1, MOE_ADAMW_MAX_TENSORS]; elements: the sum of the tensors' n;
- *   elements / 8192 + n_tensors < 2^24 (MOE_E_UNSUPPORTED otherwise) */
+ *   elements / 2048 + n_tensors < 2^24 (MOE_E_UNSUPPORTED otherwise) */
 #define MOE_ADAMW_MAX_TENSORS 65536
 typedef struct {
   int64_t elements;

@@ -40,25 +40,21 @@ MOE_DEV uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-MOE_DEV float max_of_four_lanes(float v) {
-  const auto swap = [](float x, int ctrl_is_pair) {
-    const int i = __float_as_int(x);
-    return __int_as_float(ctrl_is_pair ? __builtin_amdgcn_update_dpp(0, i, 0xB1, 0xf, 0xf, true)
-                                       : __builtin_amdgcn_update_dpp(0, i, 0x4E, 0xf, 0xf, true));
-  };
-  v = fmaxf(v, swap(v, 1));
-  return fmaxf(v, swap(v, 0));
+MOE_DEV uint32_t max_of_four_lanes(uint32_t v) {
+  const uint32_t a = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true);
+  v = v > a ? v : a;
+  const uint32_t b = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true);
+  return v > b ? v : b;
 }
 
-// The scale byte of a block whose largest magnitude is `top`: the smallest 2^(e - 127) with
-// top <= largest code * scale; CARRY is what carries into the exponent past that code's
-// mantissa, SHIFT its exponent.  255 (NaN) where the state is not finite or past 2^126.
+// The scale byte of a block whose largest magnitude has the bits `top` (as whole numbers
+// they order magnitudes, with inf and NaN above): the smallest 2^(e - 127) with top <= the
+// largest code * scale; CARRY is what carries into the exponent past that code's mantissa,
+// SHIFT its exponent.  255 (NaN) where the state is not finite or from 2^126 on.
 template <uint32_t CARRY, int SHIFT>
-MOE_DEV uint32_t scale_byte(float top) {
-  const uint32_t u = __float_as_uint(top);
-  if (!(top < 8.5070592e37f)) return 255u;
-  const int e = (int)((u + CARRY) >> 23) - SHIFT;
-  return e < 1 ? 1u : (uint32_t)e;
+MOE_DEV uint32_t scale_byte(uint32_t top) {
+  const int e = (int)((top + CARRY) >> 23) - SHIFT;
+  return top >= 0x7E800000u ? 255u : e < 1 ? 1u : (uint32_t)e;
 }
 // 2^(127 - e), e in [1, 253]
 MOE_DEV float inverse_scale(uint32_t e) { return __uint_as_float((254u - e) << 23); }
@@ -68,19 +64,24 @@ MOE_DEV float scale_of(uint32_t e) { return __uint_as_float(e << 23); }
 constexpr uint32_t M_CARRY = 0x1FFFFFu, V_CARRY = 0x0FFFFFu;  // past 1.75 (448), past 1.875
 constexpr int M_SHIFT = 8, V_SHIFT = 0;
 
-MOE_DEV uint32_t encode_m(float m, float inv, uint32_t r16) {
-  const float y = fabsf(m) * inv;
-  const bool low = y < 0x1p-6f;  // below the normal codes the distance stays 2^-9
-  const float z = low ? y + 0x1p-6f : y;
-  const uint32_t c = ((__float_as_uint(z) + (r16 << 4 | 8u)) >> 20) - (low ? 968u : 960u);
-  return c | (__float_as_uint(m) >> 31 << 7);
+// Codes from 16 random bits r16, which stand for the middle of their interval: the upper
+// neighbour where (distance from the lower one in steps) + (r16 + 1/2) / 2^16 >= 1.  The
+// conversion instruction does just that with its upper 20 random bits.
+template <int BYTE>
+MOE_DEV uint32_t encode_m(float m, float inv, uint32_t r, uint32_t word) {
+  return (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(m * inv, (int)(r << 16 | 0x8000u), (int)word, BYTE);
 }
-MOE_DEV uint32_t encode_v(float v, float inv, uint32_t r16) {
-  const uint32_t c = (__float_as_uint(v * inv) + (r16 << 4 | 8u)) >> 20;
-  return v > 0.0f ? (c > 769u ? c : 769u) - 768u : 0u;
+// v's code, plus 768: bits 20 and up of an fp32 of exponent -31 .. 0 are 768 + code
+MOE_DEV uint32_t encode_v(float v, float inv, uint32_t r) {
+  const uint32_t c = (__float_as_uint(v * inv) + ((r >> 12 & 0xffff0u) | 8u)) >> 20;
+  const uint32_t least = v > 0.0f ? 769u : 768u;
+  return c > least ? c : least;
 }
-MOE_DEV float decode_v(uint32_t c) { return c ? __uint_as_float((c + 768u) << 20) : 0.0f; }
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
+MOE_DEV uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0c0c0400u), hi = __builtin_amdgcn_perm(d, c, 0x04000c0cu);
+  return lo | hi;
+}
+MOE_DEV float decode_v(uint32_t c) { return c ? __uint_as_float(c << 20 | 0x30000000u) : 0.0f; }
 // four E4M3 codes of one word
 MOE_DEV void decode_m4(uint32_t w, float* f) {
   const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
@@ -92,6 +93,20 @@ MOE_DEV float round_bf16_at_random(float p, uint32_t r) {
   const uint32_t u = __float_as_uint(p);
   if ((u & 0x7f800000u) == 0x7f800000u) return p;  // inf and NaN as they are
   return __uint_as_float((u + (r & 0xffffu)) & 0xffff0000u);
+}
+// eight values on bf16's grid
+MOE_DEV void store_bf16_exact(void* p, int64_t i, int cnt, const float* f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w[j] = __builtin_amdgcn_perm(__float_as_uint(f[2 * j + 1]), __float_as_uint(f[2 * j]), 0x07060302u);
+  if (cnt == 8) {
+    *(uint4*)((bf16_t*)p + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < cnt) ((bf16_t*)p)[i + j] = (bf16_t)(w[j >> 1] >> (16 * (j & 1)));
 }
 
 MOE_DEV void update_state(float& m, float& v, float& g, const AdamwHyper& h) {
@@ -126,7 +141,7 @@ MOE_DEV void store8(void* p, int64_t i, int cnt, const float* f) {
       *(float4*)((float*)p + i) = make_float4(f[0], f[1], f[2], f[3]);
       *(float4*)((float*)p + i + 4) = make_float4(f[4], f[5], f[6], f[7]);
     } else {
-      *(uint4*)((bf16_t*)p + i) = pack8(f);
+      *(uint4*)((bf16_t*)p + i) = cvt8(f);
     }
     return;
   }
@@ -158,10 +173,11 @@ MOE_DEV void store_codes(void* p, int64_t i, int cnt, uint2 v) {
     if (j < cnt) ((uint8_t*)p)[i + j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
 }
 
-// The tensor of a tile: the last entry of first[0 .. n) that is <= tile and whose tensor has
-// tiles (first ascends; a tensor without elements has none).  64 entries a step.
+// The tensor of a tile: the last i in [0, n) with first[i] <= tile (first ascends; a tensor
+// without elements has no tiles, and the last of equal entries is the one that has).  64
+// entries a step.
 MOE_DEV int tensor_of(const int32_t* first, int n, int tile) {
-  int lo = 0, hi = n;  // first[lo] <= tile < first[hi]
+  int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int step = (hi - lo - 1 + 63) / 64;
     const int i = lo + ((int)(threadIdx.x & 63) + 1) * step;
@@ -176,17 +192,15 @@ MOE_DEV int tensor_of(const int32_t* first, int n, int tile) {
 template <bool P32, bool G32, bool MASTER, bool EIGHT>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
   const int tile = blockIdx.x;
-  if (tile >= a.first[a.n_tensors]) return;
   const int id = tensor_of(a.first, a.n_tensors, tile);
   const AdamwDesc d = a.desc[id];
   const AdamwHyper h = a.hyper_dev ? *a.hyper_dev : a.hyper;
   const int64_t tile0 = (int64_t)(tile - a.first[id]) * ADAMW_TILE;
-  // (a tile starts at a multiple of 2^13, so the high word of the place is the tile's)
+  if (tile0 >= d.n) return;  // the grid is an upper bound
+  // (a tile starts at a multiple of 2^11, so the high word of the place is the tile's)
   const uint32_t key = mix32(mix32((uint32_t)id + 1u) + h.seed) + (uint32_t)(tile0 >> 32) * 0x3C6EF373u;
-#pragma unroll 1
-  for (int it = 0; it < ADAMW_TILE / 2048; ++it) {
-    const int64_t i = tile0 + it * 2048 + (int)threadIdx.x * 8;
-    if (tile0 + it * 2048 >= d.n) break;
+  {
+    const int64_t i = tile0 + (int)threadIdx.x * 8;
     const int64_t left = d.n - i;
     const int cnt = left >= 8 ? 8 : left > 0 ? (int)left : 0;
     float g[8], p[8], m[8], v[8];
@@ -221,27 +235,31 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) p[j] = round_bf16_at_random(p[j], r[j] ^ (r[j] >> 16));
     }
-    store8<P32>(d.param_out, i, cnt, p);
+    if (!P32 && !MASTER) store_bf16_exact(d.param_out, i, cnt, p);
+    else store8<P32>(d.param_out, i, cnt, p);
     if (EIGHT) {
-      float mt = 0.0f, vt = 0.0f;
-      bool finite = true;
+      uint32_t mt = 0, vt = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        mt = fmaxf(mt, fabsf(m[j]));
-        vt = fmaxf(vt, v[j]);
-        finite = finite && m[j] - m[j] == 0.0f && v[j] - v[j] == 0.0f;
+        const uint32_t mu = __float_as_uint(m[j]) & 0x7fffffffu, vu = __float_as_uint(v[j]);
+        mt = mt > mu ? mt : mu;
+        vt = vt > vu ? vt : vu;
       }
-      if (!finite) mt = vt = __builtin_inff();
       mt = max_of_four_lanes(mt);
       vt = max_of_four_lanes(vt);
       const uint32_t me = scale_byte<M_CARRY, M_SHIFT>(mt), ve = scale_byte<V_CARRY, V_SHIFT>(vt);
       const float mi = inverse_scale(me), vi = inverse_scale(ve);
-      uint32_t mw[2] = {0, 0}, vw[2] = {0, 0};
+      uint32_t mw[2] = {0, 0}, c[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        mw[j >> 2] |= encode_m(m[j], mi, r[j] & 0xffffu) << (8 * (j & 3));
-        vw[j >> 2] |= encode_v(v[j], vi, r[j] >> 16) << (8 * (j & 3));
+      for (int w = 0; w < 2; ++w) {
+        mw[w] = encode_m<0>(m[4 * w], mi, r[4 * w], mw[w]);
+        mw[w] = encode_m<1>(m[4 * w + 1], mi, r[4 * w + 1], mw[w]);
+        mw[w] = encode_m<2>(m[4 * w + 2], mi, r[4 * w + 2], mw[w]);
+        mw[w] = encode_m<3>(m[4 * w + 3], mi, r[4 * w + 3], mw[w]);
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = encode_v(v[j], vi, r[j]);
+      const uint32_t vw[2] = {low_bytes(c[0], c[1], c[2], c[3]), low_bytes(c[4], c[5], c[6], c[7])};
       // a block that is not finite: codes of zero under a scale of inf, which is NaN
       store_codes(d.m_out, i, cnt, me == 255u ? make_uint2(0, 0) : make_uint2(mw[0], mw[1]));
       store_codes(d.v_out, i, cnt, ve == 255u ? make_uint2(0, 0) : make_uint2(vw[0], vw[1]));

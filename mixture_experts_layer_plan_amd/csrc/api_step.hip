@@ -106,7 +106,7 @@ BalanceWs balance_ws(const moe_shape* s, const moe_balance* b) {
   L.seg_p = c.take(segs * s->E * sizeof(float));
   L.seg_c = c.take(segs * s->E * sizeof(int32_t));
   L.seg_n = c.take(segs * sizeof(int32_t));
-  L.part = c.take((size_t)b->n_seq * ((s->E + 63) / 64) * sizeof(float));
+  L.part = c.take((size_t)b->n_seq * balance_blocks(s->E) * sizeof(float));
   L.tokens = c.take((size_t)b->n_seq * sizeof(int32_t));
   L.ticket = c.take(sizeof(int32_t));
   L.total = c.off;

@@ -8,9 +8,9 @@
 //   s_i = coef E / (k N_i^2 n)
 // An expert whose logit is -inf or NaN has p = 0 and no gradient.
 //
-// One wavefront per token, lane l holding the experts l, l + 64, ...  Workgroups sum the
-// tokens of one chunk, segment by segment; a second launch adds a sequence's segments in
-// their order, its last workgroup joining the sequences.
+// A wavefront takes a token's row, U tokens at a time.  Workgroups sum the tokens of one
+// chunk, segment by segment; a second launch adds a sequence's segments in their order, its
+// last workgroup joining the sequences.  A small batch takes one launch of one workgroup.
 #include <math.h>
 
 #include "common.hpp"
@@ -22,133 +22,304 @@ namespace moe {
 namespace {
 
 // The last i in [0, n] with start[i] <= t (entries ascend), n for a token behind the last
-// sequence, -1 for one before the first.  64 entries a step; every lane gets the result,
-// which lies in [-1, n] whatever the entries hold.
-MOE_DEV int sequence_of(const int32_t* start, int n, int t) {
-  if (!start) return t < 0 ? -1 : 0;
+// sequence, -1 for one before the first; next: start[i + 1] (for i < n).  64 entries a step;
+// every lane gets the result, which lies in [-1, n] whatever the entries hold.
+MOE_DEV int sequence_of(const int32_t* start, int n, int t, int* next) {
   int lo = -1, hi = n + 1;  // start[lo] <= t < start[hi], with -inf and inf at the ends
   while (hi - lo > 1) {
     const int step = (hi - lo - 1 + 63) / 64;
     const int i = lo + (lane_id() + 1) * step;
-    const bool le = i < hi && start[i] <= t;
-    const int ones = __popcll(ballot64(le));
-    const int nlo = lo + ones * step;
+    const int v = start[i < hi ? i : hi - 1];
+    const int ones = __popcll(ballot64(i < hi && v <= t));
     const int nhi = lo + (ones + 1) * step;
+    // the first entry above t, if this step read it
+    *next = __builtin_amdgcn_readlane(v, ones < 63 ? ones : 63);
+    if (ones > 63 || nhi >= hi) *next = hi <= n ? start[hi] : 0;
     hi = nhi < hi ? nhi : hi;
-    lo = nlo;
+    lo += ones * step;
   }
   return lo;
 }
 
-// Scores of one token: p (normalised) and, for sigmoid, q = 1 - sigmoid.  An expert out of
-// play has p = 0.  The largest exponent is 0, so that neither overflows or all vanish.
-template <int NPL, bool SIGMOID>
-MOE_DEV void scores(const float* l, float* p, float* q) {
+// How a row of E experts lies in the lanes of a wavefront: N values a lane, four
+// neighbours a load (E a multiple of 4) or one; U rows at a time.
+template <int N_, int U_, bool FOUR_>
+struct Row {
+  static constexpr int N = N_, U = U_;
+  static constexpr bool FOUR = FOUR_;
+  MOE_DEV static int expert(int j) {
+    return FOUR ? ((j >> 2) * 64 + lane_id()) * 4 + (j & 3) : j * 64 + lane_id();
+  }
+  template <typename T>
+  MOE_DEV static void load(const T* row, int E, T none, T* v) {
+#pragma unroll
+    for (int j = 0; j < N; j += FOUR ? 4 : 1) {
+      const int e = expert(j);
+      if constexpr (FOUR) {
+        typedef T T4 __attribute__((ext_vector_type(4)));
+        T4 x = {none, none, none, none};
+        if (e < E) x = *(const T4*)(row + e);
+        v[j] = x.x; v[j + 1] = x.y; v[j + 2] = x.z; v[j + 3] = x.w;
+      } else {
+        v[j] = e < E ? row[e] : none;
+      }
+    }
+  }
+  MOE_DEV static void store(float* row, int E, const float* v) {
+#pragma unroll
+    for (int j = 0; j < N; j += FOUR ? 4 : 1) {
+      const int e = expert(j);
+      if (e < E) {
+        if constexpr (FOUR) *(float4*)(row + e) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        else row[e] = v[j];
+      }
+    }
+  }
+};
+
+// e^x for |x| <= 200 or so: 2^(x log2 e) with the product's rounding carried along.
+MOE_DEV float exp_near(float x) {
+  const float h = x * 1.44269502f;
+  const float lo = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269502f, -h));
+  const float e = __builtin_amdgcn_exp2f(h);
+  return fmaf(e, lo * 0.693147181f, e);
+}
+
+// Shares of one token whose logits are far from zero: exponents relative to the largest, so
+// that they neither overflow nor all vanish.
+template <int N, bool SIGMOID>
+MOE_DEV void shares_far(const float (&l)[N], float (&p)[N]) {
   float top = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < NPL; ++j) top = fmaxf(top, l[j]);  // fmaxf leaves NaN out
+  for (int j = 0; j < N; ++j) top = fmaxf(top, l[j]);  // fmaxf leaves NaN out
   top = wave_max_f32(top);
   if (SIGMOID) top = fminf(top, 0.0f);
   float sum = 0.0f;
 #pragma unroll
-  for (int j = 0; j < NPL; ++j) {
-    const bool in = l[j] > -INFINITY;
+  for (int j = 0; j < N; ++j) {
+    float z = exp_near(fmaxf(l[j] - top, -200.0f));
     if (SIGMOID) {
-      // e^(l - top) / (1 + e^l) where l <= 0, else 1 / (1 + e^-l) e^-top with top = 0
-      const float e = expf(-fabsf(l[j]));
-      const float r = 1.0f / (1.0f + e);
-      p[j] = in ? (l[j] > 0.0f ? r : expf(l[j] - top) * r) : 0.0f;
-      q[j] = l[j] > 0.0f ? e * r : r;
-    } else {
-      p[j] = in ? expf(l[j] - top) : 0.0f;
+      // e^(l - top) / (1 + e^l) where l <= 0, else 1 / (1 + e^-l) with top = 0
+      const float r = __builtin_amdgcn_rcpf(1.0f + exp_near(fmaxf(-fabsf(l[j]), -200.0f)));
+      z = l[j] > 0.0f ? r : z * r;
     }
+    p[j] = l[j] > -INFINITY ? z : 0.0f;
     sum += p[j];
   }
   sum = dpp_sum_f32(sum);
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const float inv = sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
 #pragma unroll
-  for (int j = 0; j < NPL; ++j) p[j] *= inv;
+  for (int j = 0; j < N; ++j) p[j] *= inv;
 }
 
-template <int NPL>
-MOE_DEV void load_row(const float* row, int E, float* l) {
+// Shares p of U tokens and, for sigmoid scores, q = 1 - sigmoid.  An expert out of play has
+// p = 0.  Scores as they are, without the search for the largest, serve wherever their sum
+// is far from the ends of fp32: the others are done again by shares_far.
+template <typename R, bool SIGMOID>
+MOE_DEV void shares(const float (&l)[R::U][R::N], float (&p)[R::U][R::N], float (&q)[R::U][R::N]) {
+  float sum[R::U];
 #pragma unroll
-  for (int j = 0; j < NPL; ++j) {
-    const int e = j * 64 + lane_id();
-    l[j] = e < E ? row[e] : -INFINITY;
+  for (int u = 0; u < R::U; ++u) {
+    sum[u] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < R::N; ++j) {
+      const float v = l[u][j];
+      float z;
+      if (SIGMOID) {
+        const float e = exp_near(fmaxf(-fabsf(v), -200.0f));
+        const float r = __builtin_amdgcn_rcpf(1.0f + e), s = e * r;
+        z = v > 0.0f ? r : s;
+        q[u][j] = v > 0.0f ? s : r;
+      } else {
+        z = exp_near(fmaxf(v, -200.0f));
+      }
+      p[u][j] = v > -INFINITY ? z : 0.0f;
+      sum[u] += p[u][j];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < R::U; ++u) sum[u] = dpp_sum_f32(sum[u]);
+#pragma unroll
+  for (int u = 0; u < R::U; ++u) {
+    if (sum[u] > 0x1p-60f && sum[u] < 0x1p100f) {
+      const float inv = __builtin_amdgcn_rcpf(sum[u]);
+#pragma unroll
+      for (int j = 0; j < R::N; ++j) p[u][j] *= inv;
+    } else {
+      shares_far<R::N, SIGMOID>(l[u], p[u]);
+    }
   }
 }
 
-template <int NPL, bool SIGMOID>
-__global__ __launch_bounds__(256) void balance_part_kernel(BalanceArgs a, int chunk) {
-  extern __shared__ float s_mem[];
-  float* s_p = s_mem;                       // [4][E]
-  int32_t* s_c = (int32_t*)(s_mem + 4 * a.E);  // [E]
-  __shared__ int s_n[4];
+// Walks the tokens [t0, t1) of a workgroup of W wavefronts sequence by sequence, and calls
+// done(seq, n) for each, with its sums in LDS (s_p: one row of E per wavefront, s_c) and n,
+// the number of its tokens that count, in every thread.
+template <typename R, bool SIGMOID, int W, typename Done>
+MOE_DEV void walk(const BalanceArgs& a, int t0, int t1, float* s_p, int32_t* s_c, int* s_n, Done done) {
   const int wave = threadIdx.x >> 6, lane = lane_id();
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.ticket[0] = 0;  // for the launch that follows
-  const int t0 = blockIdx.x * chunk;
-  const int t1 = t0 + chunk < a.T ? t0 + chunk : a.T;
   int t = t0;
   while (t < t1) {
-    // the tokens [t, end) of the chunk that are in t's sequence
-    const int seq = sequence_of(a.start, a.n_seq, t);
-    if (seq >= a.n_seq) break;  // behind the last one
-    int end = t1;
+    // the first tokens' rows are on their way while their sequence is looked up
+    float l[R::U][R::N];
+    int id[R::U];
+    const auto load = [&](int u0) {
+#pragma unroll
+      for (int u = 0; u < R::U; ++u) {
+        const int v = u0 + u < t1 ? u0 + u : t1 - 1;
+        id[u] = lane < a.k ? a.idx[(size_t)v * a.k + lane] : -1;
+        R::load(a.logits + (size_t)v * a.E, a.E, -INFINITY, l[u]);
+      }
+    };
+    load(t + wave * R::U);
+    // the tokens [t, end) that are in t's sequence
+    int seq = 0, end = t1;
     if (a.start) {
-      const int next = a.start[seq + 1];
+      int next;
+      seq = sequence_of(a.start, a.n_seq, t, &next);
+      if (seq >= a.n_seq) break;  // behind the last one
       end = next < t1 ? next : t1;
       if (end <= t) end = t1;  // entries that do not ascend: no endless loop
+      if (seq < 0) {           // before the first sequence
+        t = end;
+        continue;
+      }
     }
-    if (seq < 0) {  // before the first sequence
-      t = end;
-      continue;
-    }
-    for (int e = threadIdx.x; e < a.E; e += 256) s_c[e] = 0;
+    for (int e = threadIdx.x; e < a.E; e += 64 * W) s_c[e] = 0;
     __syncthreads();
-    float acc[NPL];
+    float acc[R::N];
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) acc[j] = 0.0f;
+    for (int j = 0; j < R::N; ++j) acc[j] = 0.0f;
     int used = 0;
-    for (int u = t + wave; u < end; u += 4) {
-      const int id = lane < a.k ? a.idx[(size_t)u * a.k + lane] : -1;
-      const bool ok = (unsigned)id < (unsigned)a.E;
-      float l[NPL], p[NPL], q[NPL];
-      load_row<NPL>(a.logits + (size_t)u * a.E, a.E, l);
-      if (ok) atomicAdd(&s_c[id], 1);
-      if (!ballot64(ok)) continue;
-      ++used;
-      scores<NPL, SIGMOID>(l, p, q);
+    for (int u0 = t + wave * R::U; u0 < end; u0 += W * R::U) {
+      float p[R::U][R::N], q[R::U][R::N];
+      if (u0 > t + wave * R::U) load(u0);
+      shares<R, SIGMOID>(l, p, q);
 #pragma unroll
-      for (int j = 0; j < NPL; ++j) acc[j] += p[j];
-    }
+      for (int u = 0; u < R::U; ++u) {
+        const bool ok = u0 + u < end && (unsigned)id[u] < (unsigned)a.E;
+        if (ok) atomicAdd(&s_c[id[u]], 1);  // whole numbers: any order gives the same
+        if (ballot64(ok)) {
+          ++used;
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) {
-      const int e = j * 64 + lane;
-      if (e < a.E) s_p[wave * a.E + e] = acc[j];
+          for (int j = 0; j < R::N; ++j) acc[j] += p[u][j];
+        }
+      }
     }
+    R::store(s_p + wave * a.E, a.E, acc);
     if (lane == 0) s_n[wave] = used;
     __syncthreads();
-    const size_t seg = (size_t)blockIdx.x + seq;
-    for (int e = threadIdx.x; e < a.E; e += 256) {
-      a.seg_p[seg * a.E + e] = (s_p[e] + s_p[a.E + e]) + (s_p[2 * a.E + e] + s_p[3 * a.E + e]);
-      a.seg_c[seg * a.E + e] = s_c[e];
-    }
-    if (threadIdx.x == 0) a.seg_n[seg] = s_n[0] + s_n[1] + s_n[2] + s_n[3];
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) n += s_n[w];
+    done(seq, n);
     __syncthreads();
     t = end;
   }
 }
 
-// Adds the segments of sequence blockIdx.x / blocks for 64 experts: 16 wavefronts take
-// every 16th chunk each.  The last workgroup to finish joins the sequences.
-__global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, int chunk, int blocks) {
-  __shared__ float s_p[16][64];
-  __shared__ int s_c[16][64], s_n[16];
-  __shared__ int s_last;
+template <int W>
+MOE_DEV float rows_sum(const float* s_p, int E, int e) {
+  float v = s_p[e];
+#pragma unroll
+  for (int w = 1; w < W; ++w) v += s_p[w * E + e];
+  return v;
+}
+
+constexpr int PART_W = 8;  // wavefronts of a chunk's workgroup
+template <typename R, bool SIGMOID>
+__global__ __launch_bounds__(64 * PART_W) void balance_part_kernel(BalanceArgs a, int chunk) {
+  extern __shared__ float s_mem[];
+  float* s_p = s_mem;                               // [PART_W][E]
+  int32_t* s_c = (int32_t*)(s_mem + PART_W * a.E);  // [E]
+  __shared__ int s_n[PART_W];
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.ticket[0] = 0;  // for the launch that follows
+  const int t0 = blockIdx.x * chunk;
+  const int t1 = t0 + chunk < a.T ? t0 + chunk : a.T;
+  walk<R, SIGMOID, PART_W>(a, t0, t1, s_p, s_c, s_n, [&](int seq, int n) {
+    const size_t seg = (size_t)blockIdx.x + seq;
+    for (int e = threadIdx.x; e < a.E; e += 64 * PART_W) {
+      a.seg_p[seg * a.E + e] = rows_sum<PART_W>(s_p, a.E, e);
+      a.seg_c[seg * a.E + e] = s_c[e];
+    }
+    if (threadIdx.x == 0) a.seg_n[seg] = n;
+  });
+}
+
+MOE_DEV double wave_sum_f64(double v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// The loss and the scales from the sequences' tokens and sums of counts * p over `blocks`
+// groups of experts, in 64 bits, by one wavefront; a lane takes every 64th sequence.
+MOE_DEV void finish(const BalanceArgs& a, const int32_t* tokens, const float* part, int blocks) {
+  double loss = 0.0, have = 0.0;
+  const double per = (double)a.coef * a.E / a.k;
+  for (int i = lane_id(); i < a.n_seq; i += 64) {
+    const int N = tokens[i];
+    double x = 0.0;
+#pragma unroll 4
+    for (int k = 0; k < blocks; ++k) x += (double)part[(size_t)i * blocks + k];
+    if (N > 0) {
+      have += 1.0;
+      loss += per / ((double)N * N) * x;
+    }
+  }
+  loss = wave_sum_f64(loss);
+  have = wave_sum_f64(have);
+  const double each = have > 0.0 ? 1.0 / have : 0.0;
+  if (lane_id() == 0) a.loss[0] = (float)(loss * each);
+  for (int i = lane_id(); i < a.n_seq; i += 64) {
+    const int N = tokens[i];
+    a.scales[i] = N > 0 ? (float)(per * each / ((double)N * N)) : 0.0f;
+  }
+}
+
+// A batch of few tokens, whole, in one workgroup of 16 wavefronts.
+constexpr int SMALL_T = 256, SMALL_E = 256, SMALL_SEQ = 64;
+template <typename R, bool SIGMOID>
+__global__ __launch_bounds__(1024) void balance_small_kernel(BalanceArgs a) {
+  __shared__ float s_p[16 * SMALL_E];
+  __shared__ int32_t s_c[SMALL_E];
+  __shared__ int s_n[16];
+  __shared__ float s_part[SMALL_SEQ], s_x[4];
+  __shared__ int32_t s_tokens[SMALL_SEQ];
+  if (threadIdx.x < SMALL_SEQ) s_tokens[threadIdx.x] = -1;
+  __syncthreads();
+  walk<R, SIGMOID, 16>(a, 0, a.T, s_p, s_c, s_n, [&](int seq, int n) {
+    const int e = threadIdx.x;
+    float x = 0.0f;
+    if (e < a.E) {
+      x = rows_sum<16>(s_p, a.E, e) * (float)s_c[e];
+      a.counts[(size_t)seq * a.E + e] = s_c[e];
+    }
+    x = dpp_sum_f32(x);
+    if (e < SMALL_E && lane_id() == 0) s_x[e >> 6] = x;
+    __syncthreads();
+    if (e == 0) {
+      s_part[seq] = (s_x[0] + s_x[1]) + (s_x[2] + s_x[3]);
+      s_tokens[seq] = n;
+    }
+  });
+  __syncthreads();
+  for (int i = 0; i < a.n_seq; ++i)  // sequences that the walk met no token of
+    if (s_tokens[i] < 0 && (int)threadIdx.x < a.E) a.counts[(size_t)i * a.E + threadIdx.x] = 0;
+  if (threadIdx.x < 64) finish(a, s_tokens, s_part, 1);
+}
+
+// Adds the segments of sequence blockIdx.x / blocks for JOIN_E experts: lane l the experts
+// l, l + 1, ... of 16, W * 4 rows of lanes every (W * 4)th chunk each.  The last workgroup to
+// finish joins the sequences (TICKET; else balance_finish_kernel does).
+constexpr int JOIN_E = 16;
+template <int W, bool TICKET>
+__global__ __launch_bounds__(64 * W) void balance_join_kernel(BalanceArgs a, int chunk, int blocks) {
+  constexpr int G = 4 * W;
+  __shared__ float s_p[G][JOIN_E];
+  __shared__ int s_c[G][JOIN_E], s_n[G];
   const int seq = blockIdx.x / blocks, blk = blockIdx.x - seq * blocks;
-  const int wave = threadIdx.x >> 6, lane = lane_id();
-  const int e = blk * 64 + lane;
+  const int lane = threadIdx.x & (JOIN_E - 1), g = threadIdx.x / JOIN_E;
+  const int e = blk * JOIN_E + lane;
   int b = a.start ? a.start[seq] : 0, end = a.start ? a.start[seq + 1] : a.T;
   b = b > 0 ? b : 0;
   end = end < a.T ? end : a.T;
@@ -156,165 +327,190 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a, int c
   int c = 0, n = 0;
   if (b < end) {
     const int c1 = (end - 1) / chunk;
-    for (int i = b / chunk + wave; i <= c1; i += 16) {
-      const size_t seg = (size_t)i + seq;
-      if (e < a.E) {
-        p += a.seg_p[seg * a.E + e];
-        c += a.seg_c[seg * a.E + e];
+    const int col = e < a.E ? e : a.E - 1;  // (lanes past the last expert are left out below)
+    for (int i0 = b / chunk + g; i0 <= c1; i0 += 8 * G) {
+      float pv[8];
+      int cv[8], nv[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {  // all on their way before the first is added
+        const int i = i0 + k * G <= c1 ? i0 + k * G : i0;
+        const size_t seg = (size_t)i + seq;
+        pv[k] = a.seg_p[seg * a.E + col];
+        cv[k] = a.seg_c[seg * a.E + col];
+        nv[k] = a.seg_n[seg];
       }
-      n += a.seg_n[seg];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (i0 + k * G <= c1) {
+          p += pv[k];
+          c += cv[k];
+          n += nv[k];
+        }
+      }
     }
   }
-  s_p[wave][lane] = p;
-  s_c[wave][lane] = c;
-  if (lane == 0) s_n[wave] = n;
+  s_p[g][lane] = p;
+  s_c[g][lane] = c;
+  if (lane == 0) s_n[g] = n;
   __syncthreads();
-  if (wave == 0) {
-    for (int w = 1; w < 16; ++w) {
-      p += s_p[w][lane];
-      c += s_c[w][lane];
-      n += s_n[w];
+  if (threadIdx.x < 64) {
+    // a quarter of the rows in each 16 lanes, then the quarters
+    const int q = threadIdx.x / JOIN_E;
+    p = s_p[q][lane];
+    c = s_c[q][lane];
+    n = s_n[q];
+#pragma unroll
+    for (int k = 4; k < G; k += 4) {
+      p += s_p[k + q][lane];
+      c += s_c[k + q][lane];
+      n += s_n[k + q];
     }
-    if (e < a.E) a.counts[(size_t)seq * a.E + e] = c;
-    const float x = dpp_sum_f32(e < a.E ? p * (float)c : 0.0f);
-    if (lane == 0) {
+#pragma unroll
+    for (int o = 16; o <= 32; o <<= 1) {
+      p += __shfl_xor(p, o, 64);
+      c += __shfl_xor(c, o, 64);
+      n += __shfl_xor(n, o, 64);
+    }
+    const bool own = e < a.E && q == 0;
+    if (own) a.counts[(size_t)seq * a.E + e] = c;
+    const float x = dpp_sum_f32(own ? p * (float)c : 0.0f);
+    if (threadIdx.x == 0) {
       a.part[(size_t)seq * blocks + blk] = x;
       if (blk == 0) a.tokens[seq] = n;
+    }
+    if constexpr (TICKET) {
+      int last = 0;
+      if (threadIdx.x == 0) {
+        __threadfence();
+        last = atomicAdd(a.ticket, 1) == (int)gridDim.x - 1;
+      }
+      if (!__builtin_amdgcn_readfirstlane(last)) return;
       __threadfence();
-      s_last = atomicAdd(a.ticket, 1) == (int)gridDim.x - 1;
+      finish(a, a.tokens, a.part, blocks);
     }
-  }
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  // n and the loss, in 64 bits; a thread takes every 1024th sequence
-  __shared__ double s_loss[16];
-  __shared__ int s_seq[16];
-  int have = 0;
-  double loss = 0.0;
-  const double per = (double)a.coef * a.E / a.k;
-  for (int i = threadIdx.x; i < a.n_seq; i += 1024) {
-    const int N = a.tokens[i];
-    if (N > 0) {
-      ++have;
-      double x = 0.0;
-      for (int k = 0; k < blocks; ++k) x += (double)a.part[(size_t)i * blocks + k];
-      loss += per / ((double)N * N) * x;
-    }
-  }
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
-    loss += __shfl_xor(loss, o, 64);
-    have += __shfl_xor(have, o, 64);
-  }
-  if (lane == 0) {
-    s_loss[wave] = loss;
-    s_seq[wave] = have;
-  }
-  __syncthreads();
-  loss = 0.0;
-  have = 0;
-  for (int w = 0; w < 16; ++w) {
-    loss += s_loss[w];
-    have += s_seq[w];
-  }
-  const double each = have ? 1.0 / have : 0.0;
-  if (threadIdx.x == 0) a.loss[0] = (float)(loss * each);
-  for (int i = threadIdx.x; i < a.n_seq; i += 1024) {
-    const int N = a.tokens[i];
-    a.scales[i] = N > 0 ? (float)(per * each / ((double)N * N)) : 0.0f;
   }
 }
 
-template <int NPL, bool SIGMOID>
+__global__ __launch_bounds__(64) void balance_finish_kernel(BalanceArgs a, int blocks) {
+  finish(a, a.tokens, a.part, blocks);
+}
+
+template <typename R, bool SIGMOID>
 __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs a) {
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= a.T) return;
+  const int t0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * R::U;
+  if (t0 >= a.T) return;
   const int lane = lane_id();
-  const int seq = sequence_of(a.start, a.n_seq, t);
-  const int id = lane < a.k ? a.idx[(size_t)t * a.k + lane] : -1;
-  const bool used = ballot64((unsigned)id < (unsigned)a.E) && seq >= 0 && seq < a.n_seq;
-  float d[NPL];
+  float l[R::U][R::N], d[R::U][R::N], p[R::U][R::N], q[R::U][R::N];
+  int id[R::U];
 #pragma unroll
-  for (int j = 0; j < NPL; ++j) {
-    const int e = j * 64 + lane;
-    d[j] = a.d_in && e < a.E ? a.d_in[(size_t)t * a.E + e] : 0.0f;
+  for (int u = 0; u < R::U; ++u) {
+    const int t = t0 + u < a.T ? t0 + u : t0;
+    id[u] = lane < a.k ? a.idx[(size_t)t * a.k + lane] : -1;
+    R::load(a.logits + (size_t)t * a.E, a.E, -INFINITY, l[u]);
+#pragma unroll
+    for (int j = 0; j < R::N; ++j) d[u][j] = 0.0f;
+    if (a.d_in) R::load(a.d_in + (size_t)t * a.E, a.E, 0.0f, d[u]);
   }
-  if (used) {
-    float l[NPL], p[NPL], q[NPL], c[NPL];
-    load_row<NPL>(a.logits + (size_t)t * a.E, a.E, l);
-    float dot = 0.0f;
-    scores<NPL, SIGMOID>(l, p, q);
+  const float up = a.d_loss ? a.d_loss[0] : 1.0f;
+  int seq = -2, end = 0, have = -2;
+  int c[R::N];
+  float scale = 0.0f;
+  shares<R, SIGMOID>(l, p, q);
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) {
-      const int e = j * 64 + lane;
-      c[j] = e < a.E ? (float)a.counts[(size_t)seq * a.E + e] : 0.0f;
-      dot = fmaf(p[j], c[j], dot);
+  for (int u = 0; u < R::U; ++u) {
+    const int t = t0 + u;
+    if (t >= a.T) break;
+    if (u == 0 || t >= end) {
+      seq = 0;
+      end = a.T;
+      if (a.start) seq = sequence_of(a.start, a.n_seq, t, &end);
+      if (seq >= a.n_seq) end = a.T;
     }
-    dot = dpp_sum_f32(dot);
-    const float scale = a.scales[seq] * (a.d_loss ? a.d_loss[0] : 1.0f);
+    if (ballot64((unsigned)id[u] < (unsigned)a.E) && seq >= 0 && seq < a.n_seq) {
+      if (have != seq) {
+        R::load(a.counts + (size_t)seq * a.E, a.E, 0, c);
+        scale = a.scales[seq] * up;
+        have = seq;
+      }
+      float dot = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) {
-      const float g = p[j] * (c[j] - dot) * (SIGMOID ? q[j] : 1.0f);
-      d[j] = l[j] > -INFINITY ? fmaf(scale, g, d[j]) : d[j];
+      for (int j = 0; j < R::N; ++j) dot = fmaf(p[u][j], (float)c[j], dot);
+      dot = dpp_sum_f32(dot);
+#pragma unroll
+      for (int j = 0; j < R::N; ++j) {
+        const float g = p[u][j] * ((float)c[j] - dot) * (SIGMOID ? q[u][j] : 1.0f);
+        d[u][j] = l[u][j] > -INFINITY ? fmaf(scale, g, d[u][j]) : d[u][j];
+      }
     }
-  }
-#pragma unroll
-  for (int j = 0; j < NPL; ++j) {
-    const int e = j * 64 + lane;
-    if (e < a.E) a.d_logits[(size_t)t * a.E + e] = d[j];
+    R::store(a.d_logits + (size_t)t * a.E, a.E, d[u]);
   }
 }
 
-template <int NPL>
-hipError_t part_as(const BalanceArgs& a, int chunk, int grid, hipStream_t s) {
-  const size_t lds = (size_t)a.E * 5 * 4;
-  if (a.sigmoid)
-    return MOE_LAUNCH("balance_part", s,
-                      balance_part_kernel<NPL, true><<<grid, 256, lds, s>>>(a, chunk));
-  return MOE_LAUNCH("balance_part", s,
-                    balance_part_kernel<NPL, false><<<grid, 256, lds, s>>>(a, chunk));
-}
-template <int NPL>
-hipError_t back_as(const BalanceArgs& a, hipStream_t s) {
-  const int grid = (a.T + 3) / 4;
-  if (a.sigmoid)
-    return MOE_LAUNCH("balance_backward", s,
-                      balance_backward_kernel<NPL, true><<<grid, 256, 0, s>>>(a));
-  return MOE_LAUNCH("balance_backward", s,
-                    balance_backward_kernel<NPL, false><<<grid, 256, 0, s>>>(a));
+// Calls f with the Row that fits E: past 128 experts four neighbours a lane where rows
+// start at 16 bytes, so that a row is one load or few.
+template <typename F>
+hipError_t with_row(int E, F f) {
+  if (E <= 64) return f(Row<1, 4, false>());
+  if (E <= 128) return f(Row<2, 4, false>());
+  const bool four = E % 4 == 0;
+  if (E <= 256) return four ? f(Row<4, 4, true>()) : f(Row<4, 4, false>());
+  if (E <= 512) return four ? f(Row<8, 2, true>()) : f(Row<8, 2, false>());
+  return four ? f(Row<16, 1, true>()) : f(Row<16, 1, false>());
 }
 
 }  // namespace
 
 int balance_chunk(int T) {
   const int c = (T + 511) / 512;
-  return c < 16 ? 16 : (c + 15) / 16 * 16;
+  return c < 32 ? 32 : (c + 31) / 32 * 32;
 }
+int balance_blocks(int E) { return (E + JOIN_E - 1) / JOIN_E; }
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
+  if (a.T <= SMALL_T && a.E <= SMALL_E && a.n_seq <= SMALL_SEQ) {
+    return with_row(a.E, [&](auto row) {
+      using R = decltype(row);
+      if constexpr (R::N > 4) return hipErrorInvalidValue;  // E is at most 256
+      else if (a.sigmoid)
+        return MOE_LAUNCH("balance_small", s, balance_small_kernel<R, true><<<1, 1024, 0, s>>>(a));
+      else
+        return MOE_LAUNCH("balance_small", s, balance_small_kernel<R, false><<<1, 1024, 0, s>>>(a));
+    });
+  }
   const int chunk = balance_chunk(a.T);
   // one workgroup at least: the second launch needs the ticket that the first one clears
   const int grid = a.T > chunk ? (a.T + chunk - 1) / chunk : 1;
-  hipError_t e;
-  if (a.E <= 64) e = part_as<1>(a, chunk, grid, s);
-  else if (a.E <= 128) e = part_as<2>(a, chunk, grid, s);
-  else if (a.E <= 256) e = part_as<4>(a, chunk, grid, s);
-  else if (a.E <= 512) e = part_as<8>(a, chunk, grid, s);
-  else e = part_as<16>(a, chunk, grid, s);
+  const size_t lds = (size_t)a.E * (PART_W + 1) * 4;
+  hipError_t e = with_row(a.E, [&](auto row) {
+    using R = decltype(row);
+    if (a.sigmoid)
+      return MOE_LAUNCH("balance_part", s,
+                        balance_part_kernel<R, true><<<grid, 64 * PART_W, lds, s>>>(a, chunk));
+    return MOE_LAUNCH("balance_part", s,
+                      balance_part_kernel<R, false><<<grid, 64 * PART_W, lds, s>>>(a, chunk));
+  });
   if (e != hipSuccess) return e;
-  const int blocks = (a.E + 63) / 64;
-  return MOE_LAUNCH("balance_join", s,
-                    balance_join_kernel<<<a.n_seq * blocks, 1024, 0, s>>>(a, chunk, blocks));
+  const int blocks = balance_blocks(a.E), n = a.n_seq * blocks;
+  // few sequences have many chunks each, and few workgroups count themselves out
+  if (n <= 256)
+    return MOE_LAUNCH("balance_join", s,
+                      balance_join_kernel<16, true><<<n, 1024, 0, s>>>(a, chunk, blocks));
+  e = MOE_LAUNCH("balance_join", s, balance_join_kernel<4, false><<<n, 256, 0, s>>>(a, chunk, blocks));
+  if (e != hipSuccess) return e;
+  return MOE_LAUNCH("balance_finish", s, balance_finish_kernel<<<1, 64, 0, s>>>(a, blocks));
 }
 
 hipError_t launch_balance_backward(const BalanceArgs& a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
-  if (a.E <= 64) return back_as<1>(a, s);
-  if (a.E <= 128) return back_as<2>(a, s);
-  if (a.E <= 256) return back_as<4>(a, s);
-  if (a.E <= 512) return back_as<8>(a, s);
-  return back_as<16>(a, s);
+  return with_row(a.E, [&](auto row) {
+    using R = decltype(row);
+    const int grid = (a.T + 4 * R::U - 1) / (4 * R::U);
+    if (a.sigmoid)
+      return MOE_LAUNCH("balance_backward", s,
+                        balance_backward_kernel<R, true><<<grid, 256, 0, s>>>(a));
+    return MOE_LAUNCH("balance_backward", s,
+                      balance_backward_kernel<R, false><<<grid, 256, 0, s>>>(a));
+  });
 }
 
 }  // namespace moe

@@ -43,6 +43,18 @@ MOE_DEV uint4 pack8(const float* f) {
   return v;
 }
 
+// Two values rounded to nearest even by the conversion instruction (a NaN stays one).
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+MOE_DEV uint32_t cvt_bf16x2(float lo, float hi) {
+  const f32x2_t f = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2_t));
+}
+MOE_DEV uint4 cvt8(const float* f) {
+  return make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]),
+                    cvt_bf16x2(f[6], f[7]));
+}
+
 MOE_DEV float silu_f(float a) { return a / (1.0f + expf(-a)); }
 
 // 64-bit wave reductions through cross-lane shuffles (fixed order: deterministic)

@@ -7,9 +7,11 @@
 //   dx = round(dh + s (g - mean(g) - xh mean(g xh)))   (mean(g) only with centring)
 //   dw = sum_t dy xh,  db = sum_t dy
 //
-// A workgroup takes one row at a time and keeps it in registers: the sums of squares are
-// of the differences from the mean, not differences of sums.  All sums are in fp32, in an
-// order that depends on the sizes alone.
+// A row stays in registers: the sums of squares are of the differences from the mean, not
+// differences of sums.  All sums are in fp32, in an order that depends on the sizes alone.
+// Rows past 512 elements take a workgroup each, shorter ones 2^i lanes each.
+#include <type_traits>
+
 #include "common.hpp"
 #include "internal.hpp"
 #include "step.hpp"
@@ -18,7 +20,9 @@
 namespace moe {
 namespace {
 
-// Eight neighbouring elements of a row: one 16-byte access in bf16, two in fp32.
+// Eight neighbouring elements of a row: one 16-byte access in bf16, two in fp32.  keep() is
+// no instruction: the compiler takes the values as new ones, so that it unpacks them again
+// behind it and does not hold them unpacked over a barrier.
 template <typename E>
 struct Vec8;
 template <>
@@ -27,7 +31,8 @@ struct Vec8<bf16_t> {
   MOE_DEV void load(const void* p, size_t i) { a = ((const uint4*)p)[i]; }
   MOE_DEV void store(void* p, size_t i) const { ((uint4*)p)[i] = a; }
   MOE_DEV void get(float* f) const { unpack8(a, f); }
-  MOE_DEV void set(const float* f) { a = pack8(f); }
+  MOE_DEV void keep() { asm volatile("" : "+v"(a.x), "+v"(a.y), "+v"(a.z), "+v"(a.w)); }
+  MOE_DEV void set(const float* f) { a = cvt8(f); }
 };
 template <>
 struct Vec8<float> {
@@ -43,6 +48,9 @@ struct Vec8<float> {
   MOE_DEV void get(float* f) const {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+  MOE_DEV void keep() {
+    asm volatile("" : "+v"(a.x), "+v"(a.y), "+v"(a.z), "+v"(a.w), "+v"(b.x), "+v"(b.y), "+v"(b.z), "+v"(b.w));
   }
   MOE_DEV void set(const float* f) {
     a = make_float4(f[0], f[1], f[2], f[3]);
@@ -62,6 +70,151 @@ MOE_DEV float group_sum(float v, float* slot) {
 #pragma unroll
   for (int w = 1; w < W; ++w) t += slot[w];
   return t;
+}
+
+// The sum of v over L neighbouring lanes, in each of them.
+template <int L>
+MOE_DEV float lanes_sum(float v) {
+  if constexpr (L == 64) return dpp_sum_f32(v);
+#pragma unroll
+  for (int o = L / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// Rows of at most L chunks, L lanes each, one chunk a lane.
+template <typename E, int L, bool CENTRE>
+__global__ __launch_bounds__(256) void norm_short_kernel(NormArgs p) {
+  constexpr int ROWS = 256 / L;
+  const int chunks = p.H / 8, i = threadIdx.x & (L - 1), slot = threadIdx.x / L;
+  const float inv = 1.0f / (float)p.H;
+  const bool on = i < chunks;
+  float wf[8], bf[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    wf[j] = 1.0f;
+    bf[j] = 0.0f;
+  }
+  Vec8<E> v;
+  if (on && p.w) v.load(p.w, i), v.get(wf);
+  if (on && p.b) v.load(p.b, i), v.get(bf);
+  for (int64_t row = (int64_t)blockIdx.x * ROWS + slot; row < p.T; row += (int64_t)gridDim.x * ROWS) {
+    const size_t at = (size_t)row * chunks + i;
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+    if (on) {
+      v.load(p.x, at);
+      v.get(f);
+      if (p.res) {
+        float r[8];
+        v.load(p.res, at);
+        v.get(r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] += r[j];
+        v.set(f);
+        v.store(p.h, at);
+        v.get(f);  // the norm is that of h as it is kept: the backward reads it
+      }
+    }
+    float sum = 0.0f, sq = 0.0f;
+    if (CENTRE) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += f[j];
+      sum = lanes_sum<L>(sum);
+    }
+    const float mu = sum * inv;
+    if (on) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        f[j] -= mu;
+        sq = fmaf(f[j], f[j], sq);
+      }
+    }
+    const float rstd = 1.0f / sqrtf(lanes_sum<L>(sq) * inv + p.eps);
+    if (i == 0) *(float2*)(p.stats + 2 * row) = make_float2(mu, rstd);
+    if (on) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * wf[j] + bf[j];
+      v.set(f);
+      v.store(p.y, at);
+    }
+  }
+}
+
+template <typename E, int L, bool CENTRE>
+__global__ __launch_bounds__(256) void norm_short_backward_kernel(NormBackArgs p) {
+  constexpr int ROWS = 256 / L;
+  __shared__ float s_sum[4][2][8 * L];
+  const int chunks = p.H / 8, i = threadIdx.x & (L - 1), slot = threadIdx.x / L;
+  const float inv = 1.0f / (float)p.H;
+  const bool on = i < chunks;
+  float wf[8], dw[8], db[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    wf[j] = 1.0f;
+    dw[j] = db[j] = 0.0f;
+  }
+  Vec8<E> v;
+  if (on && p.w) v.load(p.w, i), v.get(wf);
+  for (int64_t row = (int64_t)blockIdx.x * ROWS + slot; row < p.T; row += (int64_t)gridDim.x * ROWS) {
+    const size_t at = (size_t)row * chunks + i;
+    const float2 st = *(const float2*)(p.stats + 2 * row);
+    const float mu = CENTRE ? st.x : 0.0f, rstd = st.y;
+    float x[8], g[8], d[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = g[j] = d[j] = 0.0f;
+    float sg = 0.0f, sgx = 0.0f;
+    if (on) {
+      Vec8<E> vg, vd;
+      v.load(p.h, at);
+      vg.load(p.dy, at);
+      if (p.dh) vd.load(p.dh, at);
+      v.get(x);
+      vg.get(g);
+      if (p.dh) vd.get(d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[j] = (x[j] - mu) * rstd;
+        dw[j] = fmaf(g[j], x[j], dw[j]);
+        db[j] += g[j];
+        g[j] *= wf[j];
+        sg += g[j];
+        sgx = fmaf(g[j], x[j], sgx);
+      }
+    }
+    const float mg = CENTRE ? lanes_sum<L>(sg) * inv : 0.0f;
+    const float mgx = lanes_sum<L>(sgx) * inv;
+    if (on) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] += rstd * (g[j] - mg - x[j] * mgx);
+      v.set(d);
+      v.store(p.dx, at);
+    }
+  }
+  if (!p.dw && !p.db) return;
+  // the rows of a wavefront, then the wavefronts
+#pragma unroll
+  for (int o = L; o < 64; o <<= 1) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      dw[j] += __shfl_xor(dw[j], o, 64);
+      db[j] += __shfl_xor(db[j], o, 64);
+    }
+  }
+  const int wave = threadIdx.x >> 6;
+  if (lane_id() < L) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      s_sum[wave][0][j * L + i] = dw[j];
+      s_sum[wave][1][j * L + i] = db[j];
+    }
+  }
+  __syncthreads();
+  float* out = p.parts + (size_t)blockIdx.x * 2 * p.H;
+  for (int c = threadIdx.x; c < 2 * p.H; c += 256) {
+    const int k = c >= p.H, e = c - k * p.H, at = (e & 7) * L + (e >> 3);
+    out[c] = (s_sum[0][k][at] + s_sum[1][k][at]) + (s_sum[2][k][at] + s_sum[3][k][at]);
+  }
 }
 
 template <typename E, int W, int C, bool CENTRE>
@@ -146,64 +299,98 @@ __global__ __launch_bounds__(64 * W) void norm_kernel(NormArgs p) {
 
 template <typename E, int W, int C, bool CENTRE>
 __global__ __launch_bounds__(64 * W) void norm_backward_kernel(NormBackArgs p) {
-  __shared__ float s_g[2][W], s_gx[2][W];
+  // Two chunks of fp32 leave no registers for the sums of dw and db (1024 threads have 128
+  // each): they lie in LDS, each thread's own, with lanes side by side.
+  constexpr bool IN_LDS = sizeof(E) == 4 && C > 1;
+  constexpr int NT = 64 * W, SUMS = IN_LDS ? 2 * C * 8 * NT : 1;
+  __shared__ float s_g[2][W], s_gx[2][W], s_acc[SUMS];
   const int chunks = p.H / 8;
   const float inv = 1.0f / (float)p.H;
   Vec8<E> w[C];
   float dw[C][8], db[C][8];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int i = c * 64 * W + (int)threadIdx.x;
-    if (i < chunks && p.w) w[c].load(p.w, i);
+    const int i = c * NT + (int)threadIdx.x;
+    if (!IN_LDS && i < chunks && p.w) w[c].load(p.w, i);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[c][j] = db[c][j] = 0.0f;
+    for (int j = 0; j < 8; ++j) {
+      if (IN_LDS) {
+        s_acc[(c * 8 + j) * NT + threadIdx.x] = 0.0f;
+        s_acc[((C + c) * 8 + j) * NT + threadIdx.x] = 0.0f;
+      } else {
+        dw[c][j] = db[c][j] = 0.0f;
+      }
+    }
   }
   int parity = 0;
   for (int row = blockIdx.x; row < p.T; row += gridDim.x, parity ^= 1) {
     const size_t at = (size_t)row * chunks;
     const float mu = CENTRE ? p.stats[2 * (size_t)row] : 0.0f;
     const float rstd = p.stats[2 * (size_t)row + 1];
-    float xh[C][8], g[C][8];
+    Vec8<E> vh[C], vdy[C], vdh[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int i = c * NT + (int)threadIdx.x;
+      if (i < chunks) {
+        vh[c].load(p.h, at + i);
+        vdy[c].load(p.dy, at + i);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int i = c * NT + (int)threadIdx.x;
+      if (!IN_LDS && i < chunks && p.dh) vdh[c].load(p.dh, at + i);
+    }
     float sg = 0.0f, sgx = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int i = c * 64 * W + (int)threadIdx.x;
+      const int i = c * NT + (int)threadIdx.x;
       if (i < chunks) {
-        float wf[8];
-        Vec8<E> v;
-        v.load(p.h, at + i);
-        v.get(xh[c]);
-        v.load(p.dy, at + i);
-        v.get(g[c]);
+        float x[8], g[8], wf[8];
+        vh[c].get(x);
+        vdy[c].get(g);
+        if (IN_LDS && p.w) w[c].load(p.w, i);
         if (p.w) w[c].get(wf);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          xh[c][j] = (xh[c][j] - mu) * rstd;
-          dw[c][j] = fmaf(g[c][j], xh[c][j], dw[c][j]);
-          db[c][j] += g[c][j];
-          if (p.w) g[c][j] *= wf[j];
-          sg += g[c][j];
-          sgx = fmaf(g[c][j], xh[c][j], sgx);
+          x[j] = (x[j] - mu) * rstd;
+          if (IN_LDS) {
+            float* acc = s_acc + (c * 8 + j) * NT + threadIdx.x;
+            acc[0] = fmaf(g[j], x[j], acc[0]);
+            acc[C * 8 * NT] += g[j];
+          } else {
+            dw[c][j] = fmaf(g[j], x[j], dw[c][j]);
+            db[c][j] += g[j];
+          }
+          if (p.w) g[j] *= wf[j];
+          sg += g[j];
+          sgx = fmaf(g[j], x[j], sgx);
         }
+        vh[c].keep();
+        vdy[c].keep();
       }
     }
     const float mg = CENTRE ? group_sum<W>(sg, s_g[parity]) * inv : 0.0f;
     const float mgx = group_sum<W>(sgx, s_gx[parity]) * inv;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int i = c * 64 * W + (int)threadIdx.x;
+      const int i = c * NT + (int)threadIdx.x;
       if (i < chunks) {
-        float d[8];
-        Vec8<E> v;
-        if (p.dh) {
-          v.load(p.dh, at + i);
-          v.get(d);
-        }
+        float x[8], g[8], wf[8], d[8];
+        vh[c].get(x);
+        vdy[c].get(g);
+        if (IN_LDS && p.w) w[c].load(p.w, i);
+        if (IN_LDS && p.dh) vdh[c].load(p.dh, at + i);
+        if (p.w) w[c].get(wf);
+        if (p.dh) vdh[c].get(d);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float t = rstd * (g[c][j] - mg - xh[c][j] * mgx);
+          x[j] = (x[j] - mu) * rstd;
+          if (p.w) g[j] *= wf[j];
+          const float t = rstd * (g[j] - mg - x[j] * mgx);
           d[j] = p.dh ? d[j] + t : t;
         }
+        Vec8<E> v;
         v.set(d);
         v.store(p.dx, at + i);
       }
@@ -213,8 +400,15 @@ __global__ __launch_bounds__(64 * W) void norm_backward_kernel(NormBackArgs p) {
   float* out = p.parts + (size_t)blockIdx.x * 2 * p.H;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int i = c * 64 * W + (int)threadIdx.x;
+    const int i = c * NT + (int)threadIdx.x;
     if (i < chunks) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (IN_LDS) {
+          dw[c][j] = s_acc[(c * 8 + j) * NT + threadIdx.x];
+          db[c][j] = s_acc[((C + c) * 8 + j) * NT + threadIdx.x];
+        }
+      }
       Vec8<float> v;
       v.set(dw[c]);
       v.store(out, i);
@@ -224,106 +418,158 @@ __global__ __launch_bounds__(64 * W) void norm_backward_kernel(NormBackArgs p) {
   }
 }
 
-// dw and db from the workgroups' sums, added up in their order.  16 lanes take 64
-// neighbouring columns, 16 such rows of lanes every 16th part each, joined through LDS.
-template <typename E>
+// dw and db from the workgroups' sums, added up in their order: L lanes take 4 L
+// neighbouring columns, 256 / L such rows of lanes every (256 / L)th workgroup each, joined
+// through LDS.  Few columns take 4 lanes, so that there are more parts and workgroups
+// (the backward of 1003 x 2040 in fp32: 13.9 -> 12.9 us); many take 16, whose reads are longer.
+template <typename E, int L>
 __global__ __launch_bounds__(256) void norm_wgrad_kernel(NormBackArgs p, int groups) {
-  __shared__ float4 s_sum[16][16];
-  const int lane = threadIdx.x & 15, part = threadIdx.x >> 4;
-  const int col = blockIdx.x * 64 + lane * 4;  // of the 2 H columns (dw | db)
+  constexpr int PARTS = 256 / L;
+  __shared__ float4 s_sum[PARTS][L];
+  const int lane = threadIdx.x & (L - 1), part = threadIdx.x / L;
+  const int col = blockIdx.x * 4 * L + lane * 4;  // of the 2 H columns (dw | db)
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
   if (col < 2 * p.H) {
-    for (int g = part; g < groups; g += 16) {
+#pragma unroll 8
+    for (int g = part; g < groups; g += PARTS) {
       const float4 v = *(const float4*)(p.parts + (size_t)g * 2 * p.H + col);
       t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
     }
   }
   s_sum[part][lane] = t;
-  __syncthreads();
-  if (part || col >= 2 * p.H) return;
-  for (int k = 1; k < 16; ++k) {
-    const float4 v = s_sum[k][lane];
-    t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+#pragma unroll
+  for (int half = PARTS / 2; half >= 1; half >>= 1) {
+    __syncthreads();
+    if (part < half) {
+      const float4 v = s_sum[part + half][lane];
+      t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+      s_sum[part][lane] = t;
+    }
   }
+  if (part || col >= 2 * p.H) return;
   void* out = col < p.H ? p.dw : p.db;
   const int at = col < p.H ? col : col - p.H;
   if (!out) return;
   if constexpr (sizeof(E) == 2) {
-    *(uint2*)((bf16_t*)out + at) = make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
+    *(uint2*)((bf16_t*)out + at) = make_uint2(cvt_bf16x2(t.x, t.y), cvt_bf16x2(t.z, t.w));
   } else {
     *(float4*)((float*)out + at) = t;
   }
 }
 
-// Wavefronts of a row and 16-byte chunks of a thread: the fewest wavefronts whose threads
-// hold at most two chunks each.
+// Wavefronts of a row: as many as it has 64 chunks of 8 elements, so that a thread holds
+// one chunk, up to 8; then two chunks, and 16 wavefronts past 1024 chunks.
 int waves_of(int H) {
   const int chunks = H / 8;
   int w = 1;
-  while (w < 16 && 64 * w * 2 < chunks) w *= 2;
-  return w;
+  while (w < 8 && 64 * w < chunks) w *= 2;
+  return chunks > 1024 ? 16 : w;
+}
+int chunks_of(int H) { return H / 8 > 64 * waves_of(H) ? 2 : 1; }
+
+constexpr int SHORT_H = 512;
+// Lanes of a short row.
+int lanes_of(int H) {
+  int l = 1;
+  while (8 * l < H) l *= 2;
+  return l;
 }
 
-template <typename E, int W, int C>
-hipError_t norm_as(const NormArgs& p, bool centre, int grid, hipStream_t s) {
-  if (centre)
-    return MOE_LAUNCH("norm", s, norm_kernel<E, W, C, true><<<grid, 64 * W, 0, s>>>(p));
-  return MOE_LAUNCH("norm", s, norm_kernel<E, W, C, false><<<grid, 64 * W, 0, s>>>(p));
-}
-template <typename E, int W, int C>
-hipError_t norm_back_as(const NormBackArgs& p, bool centre, int grid, hipStream_t s) {
-  if (centre)
-    return MOE_LAUNCH("norm_backward", s,
-                      norm_backward_kernel<E, W, C, true><<<grid, 64 * W, 0, s>>>(p));
-  return MOE_LAUNCH("norm_backward", s,
-                    norm_backward_kernel<E, W, C, false><<<grid, 64 * W, 0, s>>>(p));
-}
-
-template <typename E>
-hipError_t norm_of(const NormArgs& p, bool centre, hipStream_t s) {
-  const int w = waves_of(p.H);
-  const int grid = p.T < 16384 / w ? p.T : 16384 / w;
-  if (w == 1 && p.H <= 512) return norm_as<E, 1, 1>(p, centre, grid, s);
-  switch (w) {
-    case 1: return norm_as<E, 1, 2>(p, centre, grid, s);
-    case 2: return norm_as<E, 2, 2>(p, centre, grid, s);
-    case 4: return norm_as<E, 4, 2>(p, centre, grid, s);
-    case 8: return norm_as<E, 8, 2>(p, centre, grid, s);
+template <int N>
+using Int = std::integral_constant<int, N>;
+// Calls f with the lanes of short rows.
+template <typename F>
+hipError_t with_lanes(int H, F f) {
+  switch (lanes_of(H)) {
+    case 1: return f(Int<1>());
+    case 2: return f(Int<2>());
+    case 4: return f(Int<4>());
+    case 8: return f(Int<8>());
+    case 16: return f(Int<16>());
+    case 32: return f(Int<32>());
   }
-  return norm_as<E, 16, 2>(p, centre, grid, s);
+  return f(Int<64>());
 }
-template <typename E>
-hipError_t norm_back_of(const NormBackArgs& p, bool centre, hipStream_t s) {
-  const int w = waves_of(p.H), grid = norm_groups(p.T, p.H);
+// Calls f with the wavefronts and the chunks of long rows.
+template <typename F>
+hipError_t with_waves(int H, F f) {
+  switch (waves_of(H) * chunks_of(H)) {
+    case 2: return f(Int<2>(), Int<1>());
+    case 4: return f(Int<4>(), Int<1>());
+    case 8: return f(Int<8>(), Int<1>());
+    case 16: return f(Int<8>(), Int<2>());
+  }
+  return f(Int<16>(), Int<2>());
+}
+
+template <typename E, bool CENTRE>
+hipError_t norm_of(const NormArgs& p, hipStream_t s) {
+  if (p.H <= SHORT_H)
+    return with_lanes(p.H, [&](auto l) {
+      constexpr int L = decltype(l)::value;
+      const int64_t passes = ((int64_t)p.T + 256 / L - 1) / (256 / L);
+      const int grid = passes < 4096 ? (int)passes : 4096;
+      return MOE_LAUNCH("norm", s, norm_short_kernel<E, L, CENTRE><<<grid, 256, 0, s>>>(p));
+    });
+  return with_waves(p.H, [&](auto w, auto c) {
+    constexpr int W = decltype(w)::value, C = decltype(c)::value;
+    const int grid = p.T < 16384 / W ? p.T : 16384 / W;
+    return MOE_LAUNCH("norm", s, norm_kernel<E, W, C, CENTRE><<<grid, 64 * W, 0, s>>>(p));
+  });
+}
+template <typename E, bool CENTRE>
+hipError_t norm_back_of(const NormBackArgs& p, hipStream_t s) {
+  const int grid = norm_groups(p.T, p.H);
   if (p.T > 0) {
-    hipError_t e;
-    if (w == 1 && p.H <= 512) e = norm_back_as<E, 1, 1>(p, centre, grid, s);
-    else if (w == 1) e = norm_back_as<E, 1, 2>(p, centre, grid, s);
-    else if (w == 2) e = norm_back_as<E, 2, 2>(p, centre, grid, s);
-    else if (w == 4) e = norm_back_as<E, 4, 2>(p, centre, grid, s);
-    else if (w == 8) e = norm_back_as<E, 8, 2>(p, centre, grid, s);
-    else e = norm_back_as<E, 16, 2>(p, centre, grid, s);
+    const hipError_t e =
+        p.H <= SHORT_H
+            ? with_lanes(p.H,
+                         [&](auto l) {
+                           constexpr int L = decltype(l)::value;
+                           return MOE_LAUNCH("norm_backward", s,
+                                             norm_short_backward_kernel<E, L, CENTRE>
+                                             <<<grid, 256, 0, s>>>(p));
+                         })
+            : with_waves(p.H, [&](auto w, auto c) {
+                constexpr int W = decltype(w)::value, C = decltype(c)::value;
+                return MOE_LAUNCH("norm_backward", s,
+                                  norm_backward_kernel<E, W, C, CENTRE><<<grid, 64 * W, 0, s>>>(p));
+              });
     if (e != hipSuccess) return e;
   }
   if (!p.dw && !p.db) return hipSuccess;
-  const int blocks = (2 * p.H + 63) / 64;
-  return MOE_LAUNCH("norm_wgrad", s, norm_wgrad_kernel<E><<<blocks, 256, 0, s>>>(p, grid));
+  if (2 * p.H < 4096)
+    return MOE_LAUNCH("norm_wgrad", s,
+                      norm_wgrad_kernel<E, 4><<<(2 * p.H + 15) / 16, 256, 0, s>>>(p, grid));
+  return MOE_LAUNCH("norm_wgrad", s,
+                    norm_wgrad_kernel<E, 16><<<(2 * p.H + 63) / 64, 256, 0, s>>>(p, grid));
 }
 
 }  // namespace
 
+// Workgroups of the backward: each leaves a row of sums, so that there are no more than fill
+// the card, and several rows for each.
 int norm_groups(int T, int H) {
-  const int most = 4096 / waves_of(H);
-  const int rows = (T + 3) / 4;
-  return rows < most ? rows : most;
+  int most, rows;
+  if (H <= SHORT_H) {
+    most = 1024;
+    rows = 2 * 256 / lanes_of(H);
+  } else {
+    most = 4096 / waves_of(H);
+    rows = 4;
+  }
+  const int want = (int)(((int64_t)T + rows - 1) / rows);
+  return want < most ? want : most;
 }
 
 hipError_t launch_norm(const NormArgs& p, bool f32, bool centre, hipStream_t s) {
-  return f32 ? norm_of<float>(p, centre, s) : norm_of<bf16_t>(p, centre, s);
+  if (f32) return centre ? norm_of<float, true>(p, s) : norm_of<float, false>(p, s);
+  return centre ? norm_of<bf16_t, true>(p, s) : norm_of<bf16_t, false>(p, s);
 }
 
 hipError_t launch_norm_backward(const NormBackArgs& p, bool f32, bool centre, hipStream_t s) {
-  return f32 ? norm_back_of<float>(p, centre, s) : norm_back_of<bf16_t>(p, centre, s);
+  if (f32) return centre ? norm_back_of<float, true>(p, s) : norm_back_of<float, false>(p, s);
+  return centre ? norm_back_of<bf16_t, true>(p, s) : norm_back_of<bf16_t, false>(p, s);
 }
 
 }  // namespace moe

@@ -47,7 +47,7 @@ struct BalanceArgs {
   float* seg_p;       // [n_chunks + n_seq, E]
   int32_t* seg_c;     // the same
   int32_t* seg_n;     // [n_chunks + n_seq]
-  float* part;        // [n_seq, blocks]: sum of counts * p over 64 experts
+  float* part;        // [n_seq, blocks]: sum of counts * p over a block's experts
   int32_t* tokens;    // [n_seq]
   int32_t* ticket;    // [1]
   // backward
@@ -55,7 +55,8 @@ struct BalanceArgs {
   const float* d_in;    // [T, E] or null
   float* d_logits;
 };
-int balance_chunk(int T);  // tokens of a chunk
+int balance_chunk(int T);   // tokens of a chunk
+int balance_blocks(int E);  // workgroups that add up one sequence
 hipError_t launch_balance(const BalanceArgs& p, hipStream_t s);
 hipError_t launch_balance_backward(const BalanceArgs& p, hipStream_t s);
 
@@ -72,7 +73,7 @@ struct AdamwDesc {
   float weight_decay;
   int32_t pad;
 };
-constexpr int ADAMW_TILE = 8192;       // elements of a workgroup
+constexpr int ADAMW_TILE = 2048;       // elements of a workgroup
 constexpr int ADAMW_TABLE_CHUNK = 24;  // tensors that one launch writes into the table
 struct AdamwChunk {
   AdamwDesc d[ADAMW_TABLE_CHUNK];

@@ -166,9 +166,8 @@ def encode_state(x, r16, which):
             y = float(F32(abs(F32(val)) * F32(2.0 ** -X)))
             rnd = (int(r16[32 * b + j]) * 16 + 8) / 2 ** 20
             if which == "m":
-                if y < 2.0 ** -6:      # a step of 2^-9, on a grid of 2^-29
-                    z = float(F32(y) + F32(2.0 ** -6))
-                    c = int(np.floor((z - 2.0 ** -6) / 2.0 ** -9 + rnd))
+                if y < 2.0 ** -6:      # steps of 2^-9
+                    c = int(np.floor(y / 2.0 ** -9 + rnd))
                 else:
                     c = int(np.searchsorted(table, y, side="right")) - 1
                     step = 2.0 ** (np.floor(np.log2(y)) - 3)
