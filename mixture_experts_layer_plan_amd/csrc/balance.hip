@@ -21,6 +21,16 @@
 namespace moe {
 namespace {
 
+constexpr int PART_W = 8;  // wavefronts of a chunk's workgroup
+
+// A barrier for what lies in LDS alone: stores to memory stay under way (__syncthreads waits
+// for them too, a microsecond a sequence here).
+MOE_DEV void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // The last i in [0, n] with start[i] <= t (entries ascend), n for a token behind the last
 // sequence, -1 for one before the first; next: start[i + 1] (for i < n).  64 entries a step;
 // every lane gets the result, which lies in [-1, n] whatever the entries hold.
@@ -40,6 +50,24 @@ MOE_DEV int sequence_of(const int32_t* start, int n, int t, int* next) {
   }
   return lo;
 }
+
+// Looks up sequences; fewer than 64 have their starts read once, an entry a lane.
+struct Sequences {
+  const int32_t* start;
+  int n, v;
+  MOE_DEV Sequences(const BalanceArgs& a) : start(a.start), n(a.n_seq), v(INT_MAX) {
+    if (start && n < 64 && lane_id() <= n) v = start[lane_id()];
+  }
+  // as sequence_of; without starts one sequence takes every token
+  MOE_DEV int of(int t, int* next) const {
+    *next = INT_MAX;
+    if (!start) return 0;
+    if (n >= 64) return sequence_of(start, n, t, next);
+    const int ones = __popcll(ballot64(lane_id() <= n && v <= t));
+    if (ones <= n) *next = __builtin_amdgcn_readlane(v, ones);
+    return ones - 1;
+  }
+};
 
 // How a row of E experts lies in the lanes of a wavefront: N values a lane, four
 // neighbours a load (E a multiple of 4) or one; U rows at a time.
@@ -151,68 +179,59 @@ MOE_DEV void shares(const float (&l)[R::U][R::N], float (&p)[R::U][R::N], float 
   }
 }
 
-// Walks the tokens [t0, t1) of a workgroup of W wavefronts sequence by sequence, and calls
-// done(seq, n) for each, with its sums in LDS (s_p: one row of E per wavefront, s_c) and n,
-// the number of its tokens that count, in every thread.
+// The tokens [t0, t1) of a workgroup of W wavefronts, at most W * U: their shares once, then
+// their sums sequence by sequence.  done(seq, n) is called for each sequence with its sums in
+// LDS (s_p: one row of E per wavefront, s_c) and n, the number of its tokens that count, in
+// every thread.
 template <typename R, bool SIGMOID, int W, typename Done>
 MOE_DEV void walk(const BalanceArgs& a, int t0, int t1, float* s_p, int32_t* s_c, int* s_n, Done done) {
   const int wave = threadIdx.x >> 6, lane = lane_id();
+  const int w0 = t0 + wave * R::U;
+  float l[R::U][R::N], p[R::U][R::N], q[R::U][R::N];
+  int id[R::U];
+#pragma unroll
+  for (int u = 0; u < R::U; ++u) {
+    const int v = w0 + u < t1 ? w0 + u : t1 - 1;
+    id[u] = lane < a.k ? a.idx[(size_t)v * a.k + lane] : -1;
+    R::load(a.logits + (size_t)v * a.E, a.E, -INFINITY, l[u]);
+  }
+  const Sequences seqs(a);
+  shares<R, SIGMOID>(l, p, q);
   int t = t0;
   while (t < t1) {
-    // the first tokens' rows are on their way while their sequence is looked up
-    float l[R::U][R::N];
-    int id[R::U];
-    const auto load = [&](int u0) {
-#pragma unroll
-      for (int u = 0; u < R::U; ++u) {
-        const int v = u0 + u < t1 ? u0 + u : t1 - 1;
-        id[u] = lane < a.k ? a.idx[(size_t)v * a.k + lane] : -1;
-        R::load(a.logits + (size_t)v * a.E, a.E, -INFINITY, l[u]);
-      }
-    };
-    load(t + wave * R::U);
     // the tokens [t, end) that are in t's sequence
-    int seq = 0, end = t1;
-    if (a.start) {
-      int next;
-      seq = sequence_of(a.start, a.n_seq, t, &next);
-      if (seq >= a.n_seq) break;  // behind the last one
-      end = next < t1 ? next : t1;
-      if (end <= t) end = t1;  // entries that do not ascend: no endless loop
-      if (seq < 0) {           // before the first sequence
-        t = end;
-        continue;
-      }
+    int end;
+    const int seq = seqs.of(t, &end);
+    if (seq >= a.n_seq) break;               // behind the last one
+    if (end <= t || end > t1) end = t1;      // (entries that do not ascend: no endless loop)
+    if (seq < 0) {                           // before the first sequence
+      t = end;
+      continue;
     }
     for (int e = threadIdx.x; e < a.E; e += 64 * W) s_c[e] = 0;
-    __syncthreads();
+    lds_barrier();
     float acc[R::N];
 #pragma unroll
     for (int j = 0; j < R::N; ++j) acc[j] = 0.0f;
     int used = 0;
-    for (int u0 = t + wave * R::U; u0 < end; u0 += W * R::U) {
-      float p[R::U][R::N], q[R::U][R::N];
-      if (u0 > t + wave * R::U) load(u0);
-      shares<R, SIGMOID>(l, p, q);
 #pragma unroll
-      for (int u = 0; u < R::U; ++u) {
-        const bool ok = u0 + u < end && (unsigned)id[u] < (unsigned)a.E;
-        if (ok) atomicAdd(&s_c[id[u]], 1);  // whole numbers: any order gives the same
-        if (ballot64(ok)) {
-          ++used;
+    for (int u = 0; u < R::U; ++u) {
+      const bool ok = w0 + u >= t && w0 + u < end && (unsigned)id[u] < (unsigned)a.E;
+      if (ok) atomicAdd(&s_c[id[u]], 1);  // whole numbers: any order gives the same
+      if (ballot64(ok)) {
+        ++used;
 #pragma unroll
-          for (int j = 0; j < R::N; ++j) acc[j] += p[u][j];
-        }
+        for (int j = 0; j < R::N; ++j) acc[j] += p[u][j];
       }
     }
     R::store(s_p + wave * a.E, a.E, acc);
     if (lane == 0) s_n[wave] = used;
-    __syncthreads();
+    lds_barrier();
     int n = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) n += s_n[w];
     done(seq, n);
-    __syncthreads();
+    lds_barrier();
     t = end;
   }
 }
@@ -225,7 +244,6 @@ MOE_DEV float rows_sum(const float* s_p, int E, int e) {
   return v;
 }
 
-constexpr int PART_W = 8;  // wavefronts of a chunk's workgroup
 template <typename R, bool SIGMOID>
 __global__ __launch_bounds__(64 * PART_W) void balance_part_kernel(BalanceArgs a, int chunk) {
   extern __shared__ float s_mem[];
@@ -235,6 +253,7 @@ __global__ __launch_bounds__(64 * PART_W) void balance_part_kernel(BalanceArgs a
   if (blockIdx.x == 0 && threadIdx.x == 0) a.ticket[0] = 0;  // for the launch that follows
   const int t0 = blockIdx.x * chunk;
   const int t1 = t0 + chunk < a.T ? t0 + chunk : a.T;
+  if (t0 >= t1) return;  // no tokens at all
   walk<R, SIGMOID, PART_W>(a, t0, t1, s_p, s_c, s_n, [&](int seq, int n) {
     const size_t seg = (size_t)blockIdx.x + seq;
     for (int e = threadIdx.x; e < a.E; e += 64 * PART_W) {
@@ -245,18 +264,29 @@ __global__ __launch_bounds__(64 * PART_W) void balance_part_kernel(BalanceArgs a
   });
 }
 
-MOE_DEV double wave_sum_f64(double v) {
+// Sum over W wavefronts in 64 bits, in every thread.
+template <int W>
+MOE_DEV double sum_f64(double v) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  if constexpr (W == 1) return v;
+  __shared__ double slot[W];
+  __syncthreads();
+  if (lane_id() == 0) slot[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = slot[0];
+#pragma unroll
+  for (int w = 1; w < W; ++w) v += slot[w];
   return v;
 }
 
 // The loss and the scales from the sequences' tokens and sums of counts * p over `blocks`
-// groups of experts, in 64 bits, by one wavefront; a lane takes every 64th sequence.
+// groups of experts, in 64 bits, by W wavefronts; a thread takes every (64 W)th sequence.
+template <int W>
 MOE_DEV void finish(const BalanceArgs& a, const int32_t* tokens, const float* part, int blocks) {
   double loss = 0.0, have = 0.0;
   const double per = (double)a.coef * a.E / a.k;
-  for (int i = lane_id(); i < a.n_seq; i += 64) {
+  for (int i = threadIdx.x; i < a.n_seq; i += 64 * W) {
     const int N = tokens[i];
     double x = 0.0;
 #pragma unroll 4
@@ -266,46 +296,103 @@ MOE_DEV void finish(const BalanceArgs& a, const int32_t* tokens, const float* pa
       loss += per / ((double)N * N) * x;
     }
   }
-  loss = wave_sum_f64(loss);
-  have = wave_sum_f64(have);
+  loss = sum_f64<W>(loss);
+  have = sum_f64<W>(have);
   const double each = have > 0.0 ? 1.0 / have : 0.0;
-  if (lane_id() == 0) a.loss[0] = (float)(loss * each);
-  for (int i = lane_id(); i < a.n_seq; i += 64) {
+  if (threadIdx.x == 0) a.loss[0] = (float)(loss * each);
+  for (int i = threadIdx.x; i < a.n_seq; i += 64 * W) {
     const int N = tokens[i];
     a.scales[i] = N > 0 ? (float)(per * each / ((double)N * N)) : 0.0f;
   }
 }
 
-// A batch of few tokens, whole, in one workgroup of 16 wavefronts.
-constexpr int SMALL_T = 256, SMALL_E = 256, SMALL_SEQ = 64;
+// A batch of few tokens, whole, in one workgroup of 16 wavefronts: the tokens' shares and the
+// sequences' counts in LDS, then a thread for each (sequence, expert).
+constexpr int SMALL_T = 128, SMALL_E = 256, SMALL_SEQ = 64, SMALL_COUNTS = 4096;
+bool is_small(const BalanceArgs& a) {
+  return a.T <= SMALL_T && a.E <= SMALL_E && a.n_seq <= SMALL_SEQ && a.n_seq * a.E <= SMALL_COUNTS;
+}
 template <typename R, bool SIGMOID>
 __global__ __launch_bounds__(1024) void balance_small_kernel(BalanceArgs a) {
-  __shared__ float s_p[16 * SMALL_E];
-  __shared__ int32_t s_c[SMALL_E];
-  __shared__ int s_n[16];
-  __shared__ float s_part[SMALL_SEQ], s_x[4];
-  __shared__ int32_t s_tokens[SMALL_SEQ];
-  if (threadIdx.x < SMALL_SEQ) s_tokens[threadIdx.x] = -1;
-  __syncthreads();
-  walk<R, SIGMOID, 16>(a, 0, a.T, s_p, s_c, s_n, [&](int seq, int n) {
-    const int e = threadIdx.x;
+  __shared__ float s_p[SMALL_T * SMALL_E];
+  __shared__ int32_t s_c[SMALL_COUNTS];
+  __shared__ float s_part[SMALL_SEQ];
+  __shared__ int32_t s_seq[SMALL_T], s_tokens[SMALL_SEQ];
+  const int wave = threadIdx.x >> 6, lane = lane_id(), w0 = wave * R::U;
+  float l[R::U][R::N], p[R::U][R::N], q[R::U][R::N];
+  int id[R::U], seq[R::U];
+  if (w0 < a.T) {
+#pragma unroll
+    for (int u = 0; u < R::U; ++u) {
+      const int v = w0 + u < a.T ? w0 + u : a.T - 1;
+      id[u] = lane < a.k && w0 + u < a.T ? a.idx[(size_t)v * a.k + lane] : -1;
+      R::load(a.logits + (size_t)v * a.E, a.E, -INFINITY, l[u]);
+    }
+  }
+  const Sequences seqs(a);
+  for (int i = threadIdx.x; i < a.n_seq * a.E; i += 1024) s_c[i] = 0;
+  if (w0 < a.T) {
+    shares<R, SIGMOID>(l, p, q);
+#pragma unroll
+    for (int u = 0; u < R::U; ++u) {
+      if (w0 + u >= a.T) break;
+      int end;
+      seq[u] = seqs.of(w0 + u, &end);
+      const bool used = ballot64((unsigned)id[u] < (unsigned)a.E) && seq[u] >= 0 && seq[u] < a.n_seq;
+      if (!used) {
+        seq[u] = -1;
+#pragma unroll
+        for (int j = 0; j < R::N; ++j) p[u][j] = 0.0f;
+      }
+      R::store(s_p + (w0 + u) * a.E, a.E, p[u]);
+      if (lane == 0) s_seq[w0 + u] = seq[u];
+    }
+  }
+  lds_barrier();
+  if (w0 < a.T) {
+#pragma unroll
+    for (int u = 0; u < R::U; ++u)  // whole numbers: any order gives the same
+      if (w0 + u < a.T && seq[u] >= 0 && (unsigned)id[u] < (unsigned)a.E)
+        atomicAdd(&s_c[seq[u] * a.E + id[u]], 1);
+  }
+  lds_barrier();
+  const auto range = [&](int i, int* b, int* end) {
+    *b = a.start ? a.start[i] : 0;
+    *end = a.start ? a.start[i + 1] : a.T;
+    *b = *b > 0 ? *b : 0;
+    *end = *end < a.T ? *end : a.T;
+  };
+  for (int i = threadIdx.x; i < a.n_seq * a.E; i += 1024) {
+    const int sq = i / a.E, e = i - sq * a.E;
+    int b, end;
+    range(sq, &b, &end);
+    float v = 0.0f;
+    for (int t = b; t < end; t += 16) {
+      float x[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = s_p[(t + k < end ? t + k : t) * a.E + e];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v += t + k < end ? x[k] : 0.0f;
+    }
+    a.counts[i] = s_c[i];
+    s_c[i] = __float_as_int(v * (float)s_c[i]);  // from here on the products
+  }
+  lds_barrier();
+  for (int i = wave; i < a.n_seq; i += 16) {
+    int b, end;
+    range(i, &b, &end);
     float x = 0.0f;
-    if (e < a.E) {
-      x = rows_sum<16>(s_p, a.E, e) * (float)s_c[e];
-      a.counts[(size_t)seq * a.E + e] = s_c[e];
-    }
+    int n = 0;
+    for (int e = lane; e < a.E; e += 64) x += __int_as_float(s_c[i * a.E + e]);
     x = dpp_sum_f32(x);
-    if (e < SMALL_E && lane_id() == 0) s_x[e >> 6] = x;
-    __syncthreads();
-    if (e == 0) {
-      s_part[seq] = (s_x[0] + s_x[1]) + (s_x[2] + s_x[3]);
-      s_tokens[seq] = n;
+    for (int t = b; t < end; t += 64) n += __popcll(ballot64(t + lane < end && s_seq[t + lane < end ? t + lane : b] == i));
+    if (lane == 0) {
+      s_part[i] = x;
+      s_tokens[i] = n;
     }
-  });
-  __syncthreads();
-  for (int i = 0; i < a.n_seq; ++i)  // sequences that the walk met no token of
-    if (s_tokens[i] < 0 && (int)threadIdx.x < a.E) a.counts[(size_t)i * a.E + threadIdx.x] = 0;
-  if (threadIdx.x < 64) finish(a, s_tokens, s_part, 1);
+  }
+  lds_barrier();
+  if (wave == 0) finish<1>(a, s_tokens, s_part, 1);
 }
 
 // Adds the segments of sequence blockIdx.x / blocks for JOIN_E experts: lane l the experts
@@ -386,13 +473,13 @@ __global__ __launch_bounds__(64 * W) void balance_join_kernel(BalanceArgs a, int
       }
       if (!__builtin_amdgcn_readfirstlane(last)) return;
       __threadfence();
-      finish(a, a.tokens, a.part, blocks);
+      finish<1>(a, a.tokens, a.part, blocks);
     }
   }
 }
 
-__global__ __launch_bounds__(64) void balance_finish_kernel(BalanceArgs a, int blocks) {
-  finish(a, a.tokens, a.part, blocks);
+__global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a, int blocks) {
+  finish<16>(a, a.tokens, a.part, blocks);
 }
 
 template <typename R, bool SIGMOID>
@@ -411,6 +498,7 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs a) {
     for (int j = 0; j < R::N; ++j) d[u][j] = 0.0f;
     if (a.d_in) R::load(a.d_in + (size_t)t * a.E, a.E, 0.0f, d[u]);
   }
+  const Sequences seqs(a);
   const float up = a.d_loss ? a.d_loss[0] : 1.0f;
   int seq = -2, end = 0, have = -2;
   int c[R::N];
@@ -421,9 +509,7 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs a) {
     const int t = t0 + u;
     if (t >= a.T) break;
     if (u == 0 || t >= end) {
-      seq = 0;
-      end = a.T;
-      if (a.start) seq = sequence_of(a.start, a.n_seq, t, &end);
+      seq = seqs.of(t, &end);
       if (seq >= a.n_seq) end = a.T;
     }
     if (ballot64((unsigned)id[u] < (unsigned)a.E) && seq >= 0 && seq < a.n_seq) {
@@ -447,28 +533,25 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs a) {
 }
 
 // Calls f with the Row that fits E: past 128 experts four neighbours a lane where rows
-// start at 16 bytes, so that a row is one load or few.
-template <typename F>
+// start at 16 bytes, so that a row is one load or few.  UP: rows at a time of few experts.
+template <int UP, typename F>
 hipError_t with_row(int E, F f) {
-  if (E <= 64) return f(Row<1, 4, false>());
-  if (E <= 128) return f(Row<2, 4, false>());
+  if (E <= 64) return f(Row<1, UP, false>());
+  if (E <= 128) return f(Row<2, UP, false>());
   const bool four = E % 4 == 0;
-  if (E <= 256) return four ? f(Row<4, 4, true>()) : f(Row<4, 4, false>());
+  if (E <= 256) return four ? f(Row<4, UP, true>()) : f(Row<4, UP, false>());
   if (E <= 512) return four ? f(Row<8, 2, true>()) : f(Row<8, 2, false>());
   return four ? f(Row<16, 1, true>()) : f(Row<16, 1, false>());
 }
 
 }  // namespace
 
-int balance_chunk(int T) {
-  const int c = (T + 511) / 512;
-  return c < 32 ? 32 : (c + 31) / 32 * 32;
-}
+int balance_chunk(int E) { return PART_W * (E <= 256 ? 4 : E <= 512 ? 2 : 1); }
 int balance_blocks(int E) { return (E + JOIN_E - 1) / JOIN_E; }
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
-  if (a.T <= SMALL_T && a.E <= SMALL_E && a.n_seq <= SMALL_SEQ) {
-    return with_row(a.E, [&](auto row) {
+  if (is_small(a)) {
+    return with_row<SMALL_T / 16>(a.E, [&](auto row) {
       using R = decltype(row);
       if constexpr (R::N > 4) return hipErrorInvalidValue;  // E is at most 256
       else if (a.sigmoid)
@@ -477,11 +560,11 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
         return MOE_LAUNCH("balance_small", s, balance_small_kernel<R, false><<<1, 1024, 0, s>>>(a));
     });
   }
-  const int chunk = balance_chunk(a.T);
+  const int chunk = balance_chunk(a.E);
   // one workgroup at least: the second launch needs the ticket that the first one clears
-  const int grid = a.T > chunk ? (a.T + chunk - 1) / chunk : 1;
+  const int grid = a.T > chunk ? (a.T - 1) / chunk + 1 : 1;
   const size_t lds = (size_t)a.E * (PART_W + 1) * 4;
-  hipError_t e = with_row(a.E, [&](auto row) {
+  hipError_t e = with_row<4>(a.E, [&](auto row) {
     using R = decltype(row);
     if (a.sigmoid)
       return MOE_LAUNCH("balance_part", s,
@@ -497,12 +580,12 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
                       balance_join_kernel<16, true><<<n, 1024, 0, s>>>(a, chunk, blocks));
   e = MOE_LAUNCH("balance_join", s, balance_join_kernel<4, false><<<n, 256, 0, s>>>(a, chunk, blocks));
   if (e != hipSuccess) return e;
-  return MOE_LAUNCH("balance_finish", s, balance_finish_kernel<<<1, 64, 0, s>>>(a, blocks));
+  return MOE_LAUNCH("balance_finish", s, balance_finish_kernel<<<1, 1024, 0, s>>>(a, blocks));
 }
 
 hipError_t launch_balance_backward(const BalanceArgs& a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
-  return with_row(a.E, [&](auto row) {
+  return with_row<4>(a.E, [&](auto row) {
     using R = decltype(row);
     const int grid = (a.T + 4 * R::U - 1) / (4 * R::U);
     if (a.sigmoid)
