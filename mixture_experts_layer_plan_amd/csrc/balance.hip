@@ -317,7 +317,7 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(BalanceArgs a) {
   __shared__ float s_p[SMALL_T * SMALL_E];
   __shared__ int32_t s_c[SMALL_COUNTS];
   __shared__ float s_part[SMALL_SEQ];
-  __shared__ int32_t s_seq[SMALL_T], s_tokens[SMALL_SEQ];
+  __shared__ int32_t s_seq[SMALL_T], s_tokens[SMALL_SEQ], s_start[SMALL_SEQ + 1];
   const int wave = threadIdx.x >> 6, lane = lane_id(), w0 = wave * R::U;
   float l[R::U][R::N], p[R::U][R::N], q[R::U][R::N];
   int id[R::U], seq[R::U];
@@ -330,6 +330,11 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(BalanceArgs a) {
     }
   }
   const Sequences seqs(a);
+  const bool one = a.n_seq == 1;
+  if ((int)threadIdx.x <= a.n_seq) {
+    const int v = a.start ? a.start[threadIdx.x] : threadIdx.x ? a.T : 0;
+    s_start[threadIdx.x] = v < 0 ? 0 : v < a.T ? v : a.T;
+  }
   for (int i = threadIdx.x; i < a.n_seq * a.E; i += 1024) s_c[i] = 0;
   if (w0 < a.T) {
     shares<R, SIGMOID>(l, p, q);
@@ -344,9 +349,21 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(BalanceArgs a) {
 #pragma unroll
         for (int j = 0; j < R::N; ++j) p[u][j] = 0.0f;
       }
-      R::store(s_p + (w0 + u) * a.E, a.E, p[u]);
+      if (!one) R::store(s_p + (w0 + u) * a.E, a.E, p[u]);
       if (lane == 0) s_seq[w0 + u] = seq[u];
     }
+  }
+  if (one) {  // one row of sums for each wavefront
+    float acc[R::N];
+#pragma unroll
+    for (int j = 0; j < R::N; ++j) acc[j] = 0.0f;
+#pragma unroll
+    for (int u = 0; u < R::U; ++u) {
+      if (w0 + u >= a.T) break;
+#pragma unroll
+      for (int j = 0; j < R::N; ++j) acc[j] += p[u][j];
+    }
+    R::store(s_p + wave * a.E, a.E, acc);
   }
   lds_barrier();
   if (w0 < a.T) {
@@ -356,16 +373,9 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(BalanceArgs a) {
         atomicAdd(&s_c[seq[u] * a.E + id[u]], 1);
   }
   lds_barrier();
-  const auto range = [&](int i, int* b, int* end) {
-    *b = a.start ? a.start[i] : 0;
-    *end = a.start ? a.start[i + 1] : a.T;
-    *b = *b > 0 ? *b : 0;
-    *end = *end < a.T ? *end : a.T;
-  };
   for (int i = threadIdx.x; i < a.n_seq * a.E; i += 1024) {
     const int sq = i / a.E, e = i - sq * a.E;
-    int b, end;
-    range(sq, &b, &end);
+    const int b = one ? 0 : s_start[sq], end = one ? 16 : s_start[sq + 1];
     float v = 0.0f;
     for (int t = b; t < end; t += 16) {
       float x[16];
@@ -379,8 +389,7 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(BalanceArgs a) {
   }
   lds_barrier();
   for (int i = wave; i < a.n_seq; i += 16) {
-    int b, end;
-    range(i, &b, &end);
+    const int b = s_start[i], end = s_start[i + 1];
     float x = 0.0f;
     int n = 0;
     for (int e = lane; e < a.E; e += 64) x += __int_as_float(s_c[i * a.E + e]);
