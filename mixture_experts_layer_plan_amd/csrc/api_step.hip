@@ -99,7 +99,7 @@ struct BalanceWs {
   size_t seg_p, seg_c, seg_n, part, tokens, ticket, total;
 };
 BalanceWs balance_ws(const moe_shape* s, const moe_balance* b) {
-  const int chunk = balance_chunk(s->E);
+  const int chunk = balance_chunk(s->T, s->E);
   const size_t segs = ((size_t)s->T + chunk - 1) / chunk + b->n_seq;
   Carve c;
   BalanceWs L;

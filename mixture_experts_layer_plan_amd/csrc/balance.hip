@@ -13,6 +13,8 @@
 // last workgroup joining the sequences.  A small batch takes one launch of one workgroup.
 #include <math.h>
 
+#include <algorithm>
+
 #include "common.hpp"
 #include "internal.hpp"
 #include "step.hpp"
@@ -179,51 +181,17 @@ MOE_DEV void shares(const float (&l)[R::U][R::N], float (&p)[R::U][R::N], float 
   }
 }
 
-// The tokens [t0, t1) of a workgroup of W wavefronts, at most W * U: their shares once, then
-// their sums sequence by sequence.  done(seq, n) is called for each sequence with its sums in
-// LDS (s_p: one row of E per wavefront, s_c) and n, the number of its tokens that count, in
-// every thread.
+// The tokens [t0, t1) of a workgroup of W wavefronts, W * U at a time: their shares, summed
+// sequence by sequence.  done(seq, n) is called for each sequence with its sums in LDS (s_p:
+// one row of E per wavefront, s_c) and n, the number of its tokens that count, in every thread.
 template <typename R, bool SIGMOID, int W, typename Done>
 MOE_DEV void walk(const BalanceArgs& a, int t0, int t1, float* s_p, int32_t* s_c, int* s_n, Done done) {
   const int wave = threadIdx.x >> 6, lane = lane_id();
-  const int w0 = t0 + wave * R::U;
-  float l[R::U][R::N], p[R::U][R::N], q[R::U][R::N];
-  int id[R::U];
-#pragma unroll
-  for (int u = 0; u < R::U; ++u) {
-    const int v = w0 + u < t1 ? w0 + u : t1 - 1;
-    id[u] = lane < a.k ? a.idx[(size_t)v * a.k + lane] : -1;
-    R::load(a.logits + (size_t)v * a.E, a.E, -INFINITY, l[u]);
-  }
   const Sequences seqs(a);
-  shares<R, SIGMOID>(l, p, q);
-  int t = t0;
-  while (t < t1) {
-    // the tokens [t, end) that are in t's sequence
-    int end;
-    const int seq = seqs.of(t, &end);
-    if (seq >= a.n_seq) break;               // behind the last one
-    if (end <= t || end > t1) end = t1;      // (entries that do not ascend: no endless loop)
-    if (seq < 0) {                           // before the first sequence
-      t = end;
-      continue;
-    }
-    for (int e = threadIdx.x; e < a.E; e += 64 * W) s_c[e] = 0;
-    lds_barrier();
-    float acc[R::N];
-#pragma unroll
-    for (int j = 0; j < R::N; ++j) acc[j] = 0.0f;
-    int used = 0;
-#pragma unroll
-    for (int u = 0; u < R::U; ++u) {
-      const bool ok = w0 + u >= t && w0 + u < end && (unsigned)id[u] < (unsigned)a.E;
-      if (ok) atomicAdd(&s_c[id[u]], 1);  // whole numbers: any order gives the same
-      if (ballot64(ok)) {
-        ++used;
-#pragma unroll
-        for (int j = 0; j < R::N; ++j) acc[j] += p[u][j];
-      }
-    }
+  float acc[R::N];
+  int used = 0, seq = -1, end = t0;  // the tokens [.., end) are in seq
+  const auto close = [&]() {
+    if (seq < 0) return;
     R::store(s_p + wave * a.E, a.E, acc);
     if (lane == 0) s_n[wave] = used;
     lds_barrier();
@@ -232,8 +200,49 @@ MOE_DEV void walk(const BalanceArgs& a, int t0, int t1, float* s_p, int32_t* s_c
     for (int w = 0; w < W; ++w) n += s_n[w];
     done(seq, n);
     lds_barrier();
-    t = end;
+  };
+  for (int r0 = t0; r0 < t1; r0 += W * R::U) {
+    const int r1 = r0 + W * R::U < t1 ? r0 + W * R::U : t1, w0 = r0 + wave * R::U;
+    float l[R::U][R::N], p[R::U][R::N], q[R::U][R::N];
+    int id[R::U];
+#pragma unroll
+    for (int u = 0; u < R::U; ++u) {
+      const int v = w0 + u < r1 ? w0 + u : r1 - 1;
+      id[u] = lane < a.k ? a.idx[(size_t)v * a.k + lane] : -1;
+      R::load(a.logits + (size_t)v * a.E, a.E, -INFINITY, l[u]);
+    }
+    shares<R, SIGMOID>(l, p, q);
+    for (int t = r0; t < r1;) {
+      if (t >= end) {
+        close();
+        seq = seqs.of(t, &end);
+        if (seq >= a.n_seq) return;          // behind the last one
+        if (end <= t || end > t1) end = t1;  // (entries that do not ascend: no endless loop)
+        if (seq >= 0) {
+          for (int e = threadIdx.x; e < a.E; e += 64 * W) s_c[e] = 0;
+          lds_barrier();
+        }
+        used = 0;
+#pragma unroll
+        for (int j = 0; j < R::N; ++j) acc[j] = 0.0f;
+      }
+      const int stop = end < r1 ? end : r1;
+      if (seq >= 0) {  // (tokens before the first sequence are left out)
+#pragma unroll
+        for (int u = 0; u < R::U; ++u) {
+          const bool ok = w0 + u >= t && w0 + u < stop && (unsigned)id[u] < (unsigned)a.E;
+          if (ok) atomicAdd(&s_c[id[u]], 1);  // whole numbers: any order gives the same
+          if (ballot64(ok)) {
+            ++used;
+#pragma unroll
+            for (int j = 0; j < R::N; ++j) acc[j] += p[u][j];
+          }
+        }
+      }
+      t = stop;
+    }
   }
+  close();
 }
 
 template <int W>
@@ -267,8 +276,7 @@ __global__ __launch_bounds__(64 * PART_W) void balance_part_kernel(BalanceArgs a
 // Sum over W wavefronts in 64 bits, in every thread.
 template <int W>
 MOE_DEV double sum_f64(double v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  v = wave_sum_f64(v);
   if constexpr (W == 1) return v;
   __shared__ double slot[W];
   __syncthreads();
@@ -404,86 +412,93 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(BalanceArgs a) {
   if (wave == 0) finish<1>(a, s_tokens, s_part, 1);
 }
 
-// Adds the segments of sequence blockIdx.x / blocks for JOIN_E experts: lane l the experts
-// l, l + 1, ... of 16, W * 4 rows of lanes every (W * 4)th chunk each.  The last workgroup to
-// finish joins the sequences (TICKET; else balance_finish_kernel does).
+// Adds the segments of sequence x / blocks for JOIN_E experts, for each x < n: 16 lanes an
+// expert each, W * 4 rows of lanes every (W * 4)th chunk each.  With TICKET the grid is n, and
+// the last workgroup to finish joins the sequences; else balance_finish_kernel does.
 constexpr int JOIN_E = 16;
 template <int W, bool TICKET>
-__global__ __launch_bounds__(64 * W) void balance_join_kernel(BalanceArgs a, int chunk, int blocks) {
-  constexpr int G = 4 * W;
+__global__ __launch_bounds__(64 * W) void balance_join_kernel(BalanceArgs a, int chunk, int blocks,
+                                                              int n_all) {
+  constexpr int G = 4 * W, AT = W == 16 ? 8 : 4;  // chunks a thread reads at a time
   __shared__ float s_p[G][JOIN_E];
   __shared__ int s_c[G][JOIN_E], s_n[G];
-  const int seq = blockIdx.x / blocks, blk = blockIdx.x - seq * blocks;
   const int lane = threadIdx.x & (JOIN_E - 1), g = threadIdx.x / JOIN_E;
-  const int e = blk * JOIN_E + lane;
-  int b = a.start ? a.start[seq] : 0, end = a.start ? a.start[seq + 1] : a.T;
-  b = b > 0 ? b : 0;
-  end = end < a.T ? end : a.T;
-  float p = 0.0f;
-  int c = 0, n = 0;
-  if (b < end) {
-    const int c1 = (end - 1) / chunk;
-    const int col = e < a.E ? e : a.E - 1;  // (lanes past the last expert are left out below)
-    for (int i0 = b / chunk + g; i0 <= c1; i0 += 8 * G) {
-      float pv[8];
-      int cv[8], nv[8];
+  for (int x = blockIdx.x; x < n_all; x += gridDim.x) {
+    const int seq = x / blocks, blk = x - seq * blocks;
+    const int e = blk * JOIN_E + lane;
+    int b = a.start ? a.start[seq] : 0, end = a.start ? a.start[seq + 1] : a.T;
+    b = b > 0 ? b : 0;
+    end = end < a.T ? end : a.T;
+    float p = 0.0f;
+    int c = 0, n = 0;
+    if (b < end) {
+      const int c1 = (end - 1) / chunk;
+      const int col = e < a.E ? e : a.E - 1;  // (lanes past the last expert are left out below)
+      for (int i0 = b / chunk + g; i0 <= c1; i0 += AT * G) {
+        float pv[AT];
+        int cv[AT], nv[AT];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {  // all on their way before the first is added
-        const int i = i0 + k * G <= c1 ? i0 + k * G : i0;
-        const size_t seg = (size_t)i + seq;
-        pv[k] = a.seg_p[seg * a.E + col];
-        cv[k] = a.seg_c[seg * a.E + col];
-        nv[k] = a.seg_n[seg];
-      }
+        for (int k = 0; k < AT; ++k) {  // all on their way before the first is added
+          const int i = i0 + k * G <= c1 ? i0 + k * G : i0;
+          const size_t seg = (size_t)i + seq;
+          pv[k] = a.seg_p[seg * a.E + col];
+          cv[k] = a.seg_c[seg * a.E + col];
+          nv[k] = a.seg_n[seg];
+        }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (i0 + k * G <= c1) {
-          p += pv[k];
-          c += cv[k];
-          n += nv[k];
+        for (int k = 0; k < AT; ++k) {
+          if (i0 + k * G <= c1) {
+            p += pv[k];
+            c += cv[k];
+            n += nv[k];
+          }
         }
       }
     }
-  }
-  s_p[g][lane] = p;
-  s_c[g][lane] = c;
-  if (lane == 0) s_n[g] = n;
-  __syncthreads();
-  if (threadIdx.x < 64) {
-    // a quarter of the rows in each 16 lanes, then the quarters
-    const int q = threadIdx.x / JOIN_E;
-    p = s_p[q][lane];
-    c = s_c[q][lane];
-    n = s_n[q];
+    s_p[g][lane] = p;
+    s_c[g][lane] = c;
+    if (lane == 0) s_n[g] = n;
+    lds_barrier();
+    if (threadIdx.x < 64) {
+      // every fourth row in each 16 lanes, then the four
+      const int q = threadIdx.x / JOIN_E;
+      p = s_p[q][lane];
+      c = s_c[q][lane];
+      n = s_n[q];
 #pragma unroll
-    for (int k = 4; k < G; k += 4) {
-      p += s_p[k + q][lane];
-      c += s_c[k + q][lane];
-      n += s_n[k + q];
-    }
-#pragma unroll
-    for (int o = 16; o <= 32; o <<= 1) {
-      p += __shfl_xor(p, o, 64);
-      c += __shfl_xor(c, o, 64);
-      n += __shfl_xor(n, o, 64);
-    }
-    const bool own = e < a.E && q == 0;
-    if (own) a.counts[(size_t)seq * a.E + e] = c;
-    const float x = dpp_sum_f32(own ? p * (float)c : 0.0f);
-    if (threadIdx.x == 0) {
-      a.part[(size_t)seq * blocks + blk] = x;
-      if (blk == 0) a.tokens[seq] = n;
-    }
-    if constexpr (TICKET) {
-      int last = 0;
-      if (threadIdx.x == 0) {
-        __threadfence();
-        last = atomicAdd(a.ticket, 1) == (int)gridDim.x - 1;
+      for (int k = 4; k < G; k += 4) {
+        p += s_p[k + q][lane];
+        c += s_c[k + q][lane];
+        n += s_n[k + q];
       }
-      if (!__builtin_amdgcn_readfirstlane(last)) return;
-      __threadfence();
-      finish<1>(a, a.tokens, a.part, blocks);
+#pragma unroll
+      for (int o = 16; o <= 32; o <<= 1) {
+        p += __shfl_xor(p, o, 64);
+        c += __shfl_xor(c, o, 64);
+        n += __shfl_xor(n, o, 64);
+      }
+      const bool own = e < a.E && q == 0;
+      if (own) a.counts[(size_t)seq * a.E + e] = c;
+      const float sum = dpp_sum_f32(own ? p * (float)c : 0.0f);
+      if (threadIdx.x == 0) {
+        a.part[(size_t)seq * blocks + blk] = sum;
+        if (blk == 0) a.tokens[seq] = n;
+      }
+      if constexpr (TICKET) {
+        int last = 0;
+        if (threadIdx.x == 0) {
+          // the sums are out before the count, and read after the last one is in
+          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+          last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                 (int)gridDim.x - 1;
+        }
+        if (!__builtin_amdgcn_readfirstlane(last)) return;
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+        finish<1>(a, a.tokens, a.part, blocks);
+      }
     }
+    if constexpr (TICKET) return;
+    lds_barrier();
   }
 }
 
@@ -542,25 +557,31 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs a) {
 }
 
 // Calls f with the Row that fits E: past 128 experts four neighbours a lane where rows
-// start at 16 bytes, so that a row is one load or few.  UP: rows at a time of few experts.
-template <int UP, typename F>
+// start at 16 bytes, so that a row is one load or few.  UP, UP4: rows at a time of up to 128
+// and of up to 256 experts.
+template <int UP, int UP4, typename F>
 hipError_t with_row(int E, F f) {
   if (E <= 64) return f(Row<1, UP, false>());
   if (E <= 128) return f(Row<2, UP, false>());
   const bool four = E % 4 == 0;
-  if (E <= 256) return four ? f(Row<4, UP, true>()) : f(Row<4, UP, false>());
+  if (E <= 256) return four ? f(Row<4, UP4, true>()) : f(Row<4, UP4, false>());
   if (E <= 512) return four ? f(Row<8, 2, true>()) : f(Row<8, 2, false>());
   return four ? f(Row<16, 1, true>()) : f(Row<16, 1, false>());
 }
 
 }  // namespace
 
-int balance_chunk(int E) { return PART_W * (E <= 256 ? 4 : E <= 512 ? 2 : 1); }
+// As many tokens as the wavefronts hold at once, or more, so that there are at most 1024
+// chunks to join (262144 x 128: 62 -> 40 us).
+int balance_chunk(int T, int E) {
+  const int once = PART_W * (E <= 256 ? 4 : E <= 512 ? 2 : 1);
+  return once * (int)std::max<int64_t>(1, ((int64_t)T + once * 1024 - 1) / (once * 1024));
+}
 int balance_blocks(int E) { return (E + JOIN_E - 1) / JOIN_E; }
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
   if (is_small(a)) {
-    return with_row<SMALL_T / 16>(a.E, [&](auto row) {
+    return with_row<SMALL_T / 16, SMALL_T / 16>(a.E, [&](auto row) {
       using R = decltype(row);
       if constexpr (R::N > 4) return hipErrorInvalidValue;  // E is at most 256
       else if (a.sigmoid)
@@ -569,11 +590,11 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
         return MOE_LAUNCH("balance_small", s, balance_small_kernel<R, false><<<1, 1024, 0, s>>>(a));
     });
   }
-  const int chunk = balance_chunk(a.E);
+  const int chunk = balance_chunk(a.T, a.E);
   // one workgroup at least: the second launch needs the ticket that the first one clears
   const int grid = a.T > chunk ? (a.T - 1) / chunk + 1 : 1;
   const size_t lds = (size_t)a.E * (PART_W + 1) * 4;
-  hipError_t e = with_row<4>(a.E, [&](auto row) {
+  hipError_t e = with_row<4, 4>(a.E, [&](auto row) {
     using R = decltype(row);
     if (a.sigmoid)
       return MOE_LAUNCH("balance_part", s,
@@ -586,15 +607,19 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
   // few sequences have many chunks each, and few workgroups count themselves out
   if (n <= 256)
     return MOE_LAUNCH("balance_join", s,
-                      balance_join_kernel<16, true><<<n, 1024, 0, s>>>(a, chunk, blocks));
-  e = MOE_LAUNCH("balance_join", s, balance_join_kernel<4, false><<<n, 256, 0, s>>>(a, chunk, blocks));
+                      balance_join_kernel<16, true><<<n, 1024, 0, s>>>(a, chunk, blocks, n));
+  const int most = 1 << 20, groups = n < most ? n : most;
+  e = MOE_LAUNCH("balance_join", s,
+                 balance_join_kernel<4, false><<<groups, 256, 0, s>>>(a, chunk, blocks, n));
   if (e != hipSuccess) return e;
   return MOE_LAUNCH("balance_finish", s, balance_finish_kernel<<<1, 1024, 0, s>>>(a, blocks));
 }
 
 hipError_t launch_balance_backward(const BalanceArgs& a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
-  return with_row<4>(a.E, [&](auto row) {
+  // two rows of 256 leave registers for more wavefronts (32768 x 256: 17.1 -> 14.3 us), four of
+  // 128 fit (262144 x 128: 65 -> 58)
+  return with_row<4, 2>(a.E, [&](auto row) {
     using R = decltype(row);
     const int grid = (a.T + 4 * R::U - 1) / (4 * R::U);
     if (a.sigmoid)

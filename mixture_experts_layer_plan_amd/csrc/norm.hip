@@ -241,7 +241,7 @@ __global__ __launch_bounds__(64 * W) void norm_kernel(NormArgs p) {
     if (i < chunks && p.b) b[c].load(p.b, i);
   }
   int parity = 0;
-  for (int row = blockIdx.x; row < p.T; row += gridDim.x, parity ^= 1) {
+  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, parity ^= 1) {
     const size_t at = (size_t)row * chunks;
     float f[C][8];
     float sum = 0.0f;
@@ -284,8 +284,8 @@ __global__ __launch_bounds__(64 * W) void norm_kernel(NormArgs p) {
     }
     const float rstd = 1.0f / sqrtf(group_sum<W>(sq, s_var[parity]) * inv + p.eps);
     if (threadIdx.x == 0) {
-      p.stats[2 * (size_t)row] = mu;
-      p.stats[2 * (size_t)row + 1] = rstd;
+      p.stats[2 * row] = mu;
+      p.stats[2 * row + 1] = rstd;
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -334,10 +334,10 @@ __global__ __launch_bounds__(64 * W) void norm_backward_kernel(NormBackArgs p) {
     }
   }
   int parity = 0;
-  for (int row = blockIdx.x; row < p.T; row += gridDim.x, parity ^= 1) {
+  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, parity ^= 1) {
     const size_t at = (size_t)row * chunks;
-    const float mu = CENTRE ? p.stats[2 * (size_t)row] : 0.0f;
-    const float rstd = p.stats[2 * (size_t)row + 1];
+    const float mu = CENTRE ? p.stats[2 * row] : 0.0f;
+    const float rstd = p.stats[2 * row + 1];
     Vec8<E> vh[C], vdy[C], vdh[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {

@@ -19,25 +19,6 @@
 namespace moe {
 namespace {
 
-template <int CTRL, int ROWS>
-MOE_DEV double dpp_f64(double old, double v) {
-  const int hi =
-      __builtin_amdgcn_update_dpp(__double2hiint(old), __double2hiint(v), CTRL, ROWS, 0xf, false);
-  const int lo =
-      __builtin_amdgcn_update_dpp(__double2loint(old), __double2loint(v), CTRL, ROWS, 0xf, false);
-  return __hiloint2double(hi, lo);
-}
-MOE_DEV double wave_sum_f64(double v) {
-  v += dpp_f64<0x111, 0xf>(0.0, v);
-  v += dpp_f64<0x112, 0xf>(0.0, v);
-  v += dpp_f64<0x114, 0xf>(0.0, v);
-  v += dpp_f64<0x118, 0xf>(0.0, v);
-  v += dpp_f64<0x142, 0xa>(0.0, v);
-  v += dpp_f64<0x143, 0xc>(0.0, v);
-  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), 63),
-                          __builtin_amdgcn_readlane(__double2loint(v), 63));
-}
-
 // exp(x) for x <= 0 in double, of N values at once (the constants are loaded once):
 // x = n ln 2 + r with |r| <= ln 2 / 2, the Taylor series of exp(r) to r^13 / 13! (the rest
 // is below 2^-57), scaled by 2^n (down to the subnormals).  Below -746, past the smallest

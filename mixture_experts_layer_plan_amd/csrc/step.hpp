@@ -55,8 +55,8 @@ struct BalanceArgs {
   const float* d_in;    // [T, E] or null
   float* d_logits;
 };
-int balance_chunk(int E);   // tokens of a chunk
-int balance_blocks(int E);  // workgroups that add up one sequence
+int balance_chunk(int T, int E);  // tokens of a chunk
+int balance_blocks(int E);        // workgroups that add up one sequence
 hipError_t launch_balance(const BalanceArgs& p, hipStream_t s);
 hipError_t launch_balance_backward(const BalanceArgs& p, hipStream_t s);
 

@@ -53,4 +53,23 @@ MOE_DEV float dpp_sum_f32(float v) {
          (__uint_as_float(lane_u(u, 47)) + __uint_as_float(lane_u(u, 63)));
 }
 
+template <int CTRL, int ROWS>
+MOE_DEV double dpp_f64(double old, double v) {
+  const int hi =
+      __builtin_amdgcn_update_dpp(__double2hiint(old), __double2hiint(v), CTRL, ROWS, 0xf, false);
+  const int lo =
+      __builtin_amdgcn_update_dpp(__double2loint(old), __double2loint(v), CTRL, ROWS, 0xf, false);
+  return __hiloint2double(hi, lo);
+}
+MOE_DEV double wave_sum_f64(double v) {
+  v += dpp_f64<0x111, 0xf>(0.0, v);
+  v += dpp_f64<0x112, 0xf>(0.0, v);
+  v += dpp_f64<0x114, 0xf>(0.0, v);
+  v += dpp_f64<0x118, 0xf>(0.0, v);
+  v += dpp_f64<0x142, 0xa>(0.0, v);
+  v += dpp_f64<0x143, 0xc>(0.0, v);
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), 63),
+                          __builtin_amdgcn_readlane(__double2loint(v), 63));
+}
+
 }  // namespace moe

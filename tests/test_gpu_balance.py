@@ -105,6 +105,35 @@ def test_many_sequences(B):
     verify(B, L, idx, "softmax", 1.0, start)
 
 
+def test_more_sequences_than_one_grid(B):
+    """2^20 sequences of 33 experts, most of them empty: more than a launch of the join takes
+    at once."""
+    say("balance of 2^20 sequences")
+    n = 1 << 20
+    L, idx = inputs(300, 33, 2)
+    start = np.full(n + 1, 300)
+    start[:n - 200] = 0
+    start[n - 200:n] = np.arange(200)      # 199 of one token, the last of 101
+    loss, counts, scales, dL = run(B, L, idx, "softmax", 1.0, start)
+    first = n - 200
+    rl, rc, rs, _ = oracle.balance(L, idx, "softmax", 1.0, start[first:])
+    np.testing.assert_array_equal(np_(counts[first:]), rc)
+    assert not counts[:first].any() and not scales[:first].any()
+    check(scales[first:], rs, 4 * U * rs, "scales")
+    check(loss, np.array([rl]), (share_rel(L) + 161 * U) * rl, "loss")
+    ref = oracle.balance_backward(L, idx, "softmax", 1.0, start[first:])
+    assert np.abs(np_(dL) - ref).max() <= (2 * share_rel(L) + 40 * U) * np.abs(rs).max() * rc.max()
+
+
+@pytest.mark.parametrize("T,E", [(40000, 3), (2100, 1000), (5000, 500)])
+def test_chunks_of_several_rounds(B, T, E):
+    """More tokens than 1024 chunks of one round hold, with sequences that begin inside."""
+    say(f"balance of {T} x {E} in long chunks")
+    L, idx = inputs(T, E, 2, free=0.05)
+    start = [3, 50, T // 3, T // 3 + 1, T - 5]
+    verify(B, L, idx, "sigmoid", 1.0, start)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_no_tokens_or_none_with_an_expert(B, score):
     say("balance without tokens", score)
