@@ -89,6 +89,14 @@ MOE_DEV void decode_m4(uint32_t w, float* f) {
   f[0] = lo.x; f[1] = lo.y; f[2] = hi.x; f[3] = hi.y;
 }
 
+// 16 bytes past the caches: nothing of a step is read again in it (200 million fp32
+// elements: 1098 -> 1030 us, with bf16 copies of masters 1130 -> 1040).
+template <typename V>
+MOE_DEV void store_past(void* p, V v) {
+  static_assert(sizeof(V) == 16, "");
+  __builtin_nontemporal_store(v, (V*)p);
+}
+
 MOE_DEV float round_bf16_at_random(float p, uint32_t r) {
   const uint32_t u = __float_as_uint(p);
   if ((u & 0x7f800000u) == 0x7f800000u) return p;  // inf and NaN as they are
@@ -101,7 +109,7 @@ MOE_DEV void store_bf16_exact(void* p, int64_t i, int cnt, const float* f) {
   for (int j = 0; j < 4; ++j)
     w[j] = __builtin_amdgcn_perm(__float_as_uint(f[2 * j + 1]), __float_as_uint(f[2 * j]), 0x07060302u);
   if (cnt == 8) {
-    *(uint4*)((bf16_t*)p + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    store_past((bf16_t*)p + i, u32x4_t{w[0], w[1], w[2], w[3]});
     return;
   }
 #pragma unroll
@@ -138,10 +146,10 @@ template <bool F32>
 MOE_DEV void store8(void* p, int64_t i, int cnt, const float* f) {
   if (cnt == 8) {
     if (F32) {
-      *(float4*)((float*)p + i) = make_float4(f[0], f[1], f[2], f[3]);
-      *(float4*)((float*)p + i + 4) = make_float4(f[4], f[5], f[6], f[7]);
+      store_past((float*)p + i, f32x4_t{f[0], f[1], f[2], f[3]});
+      store_past((float*)p + i + 4, f32x4_t{f[4], f[5], f[6], f[7]});
     } else {
-      *(uint4*)((bf16_t*)p + i) = cvt8(f);
+      store_past((bf16_t*)p + i, __builtin_bit_cast(u32x4_t, cvt8(f)));
     }
     return;
   }
