@@ -89,11 +89,11 @@ MOE_DEV void decode_m4(uint32_t w, float* f) {
   f[0] = lo.x; f[1] = lo.y; f[2] = hi.x; f[3] = hi.y;
 }
 
-// 16 bytes past the caches: nothing of a step is read again in it (200 million fp32
+typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+// 8 or 16 bytes past the caches: nothing of a step is read again in it (200 million fp32
 // elements: 1098 -> 1030 us, with bf16 copies of masters 1130 -> 1040).
 template <typename V>
 MOE_DEV void store_past(void* p, V v) {
-  static_assert(sizeof(V) == 16, "");
   __builtin_nontemporal_store(v, (V*)p);
 }
 
@@ -102,21 +102,6 @@ MOE_DEV float round_bf16_at_random(float p, uint32_t r) {
   if ((u & 0x7f800000u) == 0x7f800000u) return p;  // inf and NaN as they are
   return __uint_as_float((u + (r & 0xffffu)) & 0xffff0000u);
 }
-// eight values on bf16's grid
-MOE_DEV void store_bf16_exact(void* p, int64_t i, int cnt, const float* f) {
-  uint32_t w[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    w[j] = __builtin_amdgcn_perm(__float_as_uint(f[2 * j + 1]), __float_as_uint(f[2 * j]), 0x07060302u);
-  if (cnt == 8) {
-    store_past((bf16_t*)p + i, u32x4_t{w[0], w[1], w[2], w[3]});
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < cnt) ((bf16_t*)p)[i + j] = (bf16_t)(w[j >> 1] >> (16 * (j & 1)));
-}
-
 MOE_DEV void update_state(float& m, float& v, float& g, const AdamwHyper& h) {
 #pragma clang fp contract(off)
   g = g * h.grad_scale;
@@ -124,41 +109,84 @@ MOE_DEV void update_state(float& m, float& v, float& g, const AdamwHyper& h) {
   v = v * h.beta2 + (g * h.one_minus_beta2) * g;
 }
 
-template <bool F32>
-MOE_DEV void load8(const void* p, int64_t i, int cnt, float* f) {
-  if (cnt == 8) {
-    if (F32) {
-      const float4 a = *(const float4*)((const float*)p + i), b = *(const float4*)((const float*)p + i + 4);
-      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    } else {
+// Eight elements of a thread: a tile's eight neighbours (states of 8 bits, whose blocks of 32
+// are then four lanes), or four of each of its halves, so that the lanes of a 16-byte access
+// of fp32 are neighbours (SPLIT; 5.2 million elements with fp32
+// states: 25.0 -> 23.4 us).
+constexpr int HALF = ADAMW_TILE / 2;
+template <bool SPLIT>
+MOE_DEV constexpr int place(int j) {
+  return SPLIT ? (j >> 2) * HALF + (j & 3) : j;
+}
+// V neighbours; zeros from the end n on
+template <bool F32, int V>
+MOE_DEV void load_some(const void* p, int64_t i, int64_t n, float* f) {
+  if (i + V <= n) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        const float4 a = *(const float4*)((const float*)p + i + j);
+        f[j] = a.x; f[j + 1] = a.y; f[j + 2] = a.z; f[j + 3] = a.w;
+      }
+    } else if constexpr (V == 8) {
       unpack8(*(const uint4*)((const bf16_t*)p + i), f);
+    } else {
+      const uint2 a = *(const uint2*)((const bf16_t*)p + i);
+      f[0] = __uint_as_float(a.x << 16); f[1] = __uint_as_float(a.x & 0xffff0000u);
+      f[2] = __uint_as_float(a.y << 16); f[3] = __uint_as_float(a.y & 0xffff0000u);
     }
     return;
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < V; ++j) {
     f[j] = 0.0f;
-    if (j < cnt) f[j] = F32 ? ((const float*)p)[i + j] : bf16_to_f32(((const bf16_t*)p)[i + j]);
+    if (i + j < n) f[j] = F32 ? ((const float*)p)[i + j] : bf16_to_f32(((const bf16_t*)p)[i + j]);
   }
 }
-template <bool F32>
-MOE_DEV void store8(void* p, int64_t i, int cnt, const float* f) {
-  if (cnt == 8) {
-    if (F32) {
-      store_past((float*)p + i, f32x4_t{f[0], f[1], f[2], f[3]});
-      store_past((float*)p + i + 4, f32x4_t{f[4], f[5], f[6], f[7]});
+// EXACT: the values lie on bf16's grid
+template <bool F32, bool EXACT, int V>
+MOE_DEV void store_some(void* p, int64_t i, int64_t n, const float* f) {
+  uint32_t w[V / 2];
+#pragma unroll
+  for (int j = 0; j < V / 2; ++j)
+    w[j] = EXACT ? __builtin_amdgcn_perm(__float_as_uint(f[2 * j + 1]), __float_as_uint(f[2 * j]), 0x07060302u)
+                 : cvt_bf16x2(f[2 * j], f[2 * j + 1]);
+  if (i + V <= n) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int j = 0; j < V; j += 4)
+        store_past((float*)p + i + j, f32x4_t{f[j], f[j + 1], f[j + 2], f[j + 3]});
+    } else if constexpr (V == 8) {
+      store_past((bf16_t*)p + i, u32x4_t{w[0], w[1], w[2], w[3]});
     } else {
-      store_past((bf16_t*)p + i, __builtin_bit_cast(u32x4_t, cvt8(f)));
+      store_past((bf16_t*)p + i, u32x2_t{w[0], w[1]});
     }
     return;
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (j < cnt) {
+  for (int j = 0; j < V; ++j) {
+    if (i + j < n) {
       if (F32) ((float*)p)[i + j] = f[j];
-      else ((bf16_t*)p)[i + j] = f32_to_bf16(f[j]);
+      else ((bf16_t*)p)[i + j] = (bf16_t)(w[j >> 1] >> (16 * (j & 1)));
     }
+  }
+}
+template <bool F32, bool SPLIT>
+MOE_DEV void load8(const void* p, int64_t i, int64_t n, float* f) {
+  if constexpr (SPLIT) {
+    load_some<F32, 4>(p, i, n, f);
+    load_some<F32, 4>(p, i + HALF, n, f + 4);
+  } else {
+    load_some<F32, 8>(p, i, n, f);
+  }
+}
+template <bool F32, bool EXACT, bool SPLIT>
+MOE_DEV void store8(void* p, int64_t i, int64_t n, const float* f) {
+  if constexpr (SPLIT) {
+    store_some<F32, EXACT, 4>(p, i, n, f);
+    store_some<F32, EXACT, 4>(p, i + HALF, n, f + 4);
+  } else {
+    store_some<F32, EXACT, 8>(p, i, n, f);
   }
 }
 // eight codes; zeros past the end
@@ -208,14 +236,15 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
   // (a tile starts at a multiple of 2^11, so the high word of the place is the tile's)
   const uint32_t key = mix32(mix32((uint32_t)id + 1u) + h.seed) + (uint32_t)(tile0 >> 32) * 0x3C6EF373u;
   {
-    const int64_t i = tile0 + (int)threadIdx.x * 8;
-    const int64_t left = d.n - i;
-    const int cnt = left >= 8 ? 8 : left > 0 ? (int)left : 0;
+    constexpr bool SPLIT = !EIGHT;
+    const int64_t i = tile0 + (int)threadIdx.x * (SPLIT ? 4 : 8), n = d.n;
+    const int64_t left = n - i;
+    const int cnt = left >= 8 ? 8 : left > 0 ? (int)left : 0;  // (of neighbours)
     float g[8], p[8], m[8], v[8];
     uint32_t r[8];
-    load8<G32>(d.grad, i, cnt, g);
-    if (MASTER) load8<true>(d.master, i, cnt, p);
-    else load8<P32>(d.param, i, cnt, p);
+    load8<G32, SPLIT>(d.grad, i, n, g);
+    if (MASTER) load8<true, SPLIT>(d.master, i, n, p);
+    else load8<P32, SPLIT>(d.param, i, n, p);
     if (EIGHT) {
       const uint2 mc = load_codes(d.m, i, cnt), vc = load_codes(d.v, i, cnt);
       const uint32_t me = cnt ? d.m_scale[i >> 5] : 0u, ve = cnt ? d.v_scale[i >> 5] : 0u;
@@ -227,8 +256,8 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
         v[j] = decode_v(((j < 4 ? vc.x : vc.y) >> (8 * (j & 3))) & 255u) * scale_of(ve);
       }
     } else {
-      load8<true>(d.m, i, cnt, m);
-      load8<true>(d.v, i, cnt, v);
+      load8<true, SPLIT>(d.m, i, n, m);
+      load8<true, SPLIT>(d.v, i, n, v);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -236,15 +265,14 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
       // reciprocal and root of one unit: the quotient is far below the weight it is added to
       const float u = m[j] * h.corr1 * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[j] * h.corr2) + h.eps);
       p[j] = fmaf(-h.lr, fmaf(d.weight_decay, p[j], u), p[j]);
-      if (EIGHT || (!P32 && !MASTER)) r[j] = mix32((uint32_t)(i + j) ^ key);
+      if (EIGHT || (!P32 && !MASTER)) r[j] = mix32((uint32_t)(i + place<SPLIT>(j)) ^ key);
     }
-    if (MASTER) store8<true>(d.master_out, i, cnt, p);
+    if (MASTER) store8<true, false, SPLIT>(d.master_out, i, n, p);
     if (!P32 && !MASTER) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) p[j] = round_bf16_at_random(p[j], r[j] ^ (r[j] >> 16));
     }
-    if (!P32 && !MASTER) store_bf16_exact(d.param_out, i, cnt, p);
-    else store8<P32>(d.param_out, i, cnt, p);
+    store8<P32, !P32 && !MASTER, SPLIT>(d.param_out, i, n, p);
     if (EIGHT) {
       uint32_t mt = 0, vt = 0;
 #pragma unroll
@@ -276,8 +304,8 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
         ((uint8_t*)d.v_scale_out)[i >> 5] = (uint8_t)ve;
       }
     } else {
-      store8<true>(d.m_out, i, cnt, m);
-      store8<true>(d.v_out, i, cnt, v);
+      store8<true, false, SPLIT>(d.m_out, i, n, m);
+      store8<true, false, SPLIT>(d.v_out, i, n, v);
     }
   }
 }
@@ -310,7 +338,7 @@ __global__ __launch_bounds__(256) void adamw_values_kernel(int64_t n, const uint
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= s;
     }
-    store8<false>(out, i, cnt, f);
+    store8<false, true, false>(out, i, n, f);
   }
 }
 

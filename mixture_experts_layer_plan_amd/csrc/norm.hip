@@ -20,21 +20,23 @@
 namespace moe {
 namespace {
 
-// Eight neighbouring elements of a row: one 16-byte access in bf16, two in fp32.
-// store_past() writes rows past the caches in bf16, which is faster by itself and with the
-// router projection that reads y behind it (8192 x 7168, both: 145 -> 136 us); in fp32, whose
-// accesses are halves of 32 bytes, it is slower (32768 x 512: 41 -> 48).  keep() is
-// no instruction: the compiler takes the values as new ones, so that it unpacks them again
-// behind it and does not hold them unpacked over a barrier.
+// Eight elements of a row of `chunks` such eights that starts at eight `at`, in 16-byte
+// accesses whose lanes are neighbours: in bf16 the i-th eight, in fp32 the i-th four of each
+// half of the row (eight neighbours would be
+// halves of 32 bytes: 4096 x 7168, 89.6 -> 67.6 us).  column() is the
+// column of element j.  keep() is no instruction: the compiler takes the values as new ones,
+// so that it unpacks them again behind it and does not hold them unpacked over a barrier.
+// Stores of rows go past the caches, which is faster by itself and with the router projection
+// that reads y behind it (8192 x 7168, both: 145 -> 136 us).
 template <typename E>
 struct Vec8;
 template <>
 struct Vec8<bf16_t> {
   uint4 a;
-  MOE_DEV void load(const void* p, size_t i) { a = ((const uint4*)p)[i]; }
-  MOE_DEV void store(void* p, size_t i) const { ((uint4*)p)[i] = a; }
-  MOE_DEV void store_past(void* p, size_t i) const {
-    __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, a), (u32x4_t*)p + i);
+  MOE_DEV static int column(int i, int j, int) { return 8 * i + j; }
+  MOE_DEV void load(const void* p, size_t at, int i, int) { a = ((const uint4*)p)[at + i]; }
+  MOE_DEV void store(void* p, size_t at, int i, int) const {
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, a), (u32x4_t*)p + at + i);
   }
   MOE_DEV void get(float* f) const { unpack8(a, f); }
   MOE_DEV void keep() { asm volatile("" : "+v"(a.x), "+v"(a.y), "+v"(a.z), "+v"(a.w)); }
@@ -43,15 +45,17 @@ struct Vec8<bf16_t> {
 template <>
 struct Vec8<float> {
   float4 a, b;
-  MOE_DEV void load(const void* p, size_t i) {
-    a = ((const float4*)p)[2 * i];
-    b = ((const float4*)p)[2 * i + 1];
+  MOE_DEV static int column(int i, int j, int chunks) {
+    return 4 * (j < 4 ? i : chunks + i) + (j & 3);
   }
-  MOE_DEV void store(void* p, size_t i) const {
-    ((float4*)p)[2 * i] = a;
-    ((float4*)p)[2 * i + 1] = b;
+  MOE_DEV void load(const void* p, size_t at, int i, int chunks) {
+    a = ((const float4*)p)[2 * at + i];
+    b = ((const float4*)p)[2 * at + chunks + i];
   }
-  MOE_DEV void store_past(void* p, size_t i) const { store(p, i); }
+  MOE_DEV void store(void* p, size_t at, int i, int chunks) const {
+    __builtin_nontemporal_store(__builtin_bit_cast(f32x4_t, a), (f32x4_t*)p + 2 * at + i);
+    __builtin_nontemporal_store(__builtin_bit_cast(f32x4_t, b), (f32x4_t*)p + 2 * at + chunks + i);
+  }
   MOE_DEV void get(float* f) const {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
@@ -64,6 +68,13 @@ struct Vec8<float> {
     b = make_float4(f[4], f[5], f[6], f[7]);
   }
 };
+// Eight sums of a thread's columns, to a row of sums that a second launch reads.
+template <typename E>
+MOE_DEV void store_sums(float* row, int i, int chunks, const float* f) {
+  const float4 a = make_float4(f[0], f[1], f[2], f[3]), b = make_float4(f[4], f[5], f[6], f[7]);
+  *(float4*)(row + Vec8<E>::column(i, 0, chunks)) = a;
+  *(float4*)(row + Vec8<E>::column(i, 4, chunks)) = b;
+}
 
 // The sum of v over the workgroup, in every thread; `slot` is W floats of LDS that no
 // wavefront reads any more (two calls on one slot have another call between them).
@@ -102,24 +113,24 @@ __global__ __launch_bounds__(256) void norm_short_kernel(NormArgs p) {
     bf[j] = 0.0f;
   }
   Vec8<E> v;
-  if (on && p.w) v.load(p.w, i), v.get(wf);
-  if (on && p.b) v.load(p.b, i), v.get(bf);
+  if (on && p.w) v.load(p.w, 0, i, chunks), v.get(wf);
+  if (on && p.b) v.load(p.b, 0, i, chunks), v.get(bf);
   for (int64_t row = (int64_t)blockIdx.x * ROWS + slot; row < p.T; row += (int64_t)gridDim.x * ROWS) {
-    const size_t at = (size_t)row * chunks + i;
+    const size_t at = (size_t)row * chunks;
     float f[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = 0.0f;
     if (on) {
-      v.load(p.x, at);
+      v.load(p.x, at, i, chunks);
       v.get(f);
       if (p.res) {
         float r[8];
-        v.load(p.res, at);
+        v.load(p.res, at, i, chunks);
         v.get(r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] += r[j];
         v.set(f);
-        v.store_past(p.h, at);
+        v.store(p.h, at, i, chunks);
         v.get(f);  // the norm is that of h as it is kept: the backward reads it
       }
     }
@@ -143,7 +154,7 @@ __global__ __launch_bounds__(256) void norm_short_kernel(NormArgs p) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * wf[j] + bf[j];
       v.set(f);
-      v.store_past(p.y, at);
+      v.store(p.y, at, i, chunks);
     }
   }
 }
@@ -171,9 +182,9 @@ __global__ __launch_bounds__(256) void norm_short_backward_kernel(NormBackArgs p
     dw[j] = db[j] = 0.0f;
   }
   Vec8<E> v;
-  if (on && p.w) v.load(p.w, i), v.get(wf);
+  if (on && p.w) v.load(p.w, 0, i, chunks), v.get(wf);
   for (int64_t row = (int64_t)blockIdx.x * ROWS + slot; row < p.T; row += (int64_t)gridDim.x * ROWS) {
-    const size_t at = (size_t)row * chunks + i;
+    const size_t at = (size_t)row * chunks;
     const float2 st = *(const float2*)(p.stats + 2 * row);
     const float mu = CENTRE ? st.x : 0.0f, rstd = st.y;
     float x[8], g[8], d[8];
@@ -182,9 +193,9 @@ __global__ __launch_bounds__(256) void norm_short_backward_kernel(NormBackArgs p
     float sg = 0.0f, sgx = 0.0f;
     if (on) {
       Vec8<E> vg, vd;
-      v.load(p.h, at);
-      vg.load(p.dy, at);
-      if (p.dh) vd.load(p.dh, at);
+      v.load(p.h, at, i, chunks);
+      vg.load(p.dy, at, i, chunks);
+      if (p.dh) vd.load(p.dh, at, i, chunks);
       v.get(x);
       vg.get(g);
       if (p.dh) vd.get(d);
@@ -204,7 +215,7 @@ __global__ __launch_bounds__(256) void norm_short_backward_kernel(NormBackArgs p
 #pragma unroll
       for (int j = 0; j < 8; ++j) d[j] += rstd * (g[j] - mg - x[j] * mgx);
       v.set(d);
-      v.store_past(p.dx, at);
+      v.store(p.dx, at, i, chunks);
     }
   }
   if (!p.dw && !p.db) return;
@@ -228,9 +239,10 @@ __global__ __launch_bounds__(256) void norm_short_backward_kernel(NormBackArgs p
   __syncthreads();
   float* out = p.parts + (size_t)blockIdx.x * 2 * p.H;
   for (int c = threadIdx.x; c < 2 * p.H; c += 256) {
-    const int k = c >= p.H, e = c - k * p.H, at = (e & 7) * L + (e >> 3);
+    const int k = c >= p.H, x = c - k * p.H, j = x / chunks, col = x - j * chunks, at = j * L + col;
+    const int e = Vec8<E>::column(col, j, chunks);
     const float t = (s_sum[0][k][at] + s_sum[1][k][at]) + (s_sum[2][k][at] + s_sum[3][k][at]);
-    if (!alone()) out[c] = t;
+    if (!alone()) out[k * p.H + e] = t;
     else if (k ? p.db : p.dw) store_one<E>(k ? p.db : p.dw, e, t);
   }
 }
@@ -244,8 +256,8 @@ __global__ __launch_bounds__(64 * W) void norm_kernel(NormArgs p) {
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int i = c * 64 * W + (int)threadIdx.x;
-    if (i < chunks && p.w) w[c].load(p.w, i);
-    if (i < chunks && p.b) b[c].load(p.b, i);
+    if (i < chunks && p.w) w[c].load(p.w, 0, i, chunks);
+    if (i < chunks && p.b) b[c].load(p.b, 0, i, chunks);
   }
   int parity = 0;
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, parity ^= 1) {
@@ -259,17 +271,17 @@ __global__ __launch_bounds__(64 * W) void norm_kernel(NormArgs p) {
       for (int j = 0; j < 8; ++j) f[c][j] = 0.0f;
       if (i < chunks) {
         Vec8<E> x;
-        x.load(p.x, at + i);
+        x.load(p.x, at, i, chunks);
         x.get(f[c]);
         if (p.res) {
           float r[8];
           Vec8<E> v;
-          v.load(p.res, at + i);
+          v.load(p.res, at, i, chunks);
           v.get(r);
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[c][j] += r[j];
           v.set(f[c]);
-          v.store_past(p.h, at + i);
+          v.store(p.h, at, i, chunks);
           v.get(f[c]);  // the norm is that of h as it is kept: the backward reads it
         }
       }
@@ -309,7 +321,7 @@ __global__ __launch_bounds__(64 * W) void norm_kernel(NormArgs p) {
         }
         Vec8<E> y;
         y.set(f[c]);
-        y.store_past(p.y, at + i);
+        y.store(p.y, at, i, chunks);
       }
     }
   }
@@ -329,7 +341,7 @@ __global__ __launch_bounds__(64 * W) void norm_backward_kernel(NormBackArgs p) {
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int i = c * NT + (int)threadIdx.x;
-    if (!IN_LDS && i < chunks && p.w) w[c].load(p.w, i);
+    if (!IN_LDS && i < chunks && p.w) w[c].load(p.w, 0, i, chunks);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (IN_LDS) {
@@ -350,14 +362,14 @@ __global__ __launch_bounds__(64 * W) void norm_backward_kernel(NormBackArgs p) {
     for (int c = 0; c < C; ++c) {
       const int i = c * NT + (int)threadIdx.x;
       if (i < chunks) {
-        vh[c].load(p.h, at + i);
-        vdy[c].load(p.dy, at + i);
+        vh[c].load(p.h, at, i, chunks);
+        vdy[c].load(p.dy, at, i, chunks);
       }
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = c * NT + (int)threadIdx.x;
-      if (!IN_LDS && i < chunks && p.dh) vdh[c].load(p.dh, at + i);
+      if (!IN_LDS && i < chunks && p.dh) vdh[c].load(p.dh, at, i, chunks);
     }
     float sg = 0.0f, sgx = 0.0f;
 #pragma unroll
@@ -367,7 +379,7 @@ __global__ __launch_bounds__(64 * W) void norm_backward_kernel(NormBackArgs p) {
         float x[8], g[8], wf[8];
         vh[c].get(x);
         vdy[c].get(g);
-        if (IN_LDS && p.w) w[c].load(p.w, i);
+        if (IN_LDS && p.w) w[c].load(p.w, 0, i, chunks);
         if (p.w) w[c].get(wf);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -397,8 +409,8 @@ __global__ __launch_bounds__(64 * W) void norm_backward_kernel(NormBackArgs p) {
         float x[8], g[8], wf[8], d[8];
         vh[c].get(x);
         vdy[c].get(g);
-        if (IN_LDS && p.w) w[c].load(p.w, i);
-        if (IN_LDS && p.dh) vdh[c].load(p.dh, at + i);
+        if (IN_LDS && p.w) w[c].load(p.w, 0, i, chunks);
+        if (IN_LDS && p.dh) vdh[c].load(p.dh, at, i, chunks);
         if (p.w) w[c].get(wf);
         if (p.dh) vdh[c].get(d);
 #pragma unroll
@@ -410,7 +422,7 @@ __global__ __launch_bounds__(64 * W) void norm_backward_kernel(NormBackArgs p) {
         }
         Vec8<E> v;
         v.set(d);
-        v.store_past(p.dx, at + i);
+        v.store(p.dx, at, i, chunks);
       }
     }
   }
@@ -429,15 +441,12 @@ __global__ __launch_bounds__(64 * W) void norm_backward_kernel(NormBackArgs p) {
       }
       if (alone()) {
         Vec8<E> v;
-        if (p.dw) v.set(dw[c]), v.store(p.dw, i);
-        if (p.db) v.set(db[c]), v.store(p.db, i);
+        if (p.dw) v.set(dw[c]), v.store(p.dw, 0, i, chunks);
+        if (p.db) v.set(db[c]), v.store(p.db, 0, i, chunks);
         continue;
       }
-      Vec8<float> v;
-      v.set(dw[c]);
-      v.store(out, i);
-      v.set(db[c]);
-      v.store(out + p.H, i);
+      store_sums<E>(out, i, chunks, dw[c]);
+      store_sums<E>(out + p.H, i, chunks, db[c]);
     }
   }
 }
