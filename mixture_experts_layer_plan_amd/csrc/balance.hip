@@ -253,6 +253,9 @@ MOE_DEV float rows_sum(const float* s_p, int E, int e) {
   return v;
 }
 
+// The sums of one chunk, segment by segment.  32768 x 256 sigmoid: 12.6 us, 54 % of vector
+// issue (529 instructions for a wavefront's four rows, 40 of them for each sigmoid) at 2.8 TB/s.
+// Eight wavefronts: 32 tokens a chunk, whose sums are a sixteenth of the logits.
 template <typename R, bool SIGMOID>
 __global__ __launch_bounds__(64 * PART_W) void balance_part_kernel(BalanceArgs a, int chunk) {
   extern __shared__ float s_mem[];
@@ -414,7 +417,10 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(BalanceArgs a) {
 
 // Adds the segments of sequence x / blocks for JOIN_E experts, for each x < n: 16 lanes an
 // expert each, W * 4 rows of lanes every (W * 4)th chunk each.  With TICKET the grid is n, and
-// the last workgroup to finish joins the sequences; else balance_finish_kernel does.
+// the last workgroup to finish joins the sequences; else balance_finish_kernel does.  Bound by
+// waits: for sums that other dies wrote, for the count of finished workgroups, for the
+// sequences' sums (5 to 8 us; a launch of its own for the last step takes as long, and 4 us of
+// the host).
 constexpr int JOIN_E = 16;
 template <int W, bool TICKET>
 __global__ __launch_bounds__(64 * W) void balance_join_kernel(BalanceArgs a, int chunk, int blocks,
@@ -506,6 +512,9 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a, int
   finish<16>(a, a.tokens, a.part, blocks);
 }
 
+// U tokens a wavefront, nothing shared: the shares again (cheaper than 4 bytes a logit each
+// way), the counts of the sequence from cache.  32768 x 256 sigmoid: 14.3 us, 62 % of vector
+// issue, 4.6 TB/s of logits and gradients.
 template <typename R, bool SIGMOID>
 __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs a) {
   const int t0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * R::U;
