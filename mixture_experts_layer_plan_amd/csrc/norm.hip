@@ -90,6 +90,65 @@ MOE_DEV float group_sum(float v, float* slot) {
   return t;
 }
 
+// dw and db of eight chunks of columns over all rows, by one workgroup of W wavefronts: a lane
+// takes a chunk of every (8 W)th row.  They need h, dy and the forward's stats alone, so that
+// workgroups of this kind run beside those of the rows, in one launch.
+constexpr int COLS = 8;
+template <typename E, int W, bool CENTRE>
+MOE_DEV void column_sums(const NormBackArgs& p, int block) {
+  constexpr int ROWS = 64 * W / COLS, AT = 4;
+  __shared__ float s_sum[W][16][COLS];
+  const int chunks = p.H / 8, lane = threadIdx.x & (COLS - 1), i = block * COLS + lane;
+  const int col = i < chunks ? i : chunks - 1;
+  float sum[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) sum[j] = 0.0f;
+  for (int64_t r0 = threadIdx.x / COLS; r0 < p.T; r0 += AT * ROWS) {
+    Vec8<E> h[AT], dy[AT];
+    float2 st[AT];
+#pragma unroll
+    for (int k = 0; k < AT; ++k) {  // all on their way before the first is used
+      const int64_t row = r0 + k * ROWS < p.T ? r0 + k * ROWS : r0;
+      h[k].load(p.h, (size_t)row * chunks, col, chunks);
+      dy[k].load(p.dy, (size_t)row * chunks, col, chunks);
+      st[k] = *(const float2*)(p.stats + 2 * row);
+    }
+#pragma unroll
+    for (int k = 0; k < AT; ++k) {
+      if (r0 + k * ROWS < p.T) {
+        float x[8], g[8];
+        h[k].get(x);
+        dy[k].get(g);
+        const float mu = CENTRE ? st[k].x : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          sum[j] = fmaf(g[j], (x[j] - mu) * st[k].y, sum[j]);
+          sum[8 + j] += g[j];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int o = COLS; o < 64; o <<= 1) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) sum[j] += __shfl_xor(sum[j], o, 64);
+  }
+  if (lane_id() < COLS) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) s_sum[threadIdx.x >> 6][j][lane] = sum[j];
+  }
+  __syncthreads();
+  if (threadIdx.x >= COLS || i >= chunks) return;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+#pragma unroll
+    for (int w = 1; w < W; ++w) sum[j] += s_sum[w][j][lane];
+  }
+  Vec8<E> v;
+  if (p.dw) v.set(sum), v.store(p.dw, 0, i, chunks);
+  if (p.db) v.set(sum + 8), v.store(p.db, 0, i, chunks);
+}
+
 // The sum of v over L neighbouring lanes, in each of them.
 template <int L>
 MOE_DEV float lanes_sum(float v) {
@@ -161,17 +220,9 @@ __global__ __launch_bounds__(256) void norm_short_kernel(NormArgs p) {
   }
 }
 
-// Whether this launch is one workgroup, which stores dw and db itself: no sums to join.
-MOE_DEV bool alone() { return gridDim.x == 1; }
-
-template <typename E>
-MOE_DEV void store_one(void* p, int i, float v) {
-  if constexpr (sizeof(E) == 2) ((bf16_t*)p)[i] = (bf16_t)cvt_bf16x2(v, v);
-  else ((float*)p)[i] = v;
-}
-
 template <typename E, int L, bool CENTRE>
 __global__ __launch_bounds__(256) void norm_short_backward_kernel(NormBackArgs p) {
+  if ((int)blockIdx.x >= p.groups) return column_sums<E, 4, CENTRE>(p, blockIdx.x - p.groups);
   constexpr int ROWS = 256 / L;
   __shared__ float s_sum[4][2][8 * L];
   const int chunks = p.H / 8, i = threadIdx.x & (L - 1), slot = threadIdx.x / L;
@@ -185,7 +236,7 @@ __global__ __launch_bounds__(256) void norm_short_backward_kernel(NormBackArgs p
   }
   Vec8<E> v;
   if (on && p.w) v.load(p.w, 0, i, chunks), v.get(wf);
-  for (int64_t row = (int64_t)blockIdx.x * ROWS + slot; row < p.T; row += (int64_t)gridDim.x * ROWS) {
+  for (int64_t row = (int64_t)blockIdx.x * ROWS + slot; row < p.T; row += (int64_t)p.groups * ROWS) {
     const size_t at = (size_t)row * chunks;
     const float2 st = *(const float2*)(p.stats + 2 * row);
     const float mu = CENTRE ? st.x : 0.0f, rstd = st.y;
@@ -220,7 +271,7 @@ __global__ __launch_bounds__(256) void norm_short_backward_kernel(NormBackArgs p
       v.store(p.dx, at, i, chunks);
     }
   }
-  if (!p.dw && !p.db) return;
+  if (!p.sums) return;
   // the rows of a wavefront, then the wavefronts
 #pragma unroll
   for (int o = L; o < 64; o <<= 1) {
@@ -243,9 +294,7 @@ __global__ __launch_bounds__(256) void norm_short_backward_kernel(NormBackArgs p
   for (int c = threadIdx.x; c < 2 * p.H; c += 256) {
     const int k = c >= p.H, x = c - k * p.H, j = x / chunks, col = x - j * chunks, at = j * L + col;
     const int e = Vec8<E>::column(col, j, chunks);
-    const float t = (s_sum[0][k][at] + s_sum[1][k][at]) + (s_sum[2][k][at] + s_sum[3][k][at]);
-    if (!alone()) out[k * p.H + e] = t;
-    else if (k ? p.db : p.dw) store_one<E>(k ? p.db : p.dw, e, t);
+    out[k * p.H + e] = (s_sum[0][k][at] + s_sum[1][k][at]) + (s_sum[2][k][at] + s_sum[3][k][at]);
   }
 }
 
@@ -333,12 +382,13 @@ __global__ __launch_bounds__(64 * W) void norm_kernel(NormArgs p) {
   }
 }
 
-// As norm_kernel, over every gridDim.x-th row, with the sums of dw and db of a thread's columns
+// As norm_kernel, over every p.groups-th row, with the sums of dw and db of a thread's columns
 // beside it.  Bound by memory: h, dy, dh and dx once (8192 x 7168 bf16: 500 MB with the sums in
 // 90 us, 5.5 TB/s); rows stay packed over the barrier, so that two workgroups of 512 threads
 // fit a CU (126 registers; unpacked 129, and 121 us).
 template <typename E, int W, int C, bool CENTRE>
 __global__ __launch_bounds__(64 * W) void norm_backward_kernel(NormBackArgs p) {
+  if ((int)blockIdx.x >= p.groups) return column_sums<E, W, CENTRE>(p, blockIdx.x - p.groups);
   // Two chunks of fp32 leave no registers for the sums of dw and db (1024 threads have 128
   // each): they lie in LDS, each thread's own, with lanes side by side.
   constexpr bool IN_LDS = sizeof(E) == 4 && C > 1;
@@ -363,7 +413,7 @@ __global__ __launch_bounds__(64 * W) void norm_backward_kernel(NormBackArgs p) {
     }
   }
   int parity = 0;
-  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, parity ^= 1) {
+  for (int64_t row = blockIdx.x; row < p.T; row += p.groups, parity ^= 1) {
     const size_t at = (size_t)row * chunks;
     const float mu = CENTRE ? p.stats[2 * row] : 0.0f;
     const float rstd = p.stats[2 * row + 1];
@@ -436,7 +486,7 @@ __global__ __launch_bounds__(64 * W) void norm_backward_kernel(NormBackArgs p) {
       }
     }
   }
-  if (!p.dw && !p.db) return;
+  if (!p.sums) return;
   float* out = p.parts + (size_t)blockIdx.x * 2 * p.H;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
@@ -448,12 +498,6 @@ __global__ __launch_bounds__(64 * W) void norm_backward_kernel(NormBackArgs p) {
           dw[c][j] = s_acc[(c * 8 + j) * NT + threadIdx.x];
           db[c][j] = s_acc[((C + c) * 8 + j) * NT + threadIdx.x];
         }
-      }
-      if (alone()) {
-        Vec8<E> v;
-        if (p.dw) v.set(dw[c]), v.store(p.dw, 0, i, chunks);
-        if (p.db) v.set(db[c]), v.store(p.db, 0, i, chunks);
-        continue;
       }
       store_sums<E>(out, i, chunks, dw[c]);
       store_sums<E>(out + p.H, i, chunks, db[c]);
@@ -545,6 +589,17 @@ hipError_t with_waves(int H, F f) {
   return f(Int<16>(), Int<2>());
 }
 
+// Whether the sums of dw and db are taken by workgroups of their own beside the rows', which
+// read h and dy again but need no second launch: up to 1 KB of a column (256 x 7168: bf16 14.5
+// -> 6.8 us, fp32 18.3 -> 9.2; 512 x 4096: 11.5 -> 8.0 and, left as it is, 12.0 -> 14.3).
+bool norm_columns_beside(const NormBackArgs& p, int esize) {
+  return (p.dw || p.db) && p.T > 0 && (int64_t)p.T * esize <= 1024;
+}
+// Their workgroups where they leave no sums.
+int norm_rows_alone(int T, int H) {
+  return H <= SHORT_H ? (T + 256 / lanes_of(H) - 1) / (256 / lanes_of(H)) : T;
+}
+
 template <typename E, bool CENTRE>
 hipError_t norm_of(const NormArgs& p, hipStream_t s) {
   if (p.H <= SHORT_H)
@@ -565,54 +620,53 @@ hipError_t norm_of(const NormArgs& p, hipStream_t s) {
   return with_waves(p.H, launch);
 }
 template <typename E, bool CENTRE>
-hipError_t norm_back_of(const NormBackArgs& p, hipStream_t s) {
-  const int grid = norm_groups(p.T, p.H);
+hipError_t norm_back_launch(const NormBackArgs& p, int grid, hipStream_t s) {
+  if (p.H <= SHORT_H)
+    return with_lanes(p.H, [&](auto l) {
+      constexpr int L = decltype(l)::value;
+      return MOE_LAUNCH("norm_backward", s,
+                        norm_short_backward_kernel<E, L, CENTRE><<<grid, 256, 0, s>>>(p));
+    });
+  return with_waves(p.H, [&](auto w, auto c) {
+    constexpr int W = decltype(w)::value, C = decltype(c)::value;
+    return MOE_LAUNCH("norm_backward", s,
+                      norm_backward_kernel<E, W, C, CENTRE><<<grid, 64 * W, 0, s>>>(p));
+  });
+}
+template <typename E, bool CENTRE>
+hipError_t norm_back_of(NormBackArgs p, hipStream_t s) {
+  const bool beside = norm_columns_beside(p, sizeof(E));
+  const int groups = beside ? norm_rows_alone(p.T, p.H) : norm_groups(p.T, p.H);
+  int columns = beside ? (p.H / 8 + COLS - 1) / COLS : 0;
+  p.sums = (p.dw || p.db) && !beside;
+  if (columns && p.dx == p.dy) {  // dy is overwritten: the columns first, with the same sums
+    p.groups = 0;
+    const hipError_t e = norm_back_launch<E, CENTRE>(p, columns, s);
+    if (e != hipSuccess) return e;
+    columns = 0;
+  }
+  p.groups = groups;
   if (p.T > 0) {
-    const hipError_t e =
-        p.H <= SHORT_H
-            ? with_lanes(p.H,
-                         [&](auto l) {
-                           constexpr int L = decltype(l)::value;
-                           return MOE_LAUNCH("norm_backward", s,
-                                             norm_short_backward_kernel<E, L, CENTRE>
-                                             <<<grid, 256, 0, s>>>(p));
-                         })
-            : with_waves(p.H, [&](auto w, auto c) {
-                constexpr int W = decltype(w)::value, C = decltype(c)::value;
-                return MOE_LAUNCH("norm_backward", s,
-                                  norm_backward_kernel<E, W, C, CENTRE><<<grid, 64 * W, 0, s>>>(p));
-              });
+    const hipError_t e = norm_back_launch<E, CENTRE>(p, groups + columns, s);
     if (e != hipSuccess) return e;
   }
-  if ((!p.dw && !p.db) || grid == 1) return hipSuccess;
+  if (!p.sums) return hipSuccess;
   if (2 * p.H < 4096)
     return MOE_LAUNCH("norm_wgrad", s,
-                      norm_wgrad_kernel<E, 4><<<(2 * p.H + 15) / 16, 256, 0, s>>>(p, grid));
+                      norm_wgrad_kernel<E, 4><<<(2 * p.H + 15) / 16, 256, 0, s>>>(p, p.groups));
   return MOE_LAUNCH("norm_wgrad", s,
-                    norm_wgrad_kernel<E, 16><<<(2 * p.H + 63) / 64, 256, 0, s>>>(p, grid));
+                    norm_wgrad_kernel<E, 16><<<(2 * p.H + 63) / 64, 256, 0, s>>>(p, p.groups));
 }
 
 }  // namespace
 
-// Workgroups of the backward: each leaves a row of sums, so that there are no more than fill
-// the card, and several rows for each.  Few rows take one workgroup, one after the other,
-// whose sums need no second launch (4 rows of 7168: 11.4 -> 8.5 us, but 8 of them 15; 256 of
-// 48: 11.2 -> 7.3).
+// Workgroups of the backward's rows: each leaves a row of sums, so that there are no more
+// than fill the card, and several rows for each.
 int norm_groups(int T, int H) {
-  int most, rows, few;
-  if (H <= SHORT_H) {
-    const int pass = 256 / lanes_of(H);
-    most = 1024;
-    rows = 2 * pass;
-    few = 8 * pass;
-  } else {
-    most = 4096 / waves_of(H);
-    rows = 4;
-    few = 4;
-  }
-  if (T > 0 && T <= few) return 1;
-  const int want = (int)(((int64_t)T + rows - 1) / rows);
-  return want < most ? want : most;
+  const int most = H <= SHORT_H ? 1024 : 4096 / waves_of(H);
+  const int rows = H <= SHORT_H ? 2 * 256 / lanes_of(H) : 4;
+  const int64_t want = ((int64_t)T + rows - 1) / rows;
+  return want < most ? (int)want : most;
 }
 
 hipError_t launch_norm(const NormArgs& p, bool f32, bool centre, hipStream_t s) {

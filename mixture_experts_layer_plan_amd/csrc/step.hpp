@@ -23,6 +23,10 @@ struct NormBackArgs {
   void *dx, *dw, *db;  // dw, db may be null
   float* parts;        // [groups][2][H]: sums of dw and db over each workgroup's rows
   int T, H;
+  // set by the launch: workgroups of rows (those behind them take columns), and whether they
+  // leave sums of dw and db
+  int groups;
+  bool sums;
 };
 constexpr int NORM_MAX_H = 16384;
 int norm_groups(int T, int H);  // workgroups of the backward: from the sizes alone

@@ -61,8 +61,9 @@ def norm_back_bounds(h, w, dy, dh, xh, rstd, kind):
     dx = rstd * (U * g + e_mg + e * (gx + e_mgx) + ax * e_mgx + (rel + 6 * U) * terms)
     if dh is not None:
         dx = dx + 2 * U * np.abs(f64(dh))
-    # rows of a workgroup one after the other, workgroups by sixteenths: at most 128 + T / 16
-    depth = (128 + T / 16) * U
+    # rows of a workgroup one after the other and workgroups by sixteenths, or every 8th row or
+    # more in a thread: at most 128 + T / 8
+    depth = (128 + T / 8) * U
     return dx, (np.abs(dy) * e).sum(0) + depth * (np.abs(dy) * ax).sum(0), depth * np.abs(dy).sum(0)
 
 

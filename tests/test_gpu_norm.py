@@ -143,10 +143,23 @@ def test_a_row_that_is_not_finite_stays_alone(B):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(255, 104), (256, 1032), (257, 1032), (512, 520), (513, 520), (300, 7168),
+                                 (600, 16), (256, 16384), (2100, 2056)])
+def test_batches_at_the_borders_of_the_backwards_forms(B, T, H, dtype):
+    """Column sums beside the rows, joined by a second launch, and both row lengths."""
+    say(f"norm forms {dtype} T={T} H={H}")
+    i = inputs(T, H, dtype, True)
+    o = run(B, i, dtype)
+    verify(i, o, dtype)
+    half = run(B, i, dtype, grads=(False, True))
+    assert torch.equal(half["db"], o["db"]) and torch.equal(half["dx"], o["dx"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_in_place(B, dtype):
     """h over x, y over residual, dx over dy and over dh_in."""
     say("norm in place", dtype)
-    for T, H in ((37, 2048), (3000, 64)):
+    for T, H in ((37, 2048), (3000, 64), (200, 256), (700, 1024)):
         i = inputs(T, H, dtype, True)
         ref = run(B, i, dtype)
         f, b = calls(B, dtype)
