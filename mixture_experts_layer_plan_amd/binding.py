@@ -227,12 +227,15 @@ def _bf16(t, numel=None):
 # The current stream's handle without building a torch.cuda.Stream (0.1 us against 2.7):
 # what a call of a few microseconds on the GPU is measured by.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# And the current device without torch.cuda's check that it has been started (0.06 us against
+# 0.25): a device tensor among the arguments has started it.
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_raw_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -475,7 +478,7 @@ def _ws(t, dev):
 
 
 def _dev():
-    return torch.cuda.current_device()
+    return _raw_device()
 
 
 @functools.lru_cache(maxsize=256)
