@@ -672,18 +672,21 @@ def moe_adamw_table(s, tensors, table, stream=None):
         kinds["master"] = _F32
     if s.state_bits == 8:
         kinds["m_scale"] = kinds["v_scale"] = torch.uint8
+    places = [(k, k + "_out", dt, k.endswith("scale")) for k, dt in kinds.items()]
+    known = {"grad", "weight_decay"}.union(*(p[:2] for p in places))
     arr = (moe_adamw_tensor * s.n_tensors)()
     for a, t in zip(arr, tensors):
-        unknown = set(t) - {"grad", "weight_decay"} - set(kinds) - {k + "_out" for k in kinds}
-        if unknown:
-            raise ValueError(f"no place for {sorted(unknown)} in this shape")
-        a.n = n = t["grad"].numel()
+        if not t.keys() <= known:
+            raise ValueError(f"no place for {sorted(t.keys() - known)} in this shape")
+        grad = t["grad"]
+        a.n = n = grad.numel()
         a.weight_decay = t.get("weight_decay", 0.0)
-        a.grad = _here(t["grad"], types[s.g_type], n, d)
-        for k, dt in kinds.items():
-            m = (n + 31) // 32 if k.endswith("scale") else n
-            setattr(a, k, _here(t[k], dt, m, d))
-            setattr(a, k + "_out", _here(t.get(k + "_out", t[k]), dt, m, d))
+        a.grad = _here(grad, types[s.g_type], n, d)
+        for k, k_out, dt, by_block in places:
+            m = (n + 31) // 32 if by_block else n
+            own = _here(t[k], dt, m, d)
+            setattr(a, k, own)
+            setattr(a, k_out, _here(t[k_out], dt, m, d) if k_out in t else own)
     _call("moe_adamw_table", ctypes.byref(s), arr, _buf(table, moe_adamw_table_bytes(s), d),
           _stream(stream))
 

@@ -240,78 +240,76 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
   if (tile0 >= d.n) return;  // the grid is an upper bound
   // (a tile starts at a multiple of 2^11, so the high word of the place is the tile's)
   const uint32_t key = mix32(mix32((uint32_t)id + 1u) + h.seed) + (uint32_t)(tile0 >> 32) * 0x3C6EF373u;
-  {
-    constexpr bool SPLIT = !EIGHT;
-    const int64_t i = tile0 + (int)threadIdx.x * (SPLIT ? 4 : 8), n = d.n;
-    const int64_t left = n - i;
-    const int cnt = left >= 8 ? 8 : left > 0 ? (int)left : 0;  // (of neighbours)
-    float g[8], p[8], m[8], v[8];
-    uint32_t r[8];
-    load8<G32, SPLIT>(d.grad, i, n, g);
-    if (MASTER) load8<true, SPLIT>(d.master, i, n, p);
-    else load8<P32, SPLIT>(d.param, i, n, p);
-    if (EIGHT) {
-      const uint2 mc = load_codes(d.m, i, cnt), vc = load_codes(d.v, i, cnt);
-      const uint32_t me = cnt ? d.m_scale[i >> 5] : 0u, ve = cnt ? d.v_scale[i >> 5] : 0u;
-      decode_m4(mc.x, m);
-      decode_m4(mc.y, m + 4);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m[j] *= scale_of(me);
-        v[j] = decode_v(((j < 4 ? vc.x : vc.y) >> (8 * (j & 3))) & 255u) * scale_of(ve);
-      }
-    } else {
-      load8<true, SPLIT>(d.m, i, n, m);
-      load8<true, SPLIT>(d.v, i, n, v);
-    }
+  constexpr bool SPLIT = !EIGHT;
+  const int64_t i = tile0 + (int)threadIdx.x * (SPLIT ? 4 : 8), n = d.n;
+  const int64_t left = n - i;
+  const int cnt = left >= 8 ? 8 : left > 0 ? (int)left : 0;  // (of neighbours)
+  float g[8], p[8], m[8], v[8];
+  uint32_t r[8];
+  load8<G32, SPLIT>(d.grad, i, n, g);
+  if (MASTER) load8<true, SPLIT>(d.master, i, n, p);
+  else load8<P32, SPLIT>(d.param, i, n, p);
+  if (EIGHT) {
+    const uint2 mc = load_codes(d.m, i, cnt), vc = load_codes(d.v, i, cnt);
+    const uint32_t me = cnt ? d.m_scale[i >> 5] : 0u, ve = cnt ? d.v_scale[i >> 5] : 0u;
+    decode_m4(mc.x, m);
+    decode_m4(mc.y, m + 4);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      update_state(m[j], v[j], g[j], h);
-      // reciprocal and root of one unit: the quotient is far below the weight it is added to
-      const float u = m[j] * h.corr1 * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[j] * h.corr2) + h.eps);
-      p[j] = fmaf(-h.lr, fmaf(d.weight_decay, p[j], u), p[j]);
-      if (EIGHT || (!P32 && !MASTER)) r[j] = mix32((uint32_t)(i + place<SPLIT>(j)) ^ key);
+      m[j] *= scale_of(me);
+      v[j] = decode_v(((j < 4 ? vc.x : vc.y) >> (8 * (j & 3))) & 255u) * scale_of(ve);
     }
-    if (MASTER) store8<true, false, SPLIT>(d.master_out, i, n, p);
-    if (!P32 && !MASTER) {
+  } else {
+    load8<true, SPLIT>(d.m, i, n, m);
+    load8<true, SPLIT>(d.v, i, n, v);
+  }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) p[j] = round_bf16_at_random(p[j], r[j] ^ (r[j] >> 16));
+  for (int j = 0; j < 8; ++j) {
+    update_state(m[j], v[j], g[j], h);
+    // reciprocal and root of one unit: the quotient is far below the weight it is added to
+    const float u = m[j] * h.corr1 * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[j] * h.corr2) + h.eps);
+    p[j] = fmaf(-h.lr, fmaf(d.weight_decay, p[j], u), p[j]);
+    if (EIGHT || (!P32 && !MASTER)) r[j] = mix32((uint32_t)(i + place<SPLIT>(j)) ^ key);
+  }
+  if (MASTER) store8<true, false, SPLIT>(d.master_out, i, n, p);
+  if (!P32 && !MASTER) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = round_bf16_at_random(p[j], r[j] ^ (r[j] >> 16));
+  }
+  store8<P32, !P32 && !MASTER, SPLIT>(d.param_out, i, n, p);
+  if (EIGHT) {
+    uint32_t mt = 0, vt = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t mu = __float_as_uint(m[j]) & 0x7fffffffu, vu = __float_as_uint(v[j]);
+      mt = mt > mu ? mt : mu;
+      vt = vt > vu ? vt : vu;
     }
-    store8<P32, !P32 && !MASTER, SPLIT>(d.param_out, i, n, p);
-    if (EIGHT) {
-      uint32_t mt = 0, vt = 0;
+    mt = max_of_four_lanes(mt);
+    vt = max_of_four_lanes(vt);
+    const uint32_t me = scale_byte<M_CARRY, M_SHIFT>(mt), ve = scale_byte<V_CARRY, V_SHIFT>(vt);
+    const float mi = inverse_scale(me), vi = inverse_scale(ve);
+    uint32_t mw[2] = {0, 0}, c[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t mu = __float_as_uint(m[j]) & 0x7fffffffu, vu = __float_as_uint(v[j]);
-        mt = mt > mu ? mt : mu;
-        vt = vt > vu ? vt : vu;
-      }
-      mt = max_of_four_lanes(mt);
-      vt = max_of_four_lanes(vt);
-      const uint32_t me = scale_byte<M_CARRY, M_SHIFT>(mt), ve = scale_byte<V_CARRY, V_SHIFT>(vt);
-      const float mi = inverse_scale(me), vi = inverse_scale(ve);
-      uint32_t mw[2] = {0, 0}, c[8];
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        mw[w] = encode_m<0>(m[4 * w], mi, r[4 * w], mw[w]);
-        mw[w] = encode_m<1>(m[4 * w + 1], mi, r[4 * w + 1], mw[w]);
-        mw[w] = encode_m<2>(m[4 * w + 2], mi, r[4 * w + 2], mw[w]);
-        mw[w] = encode_m<3>(m[4 * w + 3], mi, r[4 * w + 3], mw[w]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) c[j] = encode_v(v[j], vi, r[j]);
-      const uint32_t vw[2] = {low_bytes(c[0], c[1], c[2], c[3]), low_bytes(c[4], c[5], c[6], c[7])};
-      // a block that is not finite: codes of zero under a scale of inf, which is NaN
-      store_codes(d.m_out, i, cnt, me == 255u ? make_uint2(0, 0) : make_uint2(mw[0], mw[1]));
-      store_codes(d.v_out, i, cnt, ve == 255u ? make_uint2(0, 0) : make_uint2(vw[0], vw[1]));
-      if (cnt && (threadIdx.x & 3) == 0) {
-        ((uint8_t*)d.m_scale_out)[i >> 5] = (uint8_t)me;
-        ((uint8_t*)d.v_scale_out)[i >> 5] = (uint8_t)ve;
-      }
-    } else {
-      store8<true, false, SPLIT>(d.m_out, i, n, m);
-      store8<true, false, SPLIT>(d.v_out, i, n, v);
+    for (int w = 0; w < 2; ++w) {
+      mw[w] = encode_m<0>(m[4 * w], mi, r[4 * w], mw[w]);
+      mw[w] = encode_m<1>(m[4 * w + 1], mi, r[4 * w + 1], mw[w]);
+      mw[w] = encode_m<2>(m[4 * w + 2], mi, r[4 * w + 2], mw[w]);
+      mw[w] = encode_m<3>(m[4 * w + 3], mi, r[4 * w + 3], mw[w]);
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = encode_v(v[j], vi, r[j]);
+    const uint32_t vw[2] = {low_bytes(c[0], c[1], c[2], c[3]), low_bytes(c[4], c[5], c[6], c[7])};
+    // a block that is not finite: codes of zero under a scale of inf, which is NaN
+    store_codes(d.m_out, i, cnt, me == 255u ? make_uint2(0, 0) : make_uint2(mw[0], mw[1]));
+    store_codes(d.v_out, i, cnt, ve == 255u ? make_uint2(0, 0) : make_uint2(vw[0], vw[1]));
+    if (cnt && (threadIdx.x & 3) == 0) {
+      ((uint8_t*)d.m_scale_out)[i >> 5] = (uint8_t)me;
+      ((uint8_t*)d.v_scale_out)[i >> 5] = (uint8_t)ve;
+    }
+  } else {
+    store8<true, false, SPLIT>(d.m_out, i, n, m);
+    store8<true, false, SPLIT>(d.v_out, i, n, v);
   }
 }
 
@@ -321,7 +319,6 @@ __global__ __launch_bounds__(64) void adamw_table_kernel(AdamwChunk c, AdamwDesc
     desc[c.base + i] = c.d[i];
     first[c.base + i] = c.first[i];
   }
-  if (i == 0 && c.base + c.count == c.n_tensors) first[c.n_tensors] = c.tiles;
 }
 
 // The values that codes stand for, as bf16 (exact: at most 4 significant bits, down to the

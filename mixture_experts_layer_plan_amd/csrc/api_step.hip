@@ -154,7 +154,7 @@ AdamwTable adamw_table(const moe_adamw_shape* s) {
   Carve c;
   AdamwTable L;
   L.desc = c.take((size_t)s->n_tensors * sizeof(AdamwDesc));
-  L.first = c.take(((size_t)s->n_tensors + 1) * sizeof(int32_t));
+  L.first = c.take((size_t)s->n_tensors * sizeof(int32_t));
   L.total = c.off;
   return L;
 }
@@ -334,7 +334,6 @@ moe_status moe_adamw_table(const moe_adamw_shape* s, const moe_adamw_tensor* ten
     memset(&c, 0, sizeof(c));
     c.base = base;
     c.count = std::min(ADAMW_TABLE_CHUNK, s->n_tensors - base);
-    c.n_tensors = s->n_tensors;
     for (int i = 0; i < c.count; ++i) {
       const moe_adamw_tensor& t = tensors[base + i];
       c.d[i] = {t.grad, t.param, t.m, t.v, t.master, t.m_scale, t.v_scale, t.param_out, t.m_out,
@@ -342,7 +341,6 @@ moe_status moe_adamw_table(const moe_adamw_shape* s, const moe_adamw_tensor* ten
       c.first[i] = tiles;
       tiles += (int32_t)adamw_tiles(t.n);
     }
-    c.tiles = tiles;
     MOE_TRY(launch_adamw_table(c, at<AdamwDesc>(table, L.desc), at<int32_t>(table, L.first), st));
   }
   return MOE_OK;

@@ -661,7 +661,8 @@ hipError_t norm_back_of(NormBackArgs p, hipStream_t s) {
 }  // namespace
 
 // Workgroups of the backward's rows: each leaves a row of sums, so that there are no more
-// than fill the card, and several rows for each.
+// than fill the card, and four rows for each (1003 x 2040 in fp32: 12.7 us; two 15.1, eight
+// 14.7).
 int norm_groups(int T, int H) {
   const int most = H <= SHORT_H ? 1024 : 4096 / waves_of(H);
   const int rows = H <= SHORT_H ? 2 * 256 / lanes_of(H) : 4;

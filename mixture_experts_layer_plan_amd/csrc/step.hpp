@@ -82,7 +82,7 @@ constexpr int ADAMW_TABLE_CHUNK = 24;  // tensors that one launch writes into th
 struct AdamwChunk {
   AdamwDesc d[ADAMW_TABLE_CHUNK];
   int32_t first[ADAMW_TABLE_CHUNK];  // first tile of each
-  int32_t base, count, n_tensors, tiles;
+  int32_t base, count;
 };
 struct AdamwHyper {  // = moe_adamw_hyper
   float lr, beta1, one_minus_beta1, beta2, one_minus_beta2, eps, corr1, corr2, grad_scale;
@@ -90,7 +90,7 @@ struct AdamwHyper {  // = moe_adamw_hyper
 };
 struct AdamwArgs {
   const AdamwDesc* desc;
-  const int32_t* first;  // [n_tensors + 1]
+  const int32_t* first;  // [n_tensors]: first tile of each
   int n_tensors;
   int tiles;  // an upper bound
   AdamwHyper hyper;

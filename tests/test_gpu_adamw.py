@@ -338,3 +338,55 @@ def test_elements_past_32_bits(B):
         np.testing.assert_array_equal(np_(t[k][first:]), c)
         np.testing.assert_array_equal(np_(t[k + "_scale"][first // 32:]), sc)
     assert not t["param"][:first:4097].any() and not t["m"][:first:4097].any()
+
+
+def test_copies_of_masters_at_the_ends_of_bf16(B):
+    """Subnormal masters, ties and values past bf16's largest: the conversion is torch's."""
+    say("adamw copies of masters")
+    w = torch.tensor([1e-40, -1e-40, 2.0 ** -133, 1.5 * 2.0 ** -133, 2.0 ** -126, 3.4e38, -3.4e38, 3.3895e38,
+                      1 + 2.0 ** -8, 1 + 3 * 2.0 ** -8, 0.0, -0.0] * 5)
+    n = w.numel()
+    z = dict(dtype=torch.float32)
+    host = [{"grad": torch.zeros(n, dtype=torch.bfloat16), "param": torch.zeros(n, dtype=torch.bfloat16),
+             "master": w, "m": torch.zeros(n, **z), "v": torch.zeros(n, **z), "weight_decay": 0.0}]
+    s, dev, outs, tab, oks = table(B, host, "bf16", "bf16", True, 32)
+    B.moe_adamw_step(s, tab, B.adamw_hyper(1e-3, seed=1))
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0]["master"].cpu(), w)
+    assert torch.equal(outs[0]["param"].cpu().view(torch.int16), w.bfloat16().view(torch.int16))
+
+
+def test_nan_weights_stay_nan(B):
+    """Also those whose bits are all ones, which a rounding by addition would carry to zero."""
+    say("adamw with NaN weights")
+    bits = torch.tensor([0x7FFF, -1, 0x7F81, 0x7FC0, 0x7F80, -0x80] * 8, dtype=torch.int16)
+    n = bits.numel()
+    gbits = torch.tensor([-1, 0x7FFFFFFF, 0x7FC00000] * (n // 3), dtype=torch.int32)
+    for gtype in ("bf16", "f32"):
+        g = torch.zeros(n, dtype=DT[gtype]) if gtype == "bf16" else gbits.view(torch.float32)
+        host = [{"grad": g, "param": bits.view(torch.bfloat16) if gtype == "bf16" else torch.ones(n).bfloat16(),
+                 "m": torch.zeros(n), "v": torch.zeros(n), "weight_decay": 0.0}]
+        for seed in range(4):
+            s, dev, outs, tab, oks = table(B, host, "bf16", gtype, False, 32)
+            B.moe_adamw_step(s, tab, B.adamw_hyper(1e-3, seed=seed))
+            torch.cuda.synchronize()
+            got = outs[0]["param"].cpu()
+            # (an infinite weight becomes one too: weight_decay p is 0 times inf)
+            assert torch.isnan(got).all()
+
+
+def test_two_steps_at_once(B):
+    """Two tables on two streams given by argument: nothing is shared between calls."""
+    say("adamw of two tables at once")
+    hosts = [make([300000], "bf16", "bf16", True, 8, k) for k in (1, 2)]
+    h = B.adamw_hyper(1e-2, seed=4)
+    alone, both = [], []
+    for out, streams in ((alone, [None, None]), (both, [torch.cuda.Stream(), torch.cuda.Stream()])):
+        tabs = [table(B, host, "bf16", "bf16", True, 8) for host in hosts]
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for (s, _, _, tab, _), st in zip(tabs, streams):
+                B.moe_adamw_step(s, tab, h, stream=st)
+        torch.cuda.synchronize()
+        out += [digest(*t[2][0].values()) for t in tabs]
+    assert alone == both

@@ -287,3 +287,49 @@ def test_a_large_batch(B):
     d = sc * p * (c - dot) * (1 - s)
     bound = sc * p * ((tau + 12 * U) * (c - dot).abs() + (tau + 24 * U) * dot)
     assert bool(((dL.double() - d).abs() <= bound + 2 * U * d.abs()).all())
+
+
+def test_the_largest_batch(B):
+    """The last token count that is not refused, of one expert: every share is 1."""
+    say("balance of 2^26 - 4 tokens")
+    T = (1 << 26) - 4
+    s, ba = B.shape(T, 128, 128, 1, 1), B.balance("sigmoid", 0.5, 2)
+    L = torch.randn((T, 1), generator=torch.Generator(device="cuda").manual_seed(0), device="cuda")
+    idx = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, 12345, T - 7], dtype=torch.int32, device="cuda")
+    loss, sc = torch.empty(1, device="cuda"), torch.empty(2, device="cuda")
+    c = torch.empty((2, 1), dtype=torch.int32, device="cuda")
+    ws = torch.empty(B.moe_balance_workspace_bytes(s, ba), dtype=torch.uint8, device="cuda")
+    dL = torch.full((T, 1), 9.0, device="cuda")
+    B.moe_balance_loss(s, ba, L, idx, start, loss, c, sc, ws)
+    B.moe_balance_loss_backward(s, ba, L, idx, start, c, sc, None, None, dL)
+    torch.cuda.synchronize()
+    assert c[:, 0].tolist() == [12345, T - 7 - 12345]
+    # a wavefront adds its 8192 tokens of a chunk one by one, each share within 3 units of 1
+    assert abs(float(loss) - 0.5) <= 0.5 * (8192 + 200) * U
+    # p (c - p c) with p within 3 units of 1
+    assert float(dL.abs().max()) <= float(sc.max()) * T * 8 * U
+
+
+def test_two_batches_at_once(B):
+    """Two workspaces on two streams given by argument."""
+    say("balance of two batches at once")
+    T, E, k = 3000, 60, 4
+    sets = []
+    for seed in (1, 2):
+        L, idx = inputs(T, E, k, seed=seed)
+        want = digest(*run(B, L, idx, "softmax"))
+        s, ba = B.shape(T, 128, 128, E, k), B.balance("softmax", 0.3, 1)
+        o = [torch.empty((1,), device="cuda"), torch.empty((1, E), dtype=torch.int32, device="cuda"),
+             torch.empty((1,), device="cuda"), torch.empty((T, E), device="cuda")]
+        ws = torch.empty(B.moe_balance_workspace_bytes(s, ba), dtype=torch.uint8, device="cuda")
+        sets.append((s, ba, torch.as_tensor(L).cuda(), torch.as_tensor(idx).cuda(), o, ws, want))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for (s, ba, L, idx, o, ws, _), st in zip(sets, streams):
+            B.moe_balance_loss(s, ba, L, idx, None, o[0], o[1], o[2], ws, stream=st)
+            B.moe_balance_loss_backward(s, ba, L, idx, None, o[1], o[2], None, None, o[3], stream=st)
+    torch.cuda.synchronize()
+    for x in sets:
+        assert digest(*x[4]) == x[6]
