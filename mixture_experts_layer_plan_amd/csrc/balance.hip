@@ -318,10 +318,12 @@ MOE_DEV void finish(const BalanceArgs& a, const int32_t* tokens, const float* pa
 }
 
 // A batch of few tokens, whole, in one workgroup of 16 wavefronts: the tokens' shares and the
-// sequences' counts in LDS, then a thread for each (sequence, expert).
+// sequences' counts in LDS, then a thread for each (sequence, expert).  One CU's vector issue
+// sets its limits: 128 tokens of 64 experts take 7.9 us (two launches 8.4), 64 of 256 7.4 (9.2),
+// and 128 of 256 would take 12.
 constexpr int SMALL_T = 128, SMALL_E = 256, SMALL_SEQ = 64, SMALL_COUNTS = 4096;
 bool is_small(const BalanceArgs& a) {
-  return a.T <= SMALL_T && a.E <= SMALL_E && a.n_seq <= SMALL_SEQ && a.n_seq * a.E <= SMALL_COUNTS;
+  return a.T <= (a.E <= 64 ? SMALL_T : SMALL_T / 2) && a.E <= SMALL_E && a.n_seq <= SMALL_SEQ && a.n_seq * a.E <= SMALL_COUNTS;
 }
 template <typename R, bool SIGMOID>
 __global__ __launch_bounds__(1024) void balance_small_kernel(BalanceArgs a) {
@@ -566,14 +568,14 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(BalanceArgs a) {
 }
 
 // Calls f with the Row that fits E: past 128 experts four neighbours a lane where rows
-// start at 16 bytes, so that a row is one load or few.  UP, UP4: rows at a time of up to 128
-// and of up to 256 experts.
-template <int UP, int UP4, typename F>
+// start at 16 bytes, so that a row is one load or few.  U1, U2, U4: rows at a time of up to 64,
+// 128 and 256 experts.
+template <int U1, int U2, int U4, typename F>
 hipError_t with_row(int E, F f) {
-  if (E <= 64) return f(Row<1, UP, false>());
-  if (E <= 128) return f(Row<2, UP, false>());
+  if (E <= 64) return f(Row<1, U1, false>());
+  if (E <= 128) return f(Row<2, U2, false>());
   const bool four = E % 4 == 0;
-  if (E <= 256) return four ? f(Row<4, UP4, true>()) : f(Row<4, UP4, false>());
+  if (E <= 256) return four ? f(Row<4, U4, true>()) : f(Row<4, U4, false>());
   if (E <= 512) return four ? f(Row<8, 2, true>()) : f(Row<8, 2, false>());
   return four ? f(Row<16, 1, true>()) : f(Row<16, 1, false>());
 }
@@ -590,7 +592,7 @@ int balance_blocks(int E) { return (E + JOIN_E - 1) / JOIN_E; }
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
   if (is_small(a)) {
-    return with_row<SMALL_T / 16, SMALL_T / 16>(a.E, [&](auto row) {
+    return with_row<SMALL_T / 16, SMALL_T / 32, SMALL_T / 32>(a.E, [&](auto row) {
       using R = decltype(row);
       if constexpr (R::N > 4) return hipErrorInvalidValue;  // E is at most 256
       else if (a.sigmoid)
@@ -603,7 +605,7 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
   // one workgroup at least: the second launch needs the ticket that the first one clears
   const int grid = a.T > chunk ? (a.T - 1) / chunk + 1 : 1;
   const size_t lds = (size_t)a.E * (PART_W + 1) * 4;
-  hipError_t e = with_row<4, 4>(a.E, [&](auto row) {
+  hipError_t e = with_row<4, 4, 4>(a.E, [&](auto row) {
     using R = decltype(row);
     if (a.sigmoid)
       return MOE_LAUNCH("balance_part", s,
@@ -628,7 +630,7 @@ hipError_t launch_balance_backward(const BalanceArgs& a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
   // two rows of 256 leave registers for more wavefronts (32768 x 256: 17.1 -> 14.3 us), four of
   // 128 fit (262144 x 128: 65 -> 58)
-  return with_row<4, 2>(a.E, [&](auto row) {
+  return with_row<4, 4, 2>(a.E, [&](auto row) {
     using R = decltype(row);
     const int grid = (a.T + 4 * R::U - 1) / (4 * R::U);
     if (a.sigmoid)

@@ -70,7 +70,8 @@ def verify(B, L, idx, score, coef=0.3, start=None, d_loss=None, d_in=None):
 
 
 SIZES = [(1, 1, 1), (1, 4, 1), (3, 8, 2), (16, 8, 2), (17, 60, 6), (64, 64, 6), (33, 65, 5), (200, 128, 8),
-         (65, 256, 8), (40, 257, 32), (300, 60, 4), (20, 1000, 9), (11, 1024, 32), (1003, 24, 3)]
+         (65, 256, 8), (40, 257, 32), (300, 60, 4), (20, 1000, 9), (11, 1024, 32), (1003, 24, 3),
+         (64, 200, 8), (65, 100, 3), (64, 128, 5), (128, 64, 6), (129, 64, 6), (64, 255, 2)]
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
