@@ -120,7 +120,7 @@ MOE_DEV constexpr int place(int j) {
 }
 // V neighbours; zeros from the end n on
 template <bool F32, int V>
-MOE_DEV void load_some(const void* p, int64_t i, int64_t n, float* f) {
+MOE_DEV void load_some(const void* p, int i, int n, float* f) {
   if (i + V <= n) {
     if constexpr (F32) {
 #pragma unroll
@@ -145,7 +145,7 @@ MOE_DEV void load_some(const void* p, int64_t i, int64_t n, float* f) {
 }
 // EXACT: the values lie on bf16's grid
 template <bool F32, bool EXACT, int V>
-MOE_DEV void store_some(void* p, int64_t i, int64_t n, const float* f) {
+MOE_DEV void store_some(void* p, int i, int n, const float* f) {
   uint32_t w[V / 2];
 #pragma unroll
   for (int j = 0; j < V / 2; ++j)
@@ -172,7 +172,7 @@ MOE_DEV void store_some(void* p, int64_t i, int64_t n, const float* f) {
   }
 }
 template <bool F32, bool SPLIT>
-MOE_DEV void load8(const void* p, int64_t i, int64_t n, float* f) {
+MOE_DEV void load8(const void* p, int i, int n, float* f) {
   if constexpr (SPLIT) {
     load_some<F32, 4>(p, i, n, f);
     load_some<F32, 4>(p, i + HALF, n, f + 4);
@@ -181,7 +181,7 @@ MOE_DEV void load8(const void* p, int64_t i, int64_t n, float* f) {
   }
 }
 template <bool F32, bool EXACT, bool SPLIT>
-MOE_DEV void store8(void* p, int64_t i, int64_t n, const float* f) {
+MOE_DEV void store8(void* p, int i, int n, const float* f) {
   if constexpr (SPLIT) {
     store_some<F32, EXACT, 4>(p, i, n, f);
     store_some<F32, EXACT, 4>(p, i + HALF, n, f + 4);
@@ -189,24 +189,24 @@ MOE_DEV void store8(void* p, int64_t i, int64_t n, const float* f) {
     store_some<F32, EXACT, 8>(p, i, n, f);
   }
 }
-// eight codes; zeros past the end
-MOE_DEV uint2 load_codes(const void* p, int64_t i, int cnt) {
-  if (cnt == 8) return *(const uint2*)((const uint8_t*)p + i);
+// eight codes; zeros from the end n on
+MOE_DEV uint2 load_codes(const void* p, int i, int n) {
+  if (i + 8 <= n) return *(const uint2*)((const uint8_t*)p + i);
   uint32_t w[2] = {0, 0};
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    if (j < cnt) w[j >> 2] |= (uint32_t)((const uint8_t*)p)[i + j] << (8 * (j & 3));
+    if (i + j < n) w[j >> 2] |= (uint32_t)((const uint8_t*)p)[i + j] << (8 * (j & 3));
   return make_uint2(w[0], w[1]);
 }
-MOE_DEV void store_codes(void* p, int64_t i, int cnt, uint2 v) {
-  if (cnt == 8) {
+MOE_DEV void store_codes(void* p, int i, int n, uint2 v) {
+  if (i + 8 <= n) {
     *(uint2*)((uint8_t*)p + i) = v;
     return;
   }
   const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    if (j < cnt) ((uint8_t*)p)[i + j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+    if (i + j < n) ((uint8_t*)p)[i + j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
 }
 
 // The tensor of a tile: the last i in [0, n) with first[i] <= tile (first ascends; a tensor
@@ -240,18 +240,23 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
   if (tile0 >= d.n) return;  // the grid is an upper bound
   // (a tile starts at a multiple of 2^11, so the high word of the place is the tile's)
   const uint32_t key = mix32(mix32((uint32_t)id + 1u) + h.seed) + (uint32_t)(tile0 >> 32) * 0x3C6EF373u;
+  const uint32_t place0 = (uint32_t)tile0;
+  // from here on places in the tile, of which the tensor has n: bases are scalars, offsets 32 bits
   constexpr bool SPLIT = !EIGHT;
-  const int64_t i = tile0 + (int)threadIdx.x * (SPLIT ? 4 : 8), n = d.n;
-  const int64_t left = n - i;
-  const int cnt = left >= 8 ? 8 : left > 0 ? (int)left : 0;  // (of neighbours)
+  const int n = d.n - tile0 < ADAMW_TILE ? (int)(d.n - tile0) : ADAMW_TILE;
+  const int i = (int)threadIdx.x * (SPLIT ? 4 : 8);
+  constexpr int SB = EIGHT ? 1 : 4, PB = P32 ? 4 : 2;
+  const auto at = [&](const void* base, int bytes) { return (const char*)base + tile0 * bytes; };
+  const auto to = [&](void* base, int bytes) { return (char*)base + tile0 * bytes; };
   float g[8], p[8], m[8], v[8];
   uint32_t r[8];
-  load8<G32, SPLIT>(d.grad, i, n, g);
-  if (MASTER) load8<true, SPLIT>(d.master, i, n, p);
-  else load8<P32, SPLIT>(d.param, i, n, p);
+  load8<G32, SPLIT>(at(d.grad, G32 ? 4 : 2), i, n, g);
+  if (MASTER) load8<true, SPLIT>(at(d.master, 4), i, n, p);
+  else load8<P32, SPLIT>(at(d.param, PB), i, n, p);
   if (EIGHT) {
-    const uint2 mc = load_codes(d.m, i, cnt), vc = load_codes(d.v, i, cnt);
-    const uint32_t me = cnt ? d.m_scale[i >> 5] : 0u, ve = cnt ? d.v_scale[i >> 5] : 0u;
+    const uint2 mc = load_codes(at(d.m, SB), i, n), vc = load_codes(at(d.v, SB), i, n);
+    const uint8_t *ms = d.m_scale + (tile0 >> 5), *vs = d.v_scale + (tile0 >> 5);
+    const uint32_t me = i < n ? ms[i >> 5] : 0u, ve = i < n ? vs[i >> 5] : 0u;
     decode_m4(mc.x, m);
     decode_m4(mc.y, m + 4);
 #pragma unroll
@@ -260,8 +265,8 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
       v[j] = decode_v(((j < 4 ? vc.x : vc.y) >> (8 * (j & 3))) & 255u) * scale_of(ve);
     }
   } else {
-    load8<true, SPLIT>(d.m, i, n, m);
-    load8<true, SPLIT>(d.v, i, n, v);
+    load8<true, SPLIT>(at(d.m, SB), i, n, m);
+    load8<true, SPLIT>(at(d.v, SB), i, n, v);
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -269,14 +274,14 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
     // reciprocal and root of one unit: the quotient is far below the weight it is added to
     const float u = m[j] * h.corr1 * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[j] * h.corr2) + h.eps);
     p[j] = fmaf(-h.lr, fmaf(d.weight_decay, p[j], u), p[j]);
-    if (EIGHT || (!P32 && !MASTER)) r[j] = mix32((uint32_t)(i + place<SPLIT>(j)) ^ key);
+    if (EIGHT || (!P32 && !MASTER)) r[j] = mix32((place0 + (uint32_t)(i + place<SPLIT>(j))) ^ key);
   }
-  if (MASTER) store8<true, false, SPLIT>(d.master_out, i, n, p);
+  if (MASTER) store8<true, false, SPLIT>(to(d.master_out, 4), i, n, p);
   if (!P32 && !MASTER) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) p[j] = round_bf16_at_random(p[j], r[j] ^ (r[j] >> 16));
   }
-  store8<P32, !P32 && !MASTER, SPLIT>(d.param_out, i, n, p);
+  store8<P32, !P32 && !MASTER, SPLIT>(to(d.param_out, PB), i, n, p);
   if (EIGHT) {
     uint32_t mt = 0, vt = 0;
 #pragma unroll
@@ -301,15 +306,15 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
     for (int j = 0; j < 8; ++j) c[j] = encode_v(v[j], vi, r[j]);
     const uint32_t vw[2] = {low_bytes(c[0], c[1], c[2], c[3]), low_bytes(c[4], c[5], c[6], c[7])};
     // a block that is not finite: codes of zero under a scale of inf, which is NaN
-    store_codes(d.m_out, i, cnt, me == 255u ? make_uint2(0, 0) : make_uint2(mw[0], mw[1]));
-    store_codes(d.v_out, i, cnt, ve == 255u ? make_uint2(0, 0) : make_uint2(vw[0], vw[1]));
-    if (cnt && (threadIdx.x & 3) == 0) {
-      ((uint8_t*)d.m_scale_out)[i >> 5] = (uint8_t)me;
-      ((uint8_t*)d.v_scale_out)[i >> 5] = (uint8_t)ve;
+    store_codes(to(d.m_out, SB), i, n, me == 255u ? make_uint2(0, 0) : make_uint2(mw[0], mw[1]));
+    store_codes(to(d.v_out, SB), i, n, ve == 255u ? make_uint2(0, 0) : make_uint2(vw[0], vw[1]));
+    if (i < n && (threadIdx.x & 3) == 0) {
+      (d.m_scale_out + (tile0 >> 5))[i >> 5] = (uint8_t)me;
+      (d.v_scale_out + (tile0 >> 5))[i >> 5] = (uint8_t)ve;
     }
   } else {
-    store8<true, false, SPLIT>(d.m_out, i, n, m);
-    store8<true, false, SPLIT>(d.v_out, i, n, v);
+    store8<true, false, SPLIT>(to(d.m_out, SB), i, n, m);
+    store8<true, false, SPLIT>(to(d.v_out, SB), i, n, v);
   }
 }
 
@@ -326,10 +331,10 @@ __global__ __launch_bounds__(64) void adamw_table_kernel(AdamwChunk c, AdamwDesc
 template <bool V>
 __global__ __launch_bounds__(256) void adamw_values_kernel(int64_t n, const uint8_t* codes,
                                                            const uint8_t* scales, bf16_t* out) {
-  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 2048) {
-    const int cnt = n - i >= 8 ? 8 : (int)(n - i);
-    const uint2 c = load_codes(codes, i, cnt);
-    const float s = scale_of(scales[i >> 5]);
+  for (int64_t t = (int64_t)blockIdx.x * 2048; t < n; t += (int64_t)gridDim.x * 2048) {
+    const int left = n - t < 2048 ? (int)(n - t) : 2048, i = (int)threadIdx.x * 8;
+    const uint2 c = load_codes(codes + t, i, left);
+    const float s = i < left ? scale_of((scales + (t >> 5))[i >> 5]) : 0.0f;
     float f[8];
     if (V) {
 #pragma unroll
@@ -340,7 +345,7 @@ __global__ __launch_bounds__(256) void adamw_values_kernel(int64_t n, const uint
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= s;
     }
-    store8<false, true, false>(out, i, n, f);
+    store8<false, true, false>(out + t, i, left, f);
   }
 }
 
