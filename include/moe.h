@@ -637,7 +637,8 @@ size_t moe_balance_workspace_bytes(const moe_shape* shape, const moe_balance* ba
  * grad_scale:
  *   m' = beta1 m + (1 - beta1) g,  v' = beta2 v + (1 - beta2) g^2
  *   p' = p - lr (m' corr1 / (sqrt(v' corr2) + eps) + weight_decay p),  corr = 1 / (1 - beta^step)
- * all in fp32.  All tensors of a table have the same types:
+ * all in fp32; with an eps below 2^-39, v' corr2 from 2^104 on counts as infinite (an update of
+ * 0, as wherever it passes fp32's range).  All tensors of a table have the same types:
  *   p_type, g_type  MOE_F32 or MOE_BF16, of the parameters and of the gradients
  *   master          1: bf16 parameters are copies, rounded to nearest, of fp32 masters that
  *                   the step reads and writes.  bf16 parameters without masters are rounded

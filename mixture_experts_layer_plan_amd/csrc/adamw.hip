@@ -268,11 +268,17 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
     load8<true, SPLIT>(at(d.m, SB), i, n, m);
     load8<true, SPLIT>(at(d.v, SB), i, n, v);
   }
+  // The root instruction takes a subnormal number for 0: 2^-63 off at most, which matters beside
+  // an eps below 2^-39 alone.  There it gets 2^24 times the number (inf from 2^104 on); a test of
+  // each number would cost the step of 8-bit states 2 %.
+  const bool small = h.eps < 0x1p-39f;
+  const float corr2 = small ? h.corr2 * 0x1p24f : h.corr2, unscale = small ? 0x1p-12f : 1.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     update_state(m[j], v[j], g[j], h);
     // reciprocal and root of one unit: the quotient is far below the weight it is added to
-    const float u = m[j] * h.corr1 * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[j] * h.corr2) + h.eps);
+    const float root = __builtin_amdgcn_sqrtf(v[j] * corr2);
+    const float u = m[j] * h.corr1 * __builtin_amdgcn_rcpf(fmaf(root, unscale, h.eps));
     p[j] = fmaf(-h.lr, fmaf(d.weight_decay, p[j], u), p[j]);
     if (EIGHT || (!P32 && !MASTER)) r[j] = mix32((place0 + (uint32_t)(i + place<SPLIT>(j))) ^ key);
   }

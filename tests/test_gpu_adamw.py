@@ -228,6 +228,25 @@ def test_extreme_magnitudes(B):
         verify(host, outs, "f32", False, bits, as_dict(h))
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_denominators_below_the_normal_numbers(B, bits):
+    """v of tiny gradients is subnormal; its root is not, and with a tiny eps it is the
+    denominator."""
+    say(f"adamw subnormal v bits={bits}")
+    for eps in (1e-30, 1e-12):
+        host = make([4096], "f32", "f32", False, bits, 5)
+        g = host[0]["grad"]
+        g *= torch.logspace(-21, -12, 4096).flip(0)
+        for k in ("m", "v", "m_scale", "v_scale"):
+            if k in host[0]:
+                host[0][k][:] = 0
+        h = B.adamw_hyper(1e-2, eps=eps, step=1, seed=78)
+        s, dev, outs, tab, oks = table(B, host, "f32", "f32", False, bits)
+        B.moe_adamw_step(s, tab, h)
+        torch.cuda.synchronize()
+        verify(host, outs, "f32", False, bits, as_dict(h))
+
+
 def test_values_of_codes(B):
     say("adamw values of codes")
     for n in (1, 31, 32, 100, 2048, 5000):
