@@ -540,7 +540,8 @@ moe_status moe_lora_backward_bf16(const moe_lora_shape* shape, const void* plan,
  * of h^2 (MOE_NORM_RMS).  Sums are in fp32, the variance from the differences to the mean.
  *   0 <= T; H a multiple of 8 in [8, 16384]; eps in (0, 1]
  * Where a value of a row is not finite, its rows of y and dx are not valid (NaN among them),
- * nor are dw and db; other rows are. */
+ * nor are dw and db; other rows are.  A row whose sum of squares passes fp32's range (values
+ * from about 2^57 on) has 1 / sqrt(variance + eps) = 0. */
 typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
 typedef struct {
   int32_t T, H;
@@ -569,7 +570,8 @@ moe_status moe_norm_f32(const moe_norm_shape* shape, const float* x, const float
  *   dw, db [H]  overwritten, rounded once from fp32 sums over the rows (zeros with T == 0);
  *               NULL: not wanted
  * dx may be dy or dh_in itself, and shares no bytes with h (MOE_E_UNSUPPORTED otherwise, as
- * for a dy or dh_in that begins elsewhere in dx).
+ * for a dy or dh_in that begins elsewhere in dx, and for a dw or db that shares bytes with w,
+ * dx or the other one).
  * ws [ws_bytes >= moe_norm_workspace_bytes(shape)], read only with dw or db. */
 moe_status moe_norm_backward_bf16(const moe_norm_shape* shape, const void* h, const void* w,
                                   const float* stats, const void* dy, const void* dh_in, void* dx,

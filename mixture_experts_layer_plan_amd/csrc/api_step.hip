@@ -63,8 +63,12 @@ moe_status norm_backward_impl(bool f32, const moe_norm_shape* s, const void* h, 
   if (!all_aligned({h, w, stats, dy, dh_in, dx, dw, db, ws})) return MOE_E_ALIGN;
   if ((dw || db) && ws_bytes < norm_ws_bytes(s)) return MOE_E_WORKSPACE;
   const uint64_t n = (uint64_t)s->T * s->H * (f32 ? 4 : 2);
-  if (overlap(dx, n, h, n) || overlap_base(dx, dy, n) || overlap_base(dx, dh_in, n))
+  const uint64_t row = (uint64_t)s->H * (f32 ? 4 : 2);
+  if (overlap(dx, n, h, n) || overlap_base(dx, dy, n) || overlap_base(dx, dh_in, n) ||
+      overlap(dw, row, db, row))
     return MOE_E_UNSUPPORTED;
+  for (const void* d : {dw, db})  // written while rows are still read and written
+    if (overlap(d, row, w, row) || overlap(d, row, dx, n)) return MOE_E_UNSUPPORTED;
   NormBackArgs a;
   a.h = h;
   a.w = w;

@@ -217,8 +217,6 @@ def run_backward(b: LayerBuffers, inp: dict, stream=None):
     elif "w_router" in inp:
         B.moe_router_backward_f32(s, x, inp["w_router"], b.d_logits, b.dw_router, b.dx,
                                   stream)
-
-
     if b.norm is not None:
         res = inp.get("residual")
         fn = B.moe_norm_backward_f32 if b.dtype == "f32" else B.moe_norm_backward_bf16
@@ -240,10 +238,10 @@ class AdamW:
     """The states of the weights in ``inp`` that ``b`` has gradients for, and the table of
     the step over them.  Weights and states are updated in place: both have to stay where
     they are.  ``state`` holds, by the weight's name, m and v (zeros; for state_bits = 8 codes,
-    with m_scale and v_scale) and, if ``master``, the fp32 master (the weight's value)."""
+    with m_scale and v_scale) and, if ``master``, the fp32 master (the weight's value).  They and
+    the table are written on the current stream."""
 
-    def __init__(self, b: LayerBuffers, inp: dict, state_bits=32, master=False, weight_decay=0.1,
-                 stream=None):
+    def __init__(self, b: LayerBuffers, inp: dict, state_bits=32, master=False, weight_decay=0.1):
         if master and b.dtype == "f32":
             raise ValueError("fp32 weights are their own masters")
         if not b.backward:
@@ -272,7 +270,7 @@ class AdamW:
         self.table = torch.empty(B.moe_adamw_table_bytes(self.shape), dtype=torch.uint8,
                                  device=tensors[0]["grad"].device)
         self._tensors = tensors     # the table holds their addresses
-        B.moe_adamw_table(self.shape, tensors, self.table, stream)
+        B.moe_adamw_table(self.shape, tensors, self.table)
 
     def step(self, hyper, stream=None):
         """``hyper``: a ``binding.adamw_hyper`` of this step, or a device tensor of the bytes

@@ -69,6 +69,11 @@ def test_norm_outputs_over_inputs(L):
             assert bwd(L, s, b, dx=X + off) == UNSUP and bwd(L, s, b, dx=Y + off) == UNSUP
             assert bwd(L, s, b, dh=FAR, dx=FAR + off) == UNSUP
         assert fwd(L, s, a, res=FAR, h=Z, y=Z) == UNSUP and bwd(L, s, b, dx=X) == UNSUP
+        row = size // 4
+        for off in (0, 16, -16, row - 16, 16 - row):
+            assert bwd(L, s, b, dw=FAR, db=FAR + off) == UNSUP
+            assert bwd(L, s, b, w=FAR, dw=FAR + off) == UNSUP and bwd(L, s, b, w=FAR, db=FAR + off) == UNSUP
+            assert bwd(L, s, b, dx=FAR, dw=FAR + off) == UNSUP and bwd(L, s, b, dx=FAR, db=FAR + off) == UNSUP
 
 
 # ---------------------------------------------------------------------- balance
