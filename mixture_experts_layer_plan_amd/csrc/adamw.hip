@@ -227,9 +227,10 @@ MOE_DEV int tensor_of(const int32_t* first, int n, int tile) {
 
 // 2048 elements a workgroup, eight a thread: larger tiles leave CUs without work in sets of
 // small tensors (8192: 789 thousand elements 9.1 us, now 5.4).  fp32 states are bound by memory
-// (222 million elements with masters: 6.22 GB, the least, in 1141 us, 5.45 TB/s), states of 8
-// bits by vector issue (88 % of it: 502 instructions for eight elements, 70 of them the random
-// bits, 60 the codes) at 5.65 TB/s.
+// (222 million elements with masters: 6.22 GB, the least, in 1140 us, 5.45 TB/s), states of 8
+// bits by vector issue (87 % of it: 490 instructions for eight elements, 70 of them the random
+// bits, 60 the codes) at 5.7 TB/s.  Places are 32-bit offsets over scalar bases (64-bit places:
+// 17 instructions more, 410 -> 391 us).
 template <bool P32, bool G32, bool MASTER, bool EIGHT>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
   const int tile = blockIdx.x;
