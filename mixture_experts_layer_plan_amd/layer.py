@@ -65,6 +65,7 @@ class LayerBuffers:
         self.saved = torch.empty(B.moe_saved_bytes(self.s, self.dt), **u8)
         self.ws_fwd = torch.empty(B.moe_workspace_bytes(self.s, self.dt, False), **u8)
         self.wq = torch.empty(B.moe_mx_weights_bytes(self.s), **u8) if dtype == "mxfp8" else None
+        self.wq_stale = False   # whether a step has changed the weights since wq was made
         self.y = torch.empty((T, H), dtype=tdt, device=dev)
         self.scoring = scoring
         self.router_proj = router_proj
@@ -128,11 +129,13 @@ class LayerBuffers:
 def quantize_weights(b: LayerBuffers, inp: dict, stream=None):
     """MXFP8 weights in the six orientations the MX GEMMs read (once per weight update)."""
     B.moe_quantize_weights_mxfp8(b.s, inp["w_gate"], inp["w_up"], inp["w_down"], b.wq, stream)
+    b.wq_stale = False
 
 
 def run_forward(b: LayerBuffers, inp: dict, stream=None, quantize=True):
     """route -> plan -> forward; for MXFP8 also the weight quantisation unless
-    ``quantize`` is False (weights already quantised into ``b.wq``)."""
+    ``quantize`` is False (weights already quantised into ``b.wq``) and no step of an
+    ``AdamW`` over these buffers has changed them since."""
     s = b.s
     logits = _logits(b, inp)
     if b.norm is not None:
@@ -175,7 +178,7 @@ def _x(b: LayerBuffers, inp: dict):
 def _run_experts(b: LayerBuffers, inp: dict, stream, quantize):
     s, x = b.s, _x(b, inp)
     if b.dtype == "mxfp8":
-        if quantize:
+        if quantize or b.wq_stale:
             quantize_weights(b, inp, stream)
         B.moe_forward_mxfp8(s, b.plan, x, b.topk_w, b.wq, inp.get("s_gate"),
                             inp.get("s_up"), inp.get("s_down"), b.y, b.saved, b.ws_fwd, stream)
@@ -270,16 +273,24 @@ class AdamW:
         self.table = torch.empty(B.moe_adamw_table_bytes(self.shape), dtype=torch.uint8,
                                  device=tensors[0]["grad"].device)
         self._tensors = tensors     # the table holds their addresses
+        experts = {"w_gate", "w_up", "w_down"} & self.state.keys()
+        self._quantised = b if b.dtype == "mxfp8" and experts else None
         B.moe_adamw_table(self.shape, tensors, self.table)
 
     def step(self, hyper, stream=None):
         """``hyper``: a ``binding.adamw_hyper`` of this step, or a device tensor of the bytes
-        of one (which a captured step reads anew at every replay)."""
+        of one (which a captured step reads anew at every replay).  The next forward of MXFP8
+        buffers quantises the new weights; for other buffers over the same weights, and behind
+        the replay of a captured step alone, this is the caller's to do."""
         B.moe_adamw_step(self.shape, self.table, hyper, stream)
+        if self._quantised is not None:
+            self._quantised.wq_stale = True
 
 
 def run_layer(b: LayerBuffers, inp: dict, backward: bool = True, stream=None, quantize=True,
               adamw: AdamW | None = None, hyper=None):
+    """``quantize=False``: ``b.wq`` holds the MXFP8 weights as they are before the call and,
+    with a step, as they are after it."""
     if (adamw is None) != (hyper is None):
         raise ValueError("a step takes adamw and hyper")
     if adamw is not None and not backward:
@@ -289,3 +300,5 @@ def run_layer(b: LayerBuffers, inp: dict, backward: bool = True, stream=None, qu
         run_backward(b, inp, stream)
     if adamw is not None:
         adamw.step(hyper, stream)
+        if b.wq_stale and not quantize:     # here, so that replays of a captured call do it too
+            quantize_weights(b, inp, stream)

@@ -1,0 +1,73 @@
+"""The calls that ``run_layer`` makes, in their order, with the library's entry points
+replaced by a record of their names."""
+import pytest
+import torch
+
+B = pytest.importorskip("mixture_experts_layer_plan_amd.binding")
+
+ENTRIES = ("moe_route", "moe_plan", "moe_quantize_weights_mxfp8", "moe_forward_mxfp8", "moe_backward_mxfp8",
+           "moe_forward_bf16", "moe_backward_bf16", "moe_route_backward", "moe_adamw_table", "moe_adamw_step")
+SHORT = {"moe_quantize_weights_mxfp8": "quantise", "moe_forward_mxfp8": "forward", "moe_forward_bf16": "forward",
+         "moe_adamw_step": "step"}
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    got = []
+    for name in ENTRIES:
+        monkeypatch.setattr(B, name, lambda *a, name=name: got.append(SHORT.get(name)))
+
+    def take():
+        out = [n for n in got if n]
+        got.clear()
+        return out
+    return take
+
+
+def layer(dtype):
+    from mixture_experts_layer_plan_amd import AdamW, LayerBuffers
+    T, H, I, E, k = 4, 128, 128, 2, 1
+    b = LayerBuffers(T, H, I, E, k, dtype=dtype, device="cpu")
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)    # noqa: E731
+    inp = dict(x=z(T, H), logits=torch.zeros(T, E), w_gate=z(E, I, H), w_up=z(E, I, H), w_down=z(E, H, I),
+               dy=z(T, H))
+    return b, inp, AdamW(b, inp, 8), B.adamw_hyper(1e-3, seed=1)
+
+
+def test_no_forward_reads_quantised_weights_from_before_a_step(calls):
+    """Whatever ``quantize`` says, a forward behind a step reads the step's weights."""
+    from mixture_experts_layer_plan_amd import layer as layer_, run_layer
+    b, inp, opt, h = layer("mxfp8")
+    calls()
+    run_layer(b, inp)
+    assert calls() == ["quantise", "forward"]
+    run_layer(b, inp, quantize=False)                       # nothing has changed
+    assert calls() == ["forward"]
+    for _ in range(2):                                      # the same calls again, as a replay makes them
+        run_layer(b, inp, quantize=False, adamw=opt, hyper=h)
+        assert calls() == ["forward", "step", "quantise"]
+    run_layer(b, inp, quantize=False)
+    assert calls() == ["forward"]
+    for _ in range(2):
+        run_layer(b, inp, adamw=opt, hyper=h)
+        assert calls() == ["quantise", "forward", "step"]
+    run_layer(b, inp, backward=False, quantize=False)
+    run_layer(b, inp, quantize=False)
+    assert calls() == ["quantise", "forward", "forward"]
+    opt.step(h)                                             # a step by itself
+    layer_.run_forward(b, inp, quantize=False)
+    layer_.run_forward(b, inp, quantize=False)
+    assert calls() == ["step", "quantise", "forward", "forward"]
+    opt.step(h)
+    layer_.quantize_weights(b, inp)                         # and weights quantised by the caller
+    layer_.run_forward(b, inp, quantize=False)
+    assert calls() == ["step", "quantise", "forward"]
+
+
+def test_a_bf16_layer_quantises_nothing(calls):
+    from mixture_experts_layer_plan_amd import run_layer
+    b, inp, opt, h = layer("bf16")
+    calls()
+    run_layer(b, inp, quantize=False, adamw=opt, hyper=h)
+    run_layer(b, inp, quantize=False)
+    assert calls() == ["forward", "step", "forward"]
