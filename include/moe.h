@@ -653,8 +653,9 @@ size_t moe_balance_workspace_bytes(const moe_shape* shape, const moe_balance* ba
  *                   become 0.  A block that holds a value that is not finite, or one of 2^126
  *                   and more, becomes NaN as a whole.  Zeroed buffers are the start (of 32
  *                   bits too).
- * The random bits come from the step's seed and the element's place alone: the same call
- * gives the same bits, another step takes another seed.
+ * The random bits come from the step's seed and the element's place alone (not from the
+ * step's number): the same call gives the same bits, so another step has to take another
+ * seed, or an element is rounded by the same random number in each.
  *   n_tensors in [1, MOE_ADAMW_MAX_TENSORS]; elements: the sum of the tensors' n;
  *   elements / 2048 + n_tensors < 2^24 (MOE_E_UNSUPPORTED otherwise) */
 #define MOE_ADAMW_MAX_TENSORS 65536

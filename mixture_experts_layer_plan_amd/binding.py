@@ -645,9 +645,12 @@ def adamw_shape(elements, n_tensors, p_type="bf16", g_type="bf16", master=False,
                            int(bool(master)), int(state_bits))
 
 
-def adamw_hyper(lr, beta1=0.9, beta2=0.95, eps=1e-8, step=1, grad_scale=1.0, seed=0) -> moe_adamw_hyper:
-    """A step's scalars; ``bytes(...)`` of it is what a device copy holds."""
+def adamw_hyper(lr, beta1=0.9, beta2=0.95, eps=1e-8, step=1, grad_scale=1.0, seed=None) -> moe_adamw_hyper:
+    """A step's scalars; ``bytes(...)`` of it is what a device copy holds.  ``seed`` is ``step``
+    if not given: with one seed for all steps an element would be rounded by the same random
+    number every time, up or down for good."""
     out = moe_adamw_hyper()
+    seed = step if seed is None else seed
     _call("moe_adamw_hyper_of", float(lr), float(beta1), float(beta2), float(eps), int(step),
           float(grad_scale), int(seed) & 0xFFFFFFFF, ctypes.byref(out))
     return out

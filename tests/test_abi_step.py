@@ -246,3 +246,21 @@ def test_adamw_values(L):
     assert rc(c=BAD) == ALIGN and rc(o=BAD) == ALIGN and rc(s=BAD) == ALIGN
     assert rc(o=X) == UNSUP and rc(o=X - 192) == UNSUP and rc(s=Z + 16) == UNSUP
     assert rc(n=0, c=None, s=None, o=None) == OK
+
+
+def test_steps_without_a_seed_have_random_bits_of_their_own():
+    import numpy as np
+
+    import oracle
+    seeds = [B.adamw_hyper(1e-3, step=t).seed for t in range(1, 201)]
+    assert len(set(seeds)) == 200
+    assert B.adamw_hyper(1e-3, step=5, seed=0).seed == 0 and B.adamw_hyper(1e-3, step=5, seed=9).seed == 9
+    # 64 weights of 1 that fall by 2e-4, a twentieth of their step, 200 times: with bits of
+    # their own in each step a weight stands still with probability (1 - 0.0512)^200 < 3e-5
+    # (below 1 a step is 2^-8, of which 2e-4 is 0.0512)
+    p = np.ones(64)
+    for seed in seeds:
+        p = oracle.round_bf16_at_random(p - 2e-4, oracle.random_bits(seed, 0, 64))
+    assert (p < 1).all()
+    # the average is off by less than 6 of its deviations: at most 2^-9 a step, 200 steps, 64 weights
+    assert abs(p.mean() - (1 - 200 * 2e-4)) < 6 * 2.0 ** -9 * 200 ** 0.5 / 8
