@@ -273,8 +273,7 @@ class AdamW:
         self.table = torch.empty(B.moe_adamw_table_bytes(self.shape), dtype=torch.uint8,
                                  device=tensors[0]["grad"].device)
         self._tensors = tensors     # the table holds their addresses
-        experts = {"w_gate", "w_up", "w_down"} & self.state.keys()
-        self._quantised = b if b.dtype == "mxfp8" and experts else None
+        self._buffers = b
         B.moe_adamw_table(self.shape, tensors, self.table)
 
     def step(self, hyper, stream=None):
@@ -283,22 +282,41 @@ class AdamW:
         buffers quantises the new weights; for other buffers over the same weights, and behind
         the replay of a captured step alone, this is the caller's to do."""
         B.moe_adamw_step(self.shape, self.table, hyper, stream)
-        if self._quantised is not None:
-            self._quantised.wq_stale = True
+        self._mark(self._buffers)
+
+    def _mark(self, b):
+        if b.dtype == "mxfp8" and {"w_gate", "w_up", "w_down"} & self.state.keys():
+            b.wq_stale = True
+
+    def check(self, b: LayerBuffers, inp: dict):
+        """ValueError unless the step reads the gradients of ``b`` and updates weights of
+        ``inp`` (the table holds addresses; weights that it leaves out stay as they are)."""
+        def ptr(t):
+            return None if t is None else t.data_ptr()
+        mine = {n: (ptr(t["param"]), ptr(t["grad"])) for n, t in zip(self.state, self._tensors)}
+        its = {n: (ptr(inp[n]), ptr(getattr(b, g))) for n, g, _ in _WEIGHTS
+               if n in inp and getattr(b, g, None) is not None}
+        bad = sorted(n for n in mine if mine[n] != its.get(n))
+        if bad:
+            raise ValueError(f"the step is over other weights or gradients than this call's: {bad}")
 
 
 def run_layer(b: LayerBuffers, inp: dict, backward: bool = True, stream=None, quantize=True,
               adamw: AdamW | None = None, hyper=None):
-    """``quantize=False``: ``b.wq`` holds the MXFP8 weights as they are before the call and,
+    """``adamw`` is over weights of ``inp`` and their gradients in ``b`` (ValueError otherwise).
+    ``quantize=False``: ``b.wq`` holds the MXFP8 weights as they are before the call and,
     with a step, as they are after it."""
     if (adamw is None) != (hyper is None):
         raise ValueError("a step takes adamw and hyper")
     if adamw is not None and not backward:
         raise ValueError("a step takes the gradients of the backward")
+    if adamw is not None:
+        adamw.check(b, inp)
     run_forward(b, inp, stream, quantize)
     if backward:
         run_backward(b, inp, stream)
     if adamw is not None:
         adamw.step(hyper, stream)
+        adamw._mark(b)
         if b.wq_stale and not quantize:     # here, so that replays of a captured call do it too
             quantize_weights(b, inp, stream)

@@ -6,7 +6,8 @@ import torch
 B = pytest.importorskip("mixture_experts_layer_plan_amd.binding")
 
 ENTRIES = ("moe_route", "moe_plan", "moe_quantize_weights_mxfp8", "moe_forward_mxfp8", "moe_backward_mxfp8",
-           "moe_forward_bf16", "moe_backward_bf16", "moe_route_backward", "moe_adamw_table", "moe_adamw_step")
+           "moe_forward_bf16", "moe_backward_bf16", "moe_route_backward", "moe_adamw_table", "moe_adamw_step",
+           "moe_lora_plan", "moe_lora_bf16", "moe_lora_backward_bf16")
 SHORT = {"moe_quantize_weights_mxfp8": "quantise", "moe_forward_mxfp8": "forward", "moe_forward_bf16": "forward",
          "moe_adamw_step": "step"}
 
@@ -67,6 +68,42 @@ def test_no_forward_reads_quantised_weights_from_before_a_step(calls):
 def test_a_bf16_layer_quantises_nothing(calls):
     from mixture_experts_layer_plan_amd import run_layer
     b, inp, opt, h = layer("bf16")
+    calls()
+    run_layer(b, inp, quantize=False, adamw=opt, hyper=h)
+    run_layer(b, inp, quantize=False)
+    assert calls() == ["forward", "step", "forward"]
+
+
+def test_a_step_over_other_weights_or_gradients_is_refused(calls):
+    """It would update weights that the forward did not read, or from gradients that the
+    backward did not write."""
+    from mixture_experts_layer_plan_amd import run_layer
+    b, inp, opt, h = layer("bf16")
+    b2, inp2, _, _ = layer("bf16")
+    for bb, ii in ((b2, inp), (b, inp2), (b, dict(inp, w_up=inp2["w_up"])),
+                   (b, {k: v for k, v in inp.items() if k != "w_down"})):
+        calls()
+        with pytest.raises(ValueError):
+            run_layer(bb, ii, adamw=opt, hyper=h)
+        assert calls() == []
+    run_layer(b, dict(inp, x=inp2["x"], dy=inp2["dy"]), adamw=opt, hyper=h)     # another batch
+    assert calls() == ["forward", "step"]
+    # buffers for another number of tokens that share the gradients
+    for g in ("dw_gate", "dw_up", "dw_down"):
+        setattr(b2, g, getattr(b, g))
+    run_layer(b2, dict(inp2, **{w: inp[w] for w in ("w_gate", "w_up", "w_down")}), adamw=opt, hyper=h)
+    assert calls() == ["forward", "step"]
+
+
+def test_a_step_over_some_of_the_weights(calls):
+    """Weights that the table leaves out stay as they are: an MXFP8 layer's experts too."""
+    from mixture_experts_layer_plan_amd import AdamW, LayerBuffers, run_layer
+    _, inp, _, h = layer("mxfp8")
+    b = LayerBuffers(4, 128, 128, 2, 1, dtype="mxfp8", device="cpu", adapters=(1, 16))
+    inp.update(lora_a=torch.zeros(1, 16, 128, dtype=torch.bfloat16),
+               lora_b=torch.zeros(1, 128, 16, dtype=torch.bfloat16), lora_scale=torch.zeros(1),
+               adapter_idx=torch.zeros(4, dtype=torch.int32))
+    opt = AdamW(b, {k: inp[k] for k in ("lora_a", "lora_b")})
     calls()
     run_layer(b, inp, quantize=False, adamw=opt, hyper=h)
     run_layer(b, inp, quantize=False)
