@@ -698,7 +698,7 @@ typedef struct {
 } moe_adamw_hyper;
 
 /* Fills `out` (host memory): step >= 1, 0 <= beta < 1, eps in [1e-30, 1], lr and grad_scale
- * finite. */
+ * finite in fp32. */
 moe_status moe_adamw_hyper_of(double lr, double beta1, double beta2, double eps, int64_t step,
                               double grad_scale, uint32_t seed, moe_adamw_hyper* out);
 

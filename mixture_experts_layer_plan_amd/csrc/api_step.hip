@@ -353,10 +353,11 @@ moe_status moe_adamw_table(const moe_adamw_shape* s, const moe_adamw_tensor* ten
 moe_status moe_adamw_hyper_of(double lr, double beta1, double beta2, double eps, int64_t step,
                               double grad_scale, uint32_t seed, moe_adamw_hyper* out) {
   if (!out) return MOE_E_NULL;
-  if (!(lr - lr == 0.0) || !(grad_scale - grad_scale == 0.0) || step < 1) return MOE_E_SHAPE;
+  const float lr32 = (float)lr, scale32 = (float)grad_scale;  // (1e39 is finite in double alone)
+  if (!(lr32 - lr32 == 0.0f) || !(scale32 - scale32 == 0.0f) || step < 1) return MOE_E_SHAPE;
   if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return MOE_E_SHAPE;
   if (!(eps >= 1e-30 && eps <= 1.0)) return MOE_E_SHAPE;
-  out->lr = (float)lr;
+  out->lr = lr32;
   out->beta1 = (float)beta1;
   out->one_minus_beta1 = (float)(1.0 - beta1);
   out->beta2 = (float)beta2;
@@ -364,7 +365,7 @@ moe_status moe_adamw_hyper_of(double lr, double beta1, double beta2, double eps,
   out->eps = (float)eps;
   out->corr1 = (float)(1.0 / (1.0 - pow(beta1, (double)step)));
   out->corr2 = (float)(1.0 / (1.0 - pow(beta2, (double)step)));
-  out->grad_scale = (float)grad_scale;
+  out->grad_scale = scale32;
   out->seed = seed;
   return MOE_OK;
 }

@@ -264,3 +264,10 @@ def test_steps_without_a_seed_have_random_bits_of_their_own():
     assert (p < 1).all()
     # the average is off by less than 6 of its deviations: at most 2^-9 a step, 200 steps, 64 weights
     assert abs(p.mean() - (1 - 200 * 2e-4)) < 6 * 2.0 ** -9 * 200 ** 0.5 / 8
+
+
+def test_scalars_that_fp32_does_not_hold(L):
+    out = B.moe_adamw_hyper()
+    for lr, scale in ((1e39, 1.0), (-1e300, 1.0), (1e-3, 1e39), (1e-3, -3.5e38)):
+        assert L.moe_adamw_hyper_of(lr, 0.9, 0.95, 1e-8, 1, scale, 0, ctypes.byref(out)) == SHAPE, (lr, scale)
+    assert L.moe_adamw_hyper_of(3e38, 0.9, 0.95, 1e-8, 1, -3e38, 0, ctypes.byref(out)) == OK
