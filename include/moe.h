@@ -538,7 +538,7 @@ moe_status moe_lora_backward_bf16(const moe_lora_shape* shape, const void* plan,
  *   y = (h - mean) / sqrt(variance + eps) * w + b, rounded once,
  * over the H values of a row: mean and variance of h (MOE_NORM_LAYER), or 0 and the mean
  * of h^2 (MOE_NORM_RMS).  Sums are in fp32, the variance from the differences to the mean.
- *   0 <= T; H a multiple of 8 in [8, 16384]; eps in (0, 1]
+ *   0 <= T; H a multiple of 8 in [8, 16384]; eps in [2^-126, 1]
  * Where a value of a row is not finite, its rows of y and dx are not valid (NaN among them),
  * nor are dw and db; other rows are.  A row whose sum of squares passes fp32's range (values
  * from about 2^57 on) has 1 / sqrt(variance + eps) = 0. */

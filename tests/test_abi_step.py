@@ -271,3 +271,11 @@ def test_scalars_that_fp32_does_not_hold(L):
     for lr, scale in ((1e39, 1.0), (-1e300, 1.0), (1e-3, 1e39), (1e-3, -3.5e38)):
         assert L.moe_adamw_hyper_of(lr, 0.9, 0.95, 1e-8, 1, scale, 0, ctypes.byref(out)) == SHAPE, (lr, scale)
     assert L.moe_adamw_hyper_of(3e38, 0.9, 0.95, 1e-8, 1, -3e38, 0, ctypes.byref(out)) == OK
+
+
+def test_norm_eps_below_the_normal_numbers(L):
+    for eps in (1.4e-45, 1e-40, 2.0 ** -127):
+        s = B.norm_shape(4, 64, "rms", eps)
+        assert s.eps > 0 and fwd(L, s) == SHAPE and bwd(L, s) == SHAPE and B.moe_norm_workspace_bytes(s) == 0
+    s = B.norm_shape(0, 64, "rms", 2.0 ** -126)
+    assert fwd(L, s, x=None, y=None, stats=None) == OK

@@ -287,3 +287,15 @@ def test_offsets_past_32_bits(B):
     torch.cuda.synchronize()
     verify(i, dict(y=y[-3:], dx=dy[-3:], dw=dw, db=db), "bf16")
     assert torch.equal(y[100], i["b"].cuda()) and not dy[:-3].any()
+
+
+def test_the_smallest_eps(B):
+    """Rows whose squares lie around the smallest normal number, beside an eps of it: below 640
+    additions a square is off by 2^-150 beside the sum of 2^-126 and more, 2^-24 of it, which
+    the bound has (a row of 640 takes 30 of its 56 roundings at most)."""
+    say("norm with eps = 2^-126")
+    i = inputs(6, 640, "f32")
+    i["x"] *= torch.tensor([1e-23, 1e-21, 1e-20, 1e-19, 1e-18, 1e-10])[:, None]
+    i["dy"] *= 1e-20
+    for kind in ("layer", "rms"):
+        verify(i, run(B, i, "f32", kind, 2.0 ** -126), "f32", kind, 2.0 ** -126)
