@@ -556,7 +556,8 @@ typedef struct {
  *   y [T, H]            out; it may be x or residual itself, but shares no bytes with h
  *   stats fp32 [T, 2]   out: mean (0 for RMS) and 1 / sqrt(variance + eps) of each row, which
  *                       the backward reads
- * y or h that share bytes with an x or residual that begins elsewhere: MOE_E_UNSUPPORTED. */
+ * Outputs share no other bytes with an input or with each other (MOE_E_UNSUPPORTED: y or h
+ * and an x or residual that begins elsewhere, or w or b; stats and any of them). */
 moe_status moe_norm_bf16(const moe_norm_shape* shape, const void* x, const void* residual,
                          const void* w, const void* b, void* h, void* y, float* stats,
                          hipStream_t stream);

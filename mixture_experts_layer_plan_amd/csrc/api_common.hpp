@@ -80,10 +80,20 @@ inline bool any_null_rows(const moe_shape* s, std::initializer_list<const void*>
 // output over its own base is read and written row by row: the same pointer is fine).
 inline bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
   const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
-  return a && b && p < q + nb && q < p + na;
+  return a && b && na && nb && p < q + nb && q < p + na;
 }
 inline bool overlap_base(const void* y, const void* base, uint64_t n) {
   return y != base && overlap(y, n, base, n);
+}
+// A buffer of a call, and whether it shares bytes with one of `others`.
+struct Span {
+  const void* p;
+  uint64_t n;
+};
+inline bool overlaps_any(Span a, std::initializer_list<Span> others) {
+  for (const Span& o : others)
+    if (overlap(a.p, a.n, o.p, o.n)) return true;
+  return false;
 }
 
 }  // namespace moe

@@ -36,10 +36,14 @@ moe_status norm_impl(bool f32, const moe_norm_shape* s, const void* x, const voi
   if (s->T > 0 && any_null({x, y, stats})) return MOE_E_NULL;
   if (s->T > 0 && (res != nullptr) != (h != nullptr)) return MOE_E_NULL;
   if (!all_aligned({x, res, w, b, h, y, stats})) return MOE_E_ALIGN;
-  const uint64_t n = (uint64_t)s->T * s->H * (f32 ? 4 : 2);
+  const uint64_t row = (uint64_t)s->H * (f32 ? 4 : 2), n = s->T * row;
   // a workgroup reads a row before it writes it: the same pointer is fine
   if (overlap_base(y, x, n) || overlap_base(y, res, n) || overlap_base(h, x, n) ||
       overlap_base(h, res, n) || overlap(y, n, h, n))
+    return MOE_E_UNSUPPORTED;
+  // w and b are read, and rows of stats written, while other workgroups write theirs
+  if (overlaps_any({y, n}, {{w, row}, {b, row}}) || overlaps_any({h, n}, {{w, row}, {b, row}}) ||
+      overlaps_any({stats, (uint64_t)s->T * 8}, {{x, n}, {res, n}, {w, row}, {b, row}, {h, n}, {y, n}}))
     return MOE_E_UNSUPPORTED;
   if (s->T == 0) return MOE_OK;
   NormArgs a;

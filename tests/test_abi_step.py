@@ -279,3 +279,28 @@ def test_norm_eps_below_the_normal_numbers(L):
         assert s.eps > 0 and fwd(L, s) == SHAPE and bwd(L, s) == SHAPE and B.moe_norm_workspace_bytes(s) == 0
     s = B.norm_shape(0, 64, "rms", 2.0 ** -126)
     assert fwd(L, s, x=None, y=None, stats=None) == OK
+
+
+def partly(at, size, own):
+    """Places of `own` bytes that share some with [at, at + size)"""
+    return [p for p in (at, at + 16, at - 16, at + size - 16, at - own + 16)
+            if p < at + size and at < p + own]
+
+
+def test_norm_outputs_over_the_other_inputs(L):
+    T, H = 64, 512
+    s = B.norm_shape(T, H)
+    far = dict(w=0x5000000, b=0x6000000, stats=0x7000000)
+    for f, e in (("bf16", 2), ("f32", 4)):
+        name, row, n, st = "moe_norm_" + f, H * e, T * H * e, T * 8
+        for k in ("w", "b"):
+            for p in partly(far[k], row, n):
+                assert fwd(L, s, name, **dict(far, y=p)) == UNSUP
+                assert fwd(L, s, name, **dict(far, res=FAR, h=p)) == UNSUP
+            for p in partly(far[k], row, st):
+                assert fwd(L, s, name, **dict(far, stats=p)) == UNSUP
+        for at in (X, Y, FAR, Z):
+            for p in partly(at, n, st):
+                assert fwd(L, s, name, **dict(far, res=FAR, h=Z, stats=p)) == UNSUP
+    # no rows, no bytes
+    assert fwd(L, B.norm_shape(0, H), y=F + 16, stats=F + 16) == OK
