@@ -570,10 +570,9 @@ moe_status moe_norm_f32(const moe_norm_shape* shape, const float* x, const float
  *               once; dh_in [T, H], what reaches h on the residual stream, or NULL (zero)
  *   dw, db [H]  overwritten, rounded once from fp32 sums over the rows (zeros with T == 0);
  *               NULL: not wanted
- * dx may be dy or dh_in itself, and shares no bytes with h (MOE_E_UNSUPPORTED otherwise, as
- * for a dy or dh_in that begins elsewhere in dx, and for a dw or db that shares bytes with w,
- * dx or the other one).
- * ws [ws_bytes >= moe_norm_workspace_bytes(shape)], read only with dw or db. */
+ * ws [ws_bytes >= moe_norm_workspace_bytes(shape)], used only with dw or db.
+ * dx may be dy or dh_in itself.  Outputs and ws share no other bytes with an input or with
+ * each other (MOE_E_UNSUPPORTED), whatever the number of rows. */
 moe_status moe_norm_backward_bf16(const moe_norm_shape* shape, const void* h, const void* w,
                                   const float* stats, const void* dy, const void* dh_in, void* dx,
                                   void* dw, void* db, void* ws, size_t ws_bytes,

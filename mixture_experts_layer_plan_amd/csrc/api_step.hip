@@ -68,13 +68,16 @@ moe_status norm_backward_impl(bool f32, const moe_norm_shape* s, const void* h, 
   if (s->T > 0 && (any_null({h, stats, dy, dx}) || ((dw || db) && !ws))) return MOE_E_NULL;
   if (!all_aligned({h, w, stats, dy, dh_in, dx, dw, db, ws})) return MOE_E_ALIGN;
   if ((dw || db) && ws_bytes < norm_ws_bytes(s)) return MOE_E_WORKSPACE;
-  const uint64_t n = (uint64_t)s->T * s->H * (f32 ? 4 : 2);
-  const uint64_t row = (uint64_t)s->H * (f32 ? 4 : 2);
-  if (overlap(dx, n, h, n) || overlap_base(dx, dy, n) || overlap_base(dx, dh_in, n) ||
-      overlap(dw, row, db, row))
+  const uint64_t row = (uint64_t)s->H * (f32 ? 4 : 2), n = s->T * row;
+  const Span out = {dx, n}, read = {stats, (uint64_t)s->T * 8};
+  if (overlap_base(dx, dy, n) || overlap_base(dx, dh_in, n) || overlap(dw, row, db, row) ||
+      overlaps_any(out, {{h, n}, {w, row}, read}))
     return MOE_E_UNSUPPORTED;
-  for (const void* d : {dw, db})  // written while rows are still read and written
-    if (overlap(d, row, w, row) || overlap(d, row, dx, n)) return MOE_E_UNSUPPORTED;
+  // dw, db and the sums in ws are written while rows are still read and written
+  const Span sums = {dw || db ? ws : nullptr, norm_ws_bytes(s)};
+  for (const Span& d : {Span{dw, row}, Span{db, row}, sums})
+    if (overlaps_any(d, {{h, n}, {w, row}, read, {dy, n}, {dh_in, n}, out})) return MOE_E_UNSUPPORTED;
+  if (overlaps_any(sums, {{dw, row}, {db, row}})) return MOE_E_UNSUPPORTED;
   NormBackArgs a;
   a.h = h;
   a.w = w;

@@ -304,3 +304,23 @@ def test_norm_outputs_over_the_other_inputs(L):
                 assert fwd(L, s, name, **dict(far, res=FAR, h=Z, stats=p)) == UNSUP
     # no rows, no bytes
     assert fwd(L, B.norm_shape(0, H), y=F + 16, stats=F + 16) == OK
+
+
+def test_norm_gradients_over_the_other_inputs(L):
+    """The same for few rows, whose column sums run beside them, and for many."""
+    H = 512
+    buf = dict(h=X, w=0x5000000, stats=0x6000000, dy=Y, dh=FAR, dx=Z, dw=0x7000000, db=0x7800000, ws=0xB0000000)
+    for T in (16, 256, 2000):
+        s = B.norm_shape(T, H)
+        for f, e in (("bf16", 2), ("f32", 4)):
+            name, row, n, wn = "moe_norm_backward_" + f, H * e, T * H * e, B.moe_norm_workspace_bytes(s)
+            size = dict(h=n, w=row, stats=T * 8, dy=n, dh=n, dx=n, dw=row, db=row, ws=wn)
+            pairs = [("dx", k) for k in ("h", "w", "stats")]
+            pairs += [(d, k) for d in ("dw", "db") for k in ("h", "w", "stats", "dy", "dh", "dx")]
+            pairs += [("dw", "db"), ("db", "dw")] + [("ws", k) for k in size if k != "ws"]
+            for out, k in pairs:
+                for p in partly(buf[k], size[k], size[out]):
+                    assert bwd(L, s, name, **dict(buf, **{out: p})) == UNSUP, (T, f, out, k, p - buf[k])
+    # without dw and db ws is not looked at (no rows: nothing is launched)
+    s = B.norm_shape(0, H)
+    assert bwd(L, s, **dict(buf, ws=X, dw=None, db=None)) == OK
