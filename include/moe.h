@@ -613,7 +613,8 @@ typedef struct {
  *   counts    int32 [n_seq, E]  out: c_ie
  *   scales    fp32 [n_seq]      out: coef E / (k N_i^2 n), 0 for sequences without tokens;
  *             the backward reads them
- *   ws [ws_bytes >= moe_balance_workspace_bytes(shape, balance)] */
+ *   ws [ws_bytes >= moe_balance_workspace_bytes(shape, balance)]
+ * Outputs and ws share no bytes with an input or with each other (MOE_E_UNSUPPORTED). */
 moe_status moe_balance_loss(const moe_shape* shape, const moe_balance* balance,
                             const float* logits, const int32_t* topk_idx,
                             const int32_t* seq_start, float* loss, int32_t* counts, float* scales,

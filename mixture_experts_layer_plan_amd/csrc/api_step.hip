@@ -293,6 +293,15 @@ moe_status moe_balance_loss(const moe_shape* s, const moe_balance* b, const floa
   if (!all_aligned({logits, topk_idx, seq_start, loss, counts, scales, ws})) return MOE_E_ALIGN;
   const BalanceWs W = balance_ws(s, b);
   if (ws_bytes < W.total) return MOE_E_WORKSPACE;
+  // all of them are written while others of the call are still read
+  const uint64_t T = s->T, n = b->n_seq;
+  const Span in[3] = {{logits, T * s->E * 4}, {topk_idx, T * s->k * 4}, {seq_start, (n + 1) * 4}};
+  const Span out[4] = {{loss, 4}, {counts, n * s->E * 4}, {scales, n * 4}, {ws, W.total}};
+  for (int i = 0; i < 4; ++i) {
+    if (overlaps_any(out[i], {in[0], in[1], in[2]})) return MOE_E_UNSUPPORTED;
+    for (int j = 0; j < i; ++j)
+      if (overlaps_any(out[i], {out[j]})) return MOE_E_UNSUPPORTED;
+  }
   BalanceArgs a = balance_args(s, b, logits, topk_idx, seq_start);
   a.loss = loss;
   a.counts = counts;

@@ -282,9 +282,9 @@ def test_norm_eps_below_the_normal_numbers(L):
 
 
 def partly(at, size, own):
-    """Places of `own` bytes that share some with [at, at + size)"""
+    """Aligned places of `own` bytes that share some with [at, at + size)"""
     return [p for p in (at, at + 16, at - 16, at + size - 16, at - own + 16)
-            if p < at + size and at < p + own]
+            if p < at + size and at < p + own and p % 16 == 0]
 
 
 def test_norm_outputs_over_the_other_inputs(L):
@@ -324,3 +324,15 @@ def test_norm_gradients_over_the_other_inputs(L):
     # without dw and db ws is not looked at (no rows: nothing is launched)
     s = B.norm_shape(0, H)
     assert bwd(L, s, **dict(buf, ws=X, dw=None, db=None)) == OK
+
+
+def test_balance_buffers_that_share_bytes(L):
+    s, ba = shape(T=512, E=64, k=4), B.balance("sigmoid", 0.01, 5)
+    n = B.moe_balance_workspace_bytes(s, ba)
+    at = dict(logits=X, idx=Y, start=0x4000000, out=0x5000000, counts=0x6000000, scales=0x7000000, ws=0x8000000)
+    size = dict(logits=512 * 64 * 4, idx=512 * 4 * 4, start=24, out=4, counts=5 * 64 * 4, scales=20, ws=n)
+    for o in ("out", "counts", "scales", "ws"):
+        for k in size:
+            if k != o:
+                for p in partly(at[k], size[k], size[o]):
+                    assert loss(L, s, ba, n=n, **dict(at, **{o: p})) == UNSUP, (o, k, p - at[k])
