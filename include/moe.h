@@ -625,7 +625,7 @@ moe_status moe_balance_loss(const moe_shape* shape, const moe_balance* balance,
  *                     1 - sigmoid for sigmoid scores; rows of tokens without a part: d_in
  *   d_loss fp32 [1] or NULL (1); d_in fp32 [T, E] or NULL (zero).  d_logits may be d_in (the
  *   routing's gradient, joined in place) or logits itself; it shares no bytes with one that
- *   begins elsewhere (MOE_E_UNSUPPORTED). */
+ *   begins elsewhere, nor with another input (MOE_E_UNSUPPORTED). */
 moe_status moe_balance_loss_backward(const moe_shape* shape, const moe_balance* balance,
                                      const float* logits, const int32_t* topk_idx,
                                      const int32_t* seq_start, const int32_t* counts,

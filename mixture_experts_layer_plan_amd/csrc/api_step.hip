@@ -326,8 +326,12 @@ moe_status moe_balance_loss_backward(const moe_shape* s, const moe_balance* b, c
   if (b->n_seq > 1 && !seq_start) return MOE_E_NULL;
   if (!all_aligned({logits, topk_idx, seq_start, counts, scales, d_loss, d_in, d_logits}))
     return MOE_E_ALIGN;
-  const uint64_t n = (uint64_t)s->T * s->E * 4;
+  const uint64_t T = s->T, seqs = b->n_seq, n = T * s->E * 4;
   if (overlap_base(d_logits, logits, n) || overlap_base(d_logits, d_in, n)) return MOE_E_UNSUPPORTED;
+  // read by every workgroup, at any time
+  if (overlaps_any({d_logits, n}, {{topk_idx, T * s->k * 4}, {seq_start, (seqs + 1) * 4},
+                                   {counts, seqs * s->E * 4}, {scales, seqs * 4}, {d_loss, 4}}))
+    return MOE_E_UNSUPPORTED;
   BalanceArgs a = balance_args(s, b, logits, topk_idx, seq_start);
   a.counts = const_cast<int32_t*>(counts);
   a.scales = const_cast<float*>(scales);

@@ -336,3 +336,13 @@ def test_balance_buffers_that_share_bytes(L):
             if k != o:
                 for p in partly(at[k], size[k], size[o]):
                     assert loss(L, s, ba, n=n, **dict(at, **{o: p})) == UNSUP, (o, k, p - at[k])
+
+
+def test_balance_gradient_over_the_other_inputs(L):
+    s, ba = shape(T=512, E=64, k=4), B.balance("sigmoid", 0.01, 5)
+    at = dict(logits=X, idx=Y, start=0x4000000, counts=0x5000000, scales=0x6000000, d_loss=0x7000000)
+    size = dict(idx=512 * 4 * 4, start=24, counts=5 * 64 * 4, scales=20, d_loss=4)
+    for k in size:
+        for p in partly(at[k], size[k], 512 * 64 * 4):
+            assert back(L, s, ba, **dict(at, dL=p)) == UNSUP, (k, p - at[k])
+    assert back(L, shape(T=0), ba, **dict(at, dL=0x5000010)) == OK      # no rows, no bytes
