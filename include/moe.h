@@ -686,8 +686,8 @@ typedef struct {
 
 /* Writes the table that the steps read, from `tensors`, an array in HOST memory that is read
  * before the call returns; once for as long as the tensors stay where they are.  No output
- * may share bytes with another output or with an input other than its own, of any tensor
- * (MOE_E_UNSUPPORTED).  table [moe_adamw_table_bytes(shape)]. */
+ * may share bytes with another output or with an input other than its own, of any tensor, nor
+ * may the table (MOE_E_UNSUPPORTED).  table [moe_adamw_table_bytes(shape)]. */
 size_t moe_adamw_table_bytes(const moe_adamw_shape* shape);
 moe_status moe_adamw_table(const moe_adamw_shape* shape, const moe_adamw_tensor* tensors,
                            void* table, hipStream_t stream);
@@ -705,7 +705,9 @@ moe_status moe_adamw_hyper_of(double lr, double beta1, double beta2, double eps,
 
 /* The step.  Its scalars come from host memory (hyper, read before the call returns) or from
  * device memory (hyper_dev, read by the kernel: a captured graph replays with what lies there
- * then, and grad_scale may be the work of an earlier kernel); the other is NULL. */
+ * then, and grad_scale may be the work of an earlier kernel); the other is NULL.  hyper_dev
+ * shares no bytes with an output of the table's tensors.  `shape` is the one that the table was
+ * written with. */
 moe_status moe_adamw_step(const moe_adamw_shape* shape, const void* table,
                           const moe_adamw_hyper* hyper, const moe_adamw_hyper* hyper_dev,
                           hipStream_t stream);

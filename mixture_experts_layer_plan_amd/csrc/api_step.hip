@@ -198,15 +198,16 @@ int pairs_of(const moe_adamw_shape* s, const moe_adamw_tensor& t, Pair* p) {
 }
 
 // Outputs may be their own inputs; otherwise no output shares bytes with an input or
-// with another output, of whatever tensor.
-moe_status check_ranges(const moe_adamw_shape* s, const moe_adamw_tensor* t) {
-  const size_t most = (size_t)s->n_tensors * 13;
+// with another output, of whatever tensor, nor does the table, which every step reads.
+moe_status check_ranges(const moe_adamw_shape* s, const moe_adamw_tensor* t, const void* table) {
+  const size_t most = (size_t)s->n_tensors * 13 + 1;
   Range* r = new (std::nothrow) Range[most];
   if (!r) return MOE_E_WORKSPACE;
   size_t k = 0;
   const auto add = [&](const void* p, uint64_t bytes, bool out) {
     if (bytes) r[k++] = {(uintptr_t)p, (uintptr_t)p + bytes, out};
   };
+  add(table, adamw_table(s).total, true);
   for (int i = 0; i < s->n_tensors; ++i) {
     Pair p[6];
     const int np = pairs_of(s, t[i], p);
@@ -228,7 +229,7 @@ moe_status check_ranges(const moe_adamw_shape* s, const moe_adamw_tensor* t) {
   return clash ? MOE_E_UNSUPPORTED : MOE_OK;
 }
 
-moe_status check_tensors(const moe_adamw_shape* s, const moe_adamw_tensor* t) {
+moe_status check_tensors(const moe_adamw_shape* s, const moe_adamw_tensor* t, const void* table) {
   int64_t sum = 0;
   for (int i = 0; i < s->n_tensors; ++i) {
     if (t[i].n < 0 || t[i].n > s->elements) return MOE_E_SHAPE;
@@ -245,7 +246,7 @@ moe_status check_tensors(const moe_adamw_shape* s, const moe_adamw_tensor* t) {
       if (!aligned16(p[j].out) || !aligned16(p[j].in)) return MOE_E_ALIGN;
     }
   }
-  return sum == s->elements ? check_ranges(s, t) : MOE_E_SHAPE;
+  return sum == s->elements ? check_ranges(s, t, table) : MOE_E_SHAPE;
 }
 
 }  // namespace
@@ -351,7 +352,7 @@ moe_status moe_adamw_table(const moe_adamw_shape* s, const moe_adamw_tensor* ten
   if (rc != MOE_OK) return rc;
   if (any_null({tensors, table})) return MOE_E_NULL;
   if (!aligned16(table)) return MOE_E_ALIGN;
-  rc = check_tensors(s, tensors);
+  rc = check_tensors(s, tensors, table);
   if (rc != MOE_OK) return rc;
   const AdamwTable L = adamw_table(s);
   int32_t tiles = 0;

@@ -346,3 +346,19 @@ def test_balance_gradient_over_the_other_inputs(L):
         for p in partly(at[k], size[k], 512 * 64 * 4):
             assert back(L, s, ba, **dict(at, dL=p)) == UNSUP, (k, p - at[k])
     assert back(L, shape(T=0), ba, **dict(at, dL=0x5000010)) == OK      # no rows, no bytes
+
+
+def test_adamw_table_over_a_tensor(L):
+    """The steps read addresses from it: with a gradient in its place they would go anywhere."""
+    for master, bits in ((False, 32), (True, 8)):
+        s = ashape(300000, 2, master=master, bits=bits)
+        arr = tensors(s, [100000, 200000])
+        n = B.moe_adamw_table_bytes(s)
+        for i, count in ((0, 100000), (1, 200000)):
+            names = ["grad", "m", "v", "param_out", "m_out", "v_out"] + (["master"] if master else ["param"])
+            names += ["m_scale", "v_scale_out"] if bits == 8 else []
+            for k in names:
+                at = getattr(arr[i], k)
+                size = (count + 31) // 32 if "scale" in k else count     # or more
+                for p in partly(at, size, n):
+                    assert table(L, s, arr, p) == UNSUP, (k, p - at)
