@@ -362,3 +362,17 @@ def test_adamw_table_over_a_tensor(L):
                 size = (count + 31) // 32 if "scale" in k else count     # or more
                 for p in partly(at, size, n):
                     assert table(L, s, arr, p) == UNSUP, (k, p - at)
+
+
+def test_balance_reads_three_sizes_of_the_shape(L):
+    """T, E and k alone: the layer's other limits do not hold for it."""
+    ba = B.balance("softmax", 0.01, 3)
+    full = B.moe_balance_workspace_bytes(shape(), ba)
+    for kw in (dict(H=0), dict(H=100), dict(H=-8, I=-1), dict(flags=1 << 30, I_shared=5, T_minibatch=-2)):
+        s = shape(**kw)
+        assert B.moe_balance_workspace_bytes(s, ba) == full
+        assert loss(L, s, ba, n=full - 1) == WS and back(L, s, ba, dL=F) == UNSUP    # past the shape's check
+        assert back(L, shape(T=0, **kw), ba, logits=None, idx=None, dL=None) == OK
+    assert loss(L, shape(H=0, k=17), ba) == SHAPE
+    s = shape(T=1 << 26, E=64, k=32, H=0)       # T k = 2^31
+    assert loss(L, s, ba) == SHAPE
