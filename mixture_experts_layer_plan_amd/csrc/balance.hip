@@ -322,12 +322,14 @@ MOE_DEV void finish(const BalanceArgs& a, const int32_t* tokens, const float* pa
 // sets its limits: 128 tokens of 64 experts take 7.9 us (two launches 8.4), 64 of 256 7.4 (9.2),
 // and 128 of 256 would take 12.
 constexpr int SMALL_T = 128, SMALL_E = 256, SMALL_SEQ = 64, SMALL_COUNTS = 4096;
+constexpr int SMALL_SHARES = SMALL_T / 2 * SMALL_E;  // 64 KB; a row for each token, or for each wavefront
+static_assert(SMALL_T * 64 <= SMALL_SHARES && 16 * SMALL_E <= SMALL_SHARES, "what is_small lets in");
 bool is_small(const BalanceArgs& a) {
   return a.T <= (a.E <= 64 ? SMALL_T : SMALL_T / 2) && a.E <= SMALL_E && a.n_seq <= SMALL_SEQ && a.n_seq * a.E <= SMALL_COUNTS;
 }
 template <typename R, bool SIGMOID>
 __global__ __launch_bounds__(1024) void balance_small_kernel(BalanceArgs a) {
-  __shared__ float s_p[SMALL_T * SMALL_E];
+  __shared__ float s_p[SMALL_SHARES];
   __shared__ int32_t s_c[SMALL_COUNTS];
   __shared__ float s_part[SMALL_SEQ];
   __shared__ int32_t s_seq[SMALL_T], s_tokens[SMALL_SEQ], s_start[SMALL_SEQ + 1];

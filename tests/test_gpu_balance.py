@@ -334,3 +334,13 @@ def test_two_batches_at_once(B):
     torch.cuda.synchronize()
     for x in sets:
         assert digest(*x[4]) == x[6]
+
+
+@pytest.mark.parametrize("T,E,n", [(128, 64, 64), (64, 256, 16), (128, 60, 2), (64, 255, 16), (64, 256, 1), (128, 64, 1)])
+def test_the_largest_batches_of_one_launch(B, T, E, n):
+    """Every row of shares that one workgroup holds, and every count."""
+    say(f"balance of {T} x {E} in {n} sequences")
+    L, idx = inputs(T, E, 8, free=0.05)
+    start = np.linspace(0, T, n + 1).astype(np.int64)
+    for score in ("softmax", "sigmoid"):
+        verify(B, L, idx, score, 0.5, start)
