@@ -541,7 +541,8 @@ moe_status moe_lora_backward_bf16(const moe_lora_shape* shape, const void* plan,
  *   0 <= T; H a multiple of 8 in [8, 16384]; eps in [2^-126, 1]
  * Where a value of a row is not finite, its rows of y and dx are not valid (NaN among them),
  * nor are dw and db; other rows are.  A row whose sum of squares passes fp32's range (values
- * from about 2^57 on) has 1 / sqrt(variance + eps) = 0. */
+ * from about 2^57 on) has 1 / sqrt(variance + eps) = 0, so that its y is b; where the sum of
+ * its values passes it too (from about 2^114 on), its y with MOE_NORM_LAYER is NaN. */
 typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
 typedef struct {
   int32_t T, H;

@@ -111,8 +111,7 @@ MOE_DEV void update_state(float& m, float& v, float& g, const AdamwHyper& h) {
 
 // Eight elements of a thread: a tile's eight neighbours (states of 8 bits, whose blocks of 32
 // are then four lanes), or four of each of its halves, so that the lanes of a 16-byte access
-// of fp32 are neighbours (SPLIT; 5.2 million elements with fp32
-// states: 25.0 -> 23.4 us).
+// of fp32 are neighbours (SPLIT; 5.2 million elements with fp32 states: 25.0 -> 23.4 us).
 constexpr int HALF = ADAMW_TILE / 2;
 template <bool SPLIT>
 MOE_DEV constexpr int place(int j) {

@@ -299,3 +299,17 @@ def test_the_smallest_eps(B):
     i["dy"] *= 1e-20
     for kind in ("layer", "rms"):
         verify(i, run(B, i, "f32", kind, 2.0 ** -126), "f32", kind, 2.0 ** -126)
+
+
+def test_rows_whose_squares_pass_the_range(B):
+    """1 / sqrt(variance + eps) is 0 and y is b; with a mean that passes the range too, NaN."""
+    say("norm of rows past 2^64")
+    for dtype in ("bf16", "f32"):
+        i = inputs(5, 1024, dtype)
+        i["x"] *= torch.tensor([1.0, 1e21, 1e30, 1.0, 3e37])[:, None].to(DT[dtype])
+        i["x"][4] = i["x"][4].abs()
+        for kind in ("layer", "rms"):
+            o = run(B, i, dtype, kind)
+            assert torch.equal(o["y"][[1, 2]].cpu(), i["b"].expand(2, -1))
+            assert not o["stats"][[1, 2, 4], 1].any() and torch.isfinite(o["y"][[0, 3]]).all()
+            assert torch.isnan(o["y"][4]).all() if kind == "layer" else torch.equal(o["y"][4].cpu(), i["b"])
