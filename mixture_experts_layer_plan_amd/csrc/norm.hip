@@ -593,7 +593,9 @@ hipError_t with_waves(int H, F f) {
 
 // Whether the sums of dw and db are taken by workgroups of their own beside the rows', which
 // read h and dy again but need no second launch: up to 1 KB of a column (256 x 7168: bf16 14.5
-// -> 6.8 us, fp32 18.3 -> 9.2; 512 x 4096: 11.5 -> 8.0 and, left as it is, 12.0 -> 14.3).
+// -> 6.8 us, fp32 18.3 -> 9.2; 512 x 4096: 11.5 -> 8.0 and, left as it is, 12.0 -> 14.3).  A dx
+// over dy takes two launches all the same, the columns first (kernels alone, 256 x 7168 bf16:
+// 13.2 us against 8.0), so that its sums are those of a dx elsewhere.
 bool norm_columns_beside(const NormBackArgs& p, int esize) {
   return (p.dw || p.db) && p.T > 0 && (int64_t)p.T * esize <= 1024;
 }
