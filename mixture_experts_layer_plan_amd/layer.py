@@ -22,9 +22,10 @@ Options of ``LayerBuffers`` beside the layer's shape:
   norm         (kind, eps): the layer's input is the norm of ``x``, joined with ``residual``
                [T, H] if the inputs hold one, with the weight ``norm_w`` [H] and the bias
                ``norm_b`` [H] if they hold them.  The layer then reads ``xn``; ``h`` is the joined
-               row (written only with a residual).  dx is the gradient of x and of residual alike and includes ``dh`` [T, H],
-               what reaches h on the residual stream, if the inputs hold it (rounded to the
-               element type before, as dx of the layer, and after); ``d_norm_w``, ``d_norm_b``
+               row (written only with a residual).  dx is the gradient of x and of residual alike
+               and includes ``dh`` [T, H], what reaches h on the residual stream, if the inputs
+               hold it (rounded to the element type before, as dx of the layer, and after);
+               ``d_norm_w``, ``d_norm_b``
   balance      a ``binding.balance``: ``loss`` [1] and ``counts`` int32 [n_seq, E] of the routing,
                by sequences ``seq_start`` int32 [n_seq + 1] if the inputs hold them, and its
                gradient, times ``d_loss`` fp32 [1] if they hold one, in d_logits
